@@ -360,6 +360,169 @@ int qk_gemv_chain_noalloc(const void *plan, const void *plan_dev, void *status, 
  */
 int qk_repack(int type, const void *W, void *Wp, int64_t N, int64_t K, void *stream);
 
+/*
+ * The attention side of a decode token: what runs between the projections'
+ * GEMVs.  qk_gemv leaves q, k and v (fp32, [N][ncols]); the calls below norm
+ * and rotate them, keep keys and values in a paged cache of 4-bit groups --
+ * one more quantised stream that every token reads -- and attend over it;
+ * the output projection's qk_gemv_ex reads the result as its x.
+ *
+ * qk_heads: rows of heads in memory, element (t, h, i) of row t, head h,
+ * dimension i at p[t*row + h*head + i*elem] (strides in elements, >= 0).
+ * y of a GEMV with N = heads*D rows and ncols columns, a row of q per column:
+ * {y, 1, D*ncols, ncols, 0}.  Elements of an output must not coincide: sorted
+ * by stride, each stride covers the extent of the smaller ones
+ * (QK_EINVAL_SHAPE).
+ */
+typedef struct qk_heads {
+    void *p;
+    int64_t row, head, elem;
+    int f16;              /* 1: fp16 values (2-byte aligned), 0: fp32 (4-byte aligned) */
+} qk_heads;
+
+/* Norm and rotation of one call; every pointer is a device pointer or NULL. */
+typedef struct qk_rope {
+    const float *q_norm;      /* D weights of the query heads' RMS norm, or NULL (no norm)    */
+    const float *k_norm;      /* the same for the key heads                                   */
+    const float *inv_freq;    /* rot_dim / 2 frequencies in radians per position; may be NULL
+                                 when rot_dim is 0                                            */
+    const int32_t *positions; /* rows positions, or NULL: each row's place in the cache
+                                 (qk_norm_rope: required when rot_dim > 0)                    */
+    float eps;                /* >= 0, under the norms' root                                  */
+    int rot_dim;              /* even, 0..D: the first rot_dim dimensions are rotated         */
+    int interleaved;          /* pair j is (2j, 2j+1); 0: (j, j + rot_dim/2)                  */
+} qk_rope;
+
+/*
+ * qk_norm_rope -- norm and rotation of query and key heads in one pass:
+ *
+ *   n_i = x_i / sqrt(mean_i(x_i^2) + eps) * w_i       (n = x without weights)
+ *   (u, v) of pair j -> (u cos a - v sin a, u sin a + v cos a),
+ *   a = position * inv_freq[j];  dimensions >= rot_dim keep n
+ *
+ * in fp64 (positions far from 0 keep their angle), rounded once to the output
+ * type (fp16: beyond the range +-inf).
+ *
+ *   head_dim    D: 64, 128 or 256
+ *   q, q_out    rows x n_heads x D, or both NULL (n_heads is then ignored)
+ *   k, k_out    rows x n_kv_heads x D, or both NULL
+ * An output may be its own input (the same view and type); any other overlap
+ * of an output with anything the call reads or writes is QK_EINVAL_PTR,
+ * judged by the address ranges that the views span.
+ * rows 0 does nothing.
+ */
+int qk_norm_rope(const qk_rope *rope, int rows, int head_dim, int n_heads, const qk_heads *q, const qk_heads *q_out,
+                 int n_kv_heads, const qk_heads *k, const qk_heads *k_out, void *stream);
+
+/*
+ * One layer's cache: a pool of num_pages pages, each page_size positions of
+ * every KV head.  A row of D values is held as D/32 groups of 32 consecutive
+ * dimensions, 5 bits a value: a 4-bit code each, an fp16 step d and an fp16
+ * minimum m per group, value = d * code + m.  Of an fp32 row (NaN taken as 0,
+ * values beyond +-65504 as +-65504, so a cache never holds a non-finite
+ * value), in fp32: m = fp16(min), d = fp16((max - m) / 15),
+ * code = rint((x - m) / d) kept in 0..15 (0 where d <= 0), so each value is
+ * within d/2 + 2^-11 |m| + 2^-11 (max - m) + 2^-21 of x.
+ *
+ * Page layout (bytes; S = page_size, G = D/32; little-endian): for each KV
+ * head the keys' block, then the values', each S*D*5/8 bytes:
+ *   keys    codes uint32 [S][4][G]: nibble n of word (a, g) = dimension 32g + 8a + n
+ *           d fp16 [S/4][G][4],  m fp16 [S][G]
+ *   values  codes: D >= 128 uint32 [S/4][D/128][16][4]: nibble n of word
+ *           (., w, l, .) = dimension 128w + 16n + l;  D = 64 uint16 [S/4][16][4]:
+ *           nibble n of piece l = dimension 16n + l
+ *           d, m fp16 [S/4][G][4]
+ * (a trailing [4]: the position's place in its block of 4).  The order is the
+ * one the matrix instructions of qk_kv_attn take their operands in, so that
+ * it loads whole 16-byte pieces and never transposes.
+ */
+typedef struct qk_kv_cache {
+    void *pool;           /* num_pages * qk_kv_page_bytes(...) bytes, 16-byte aligned; need
+                             not be cleared                                           */
+    int64_t num_pages;    /* 1 .. 2^31 - 1                                            */
+    int n_kv_heads;       /* 1 .. 4096                                                */
+    int head_dim;         /* D: 64, 128 or 256                                        */
+    int page_size;        /* a power of two, 32 .. 1024                               */
+} qk_kv_cache;
+
+/* Bytes of one page, or -1 for sizes the cache does not take. */
+int64_t qk_kv_page_bytes(int head_dim, int n_kv_heads, int page_size);
+
+/*
+ * The rows of one call and the sequences they continue.  Sequence s owns rows
+ * q_start[s] .. q_start[s+1] - 1 (n of them); the i-th stands at position
+ * kv_len[s] - n + i of its sequence, so kv_len counts these rows too.
+ * Position p lies on page pages[s * max_pages + p / page_size].
+ *
+ * What the arrays hold is read on the device and bounded there: rows outside
+ * every sequence are left as they were; a page number outside
+ * 0..num_pages-1 is a page not held, whose positions are neither stored nor
+ * attended to; so are positions below 0 and at max_pages * page_size or above.
+ * q_start must not decrease (rows of a q_start that does are undefined, but
+ * in bounds).  Sequences may share pages that no row of the call is
+ * appended to.
+ */
+typedef struct qk_kv_seqs {
+    int rows;              /* 0 .. 2^22                                                */
+    int nseq;              /* 1 .. 65536                                               */
+    int max_pages;         /* 1 .., max_pages * page_size <= 2^30                      */
+    const int32_t *q_start; /* device, nseq + 1 values, or NULL: rows / nseq each
+                               (rows must then be a multiple of nseq)                  */
+    const int32_t *kv_len; /* device, nseq values                                      */
+    const int32_t *pages;  /* device, nseq * max_pages values                          */
+} qk_kv_seqs;
+
+/*
+ * qk_kv_append -- keys and values of new rows into the cache, the keys normed
+ * and rotated on the way, and the rows' queries made ready in the same launch.
+ *
+ *   rope   as for qk_norm_rope, or NULL (no norm, no rotation)
+ *   k, v   rows x n_kv_heads x D
+ *   q, q_out, n_heads   as for qk_norm_rope, or both NULL
+ * Keys are rotated in fp64 and rounded to fp32 before they are grouped.
+ * Two rows of one call must not stand at the same place of the same page.
+ */
+int qk_kv_append(const qk_kv_cache *cache, const qk_kv_seqs *seqs, const qk_rope *rope, const qk_heads *k,
+                 const qk_heads *v, int n_heads, const qk_heads *q, const qk_heads *q_out, void *stream);
+
+/*
+ * qk_kv_read -- the values that the cache holds at the rows' positions, as
+ * qk_kv_attn takes them: fp32(d * code + m), rounded once (bit-exact), or
+ * that value as fp16.  The check path of the cache, as qk_dequant is of the
+ * weights; all of a sequence with n = kv_len.  A position that is not held
+ * reads as 0.  k_out or v_out may be NULL.
+ */
+int qk_kv_read(const qk_kv_cache *cache, const qk_kv_seqs *seqs, const qk_heads *k_out, const qk_heads *v_out,
+               void *stream);
+
+/*
+ * qk_kv_attn -- attention of the rows over their sequences' caches:
+ *
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . K[j][h'])  V[j][h'],
+ *   h' = h / (n_heads / n_kv_heads),
+ *
+ * over the positions j <= p (row t's own, p) that are held and, with
+ * window > 0, have j > p - window.  A row that sees no position gives zeros.
+ *
+ *   n_heads    query heads, a multiple of n_kv_heads, at most 4096
+ *   q          rows x n_heads x D, fp16 (QK_EINVAL_TYPE otherwise)
+ *   out        rows x n_heads x D, fp16 or fp32; the x of the next GEMV is
+ *              {x, 1, D*ncols, ncols, 1}
+ *   scale      finite
+ *   workspace  qk_kv_attn_workspace_bytes bytes (16-byte aligned; NULL when
+ *              that is 0), for this call until it has run: calls that may
+ *              overlap, captured ones among them, need workspaces of their own
+ * Scores, softmax statistics and sums are fp32, products of codes and queries
+ * exact; a probability times a step enters the matrix instructions as a sum
+ * of two fp16 values (2^-20 of it).  Non-finite queries give non-finite rows
+ * and touch no other row.  Accuracy, for exact p_j and, of values and keys,
+ * a_ji = d * code + |m|: within (2^-15 + 2^-17 * max_j |scale| sum_i |q_i|
+ * a_ji) * sum_j p_j a'_ji, plus the rounding of the output type.
+ */
+int64_t qk_kv_attn_workspace_bytes(const qk_kv_cache *cache, const qk_kv_seqs *seqs, int n_heads);
+int qk_kv_attn(const qk_kv_cache *cache, const qk_kv_seqs *seqs, int n_heads, const qk_heads *q, const qk_heads *out,
+               float scale, int window, void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Bytes per 256-weight superblock: 144 / 176 / 210, or -1 for a bad type. */
 int qk_block_bytes(int type);
 

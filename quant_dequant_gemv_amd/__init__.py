@@ -16,6 +16,7 @@ Q4_K, Q5_K, Q6_K = 12, 13, 14
 _BINDING_NAMES = {
     "qk_gemv", "qk_dequant", "qk_block_bytes", "qk_row_bytes", "qk_strerror", "qk_version",
     "gemv", "dequant", "load_library", "QKError", "LIB_PATH",
+    "Rope", "KVCache", "norm_rope", "kv_append", "kv_read", "kv_attn",
 }
 
 

@@ -24,7 +24,9 @@ Y_F16 = 0x1  # QK_Y_F16: epilogue flag, y stored as fp16
 EXPORTS = ("qk_gemv", "qk_gemv_ex", "qk_gemv_swiglu", "qk_gemv_batch", "qk_dequant", "qk_repack",
            "qk_block_bytes", "qk_row_bytes", "qk_strerror", "qk_version",
            "qk_chain_plan_bytes", "qk_chain_plan", "qk_chain_workspace_bytes", "qk_gemv_chain",
-           "qk_gemv_chain_noalloc")
+           "qk_gemv_chain_noalloc",
+           "qk_norm_rope", "qk_kv_page_bytes", "qk_kv_append", "qk_kv_read", "qk_kv_attn_workspace_bytes",
+           "qk_kv_attn")
 CHAIN_TIMEOUT = 0x1  # QK_CHAIN_TIMEOUT: bit of the chain workspace's first word
 CHAIN_NOALLOC_MAX_STEPS = 4094  # QK_CHAIN_NOALLOC_MAX_STEPS
 
@@ -40,6 +42,31 @@ class qk_chain_entry(ctypes.Structure):
     _fields_ = [("type", ctypes.c_int), ("flags", ctypes.c_int), ("W", ctypes.c_void_p), ("W2", ctypes.c_void_p),
                 ("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("residual", ctypes.c_void_p),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class qk_heads(ctypes.Structure):
+    """struct qk_heads of include/qkgemv.h."""
+    _fields_ = [("p", ctypes.c_void_p), ("row", ctypes.c_int64), ("head", ctypes.c_int64), ("elem", ctypes.c_int64),
+                ("f16", ctypes.c_int)]
+
+
+class qk_rope(ctypes.Structure):
+    """struct qk_rope of include/qkgemv.h."""
+    _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("eps", ctypes.c_float), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
+class qk_kv_cache(ctypes.Structure):
+    """struct qk_kv_cache of include/qkgemv.h."""
+    _fields_ = [("pool", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int)]
+
+
+class qk_kv_seqs(ctypes.Structure):
+    """struct qk_kv_seqs of include/qkgemv.h."""
+    _fields_ = [("rows", ctypes.c_int), ("nseq", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p)]
 
 
 class QKError(RuntimeError):
@@ -91,6 +118,20 @@ def load_library(path: str = LIB_PATH):
     lib.qk_gemv_chain.restype = c_int
     lib.qk_gemv_chain_noalloc.argtypes = [P, P, P, i64, P]
     lib.qk_gemv_chain_noalloc.restype = c_int
+    H, R = ctypes.POINTER(qk_heads), ctypes.POINTER(qk_rope)
+    C, S = ctypes.POINTER(qk_kv_cache), ctypes.POINTER(qk_kv_seqs)
+    lib.qk_norm_rope.argtypes = [R, c_int, c_int, c_int, H, H, c_int, H, H, P]
+    lib.qk_norm_rope.restype = c_int
+    lib.qk_kv_page_bytes.argtypes = [c_int, c_int, c_int]
+    lib.qk_kv_page_bytes.restype = i64
+    lib.qk_kv_append.argtypes = [C, S, R, H, H, c_int, H, H, P]
+    lib.qk_kv_append.restype = c_int
+    lib.qk_kv_read.argtypes = [C, S, H, H, P]
+    lib.qk_kv_read.restype = c_int
+    lib.qk_kv_attn_workspace_bytes.argtypes = [C, S, c_int]
+    lib.qk_kv_attn_workspace_bytes.restype = i64
+    lib.qk_kv_attn.argtypes = [C, S, c_int, H, H, ctypes.c_float, c_int, P, i64, P]
+    lib.qk_kv_attn.restype = c_int
     _lib = lib
     return lib
 
@@ -170,6 +211,34 @@ def qk_strerror(code: int) -> str:
 
 def qk_version() -> str:
     return load_library().qk_version().decode()
+
+
+def qk_norm_rope(rope, rows: int, head_dim: int, n_heads: int, q, q_out, n_kv_heads: int, k, k_out,
+                 stream: int = 0) -> int:
+    """rope: a qk_rope; q, q_out, k, k_out: qk_heads or None."""
+    return load_library().qk_norm_rope(rope, rows, head_dim, n_heads, q, q_out, n_kv_heads, k, k_out, stream)
+
+
+def qk_kv_page_bytes(head_dim: int, n_kv_heads: int, page_size: int) -> int:
+    return load_library().qk_kv_page_bytes(head_dim, n_kv_heads, page_size)
+
+
+def qk_kv_append(cache, seqs, rope, k, v, n_heads: int, q, q_out, stream: int = 0) -> int:
+    """cache: qk_kv_cache; seqs: qk_kv_seqs; rope: qk_rope or None; k, v, q, q_out: qk_heads (q, q_out or None)."""
+    return load_library().qk_kv_append(cache, seqs, rope, k, v, n_heads, q, q_out, stream)
+
+
+def qk_kv_read(cache, seqs, k_out, v_out, stream: int = 0) -> int:
+    return load_library().qk_kv_read(cache, seqs, k_out, v_out, stream)
+
+
+def qk_kv_attn_workspace_bytes(cache, seqs, n_heads: int) -> int:
+    return load_library().qk_kv_attn_workspace_bytes(cache, seqs, n_heads)
+
+
+def qk_kv_attn(cache, seqs, n_heads: int, q, out, scale: float, window: int, workspace, workspace_bytes: int,
+               stream: int = 0) -> int:
+    return load_library().qk_kv_attn(cache, seqs, n_heads, q, out, scale, window, workspace, workspace_bytes, stream)
 
 
 # ---------------------------------------------------------------- torch helpers
@@ -410,3 +479,249 @@ class Chain:
     def status(self) -> int:
         """The workspace's flag word (synchronises): 0, or CHAIN_TIMEOUT."""
         return int(self.workspace[0].item())
+
+
+# ------------------------------------------------- the attention side (torch)
+# Heads are tensors [rows, heads, D] of any strides >= 0, float16 or float32:
+# y of a GEMV is y.view(heads, D, ncols).permute(2, 0, 1).  Work runs, and
+# what a helper allocates is allocated, on the tensors' device and on
+# ``stream`` (None: that device's current stream).
+
+def _heads_arg(t, name, rows=None, heads=None, D=None, dtypes=None):
+    """The qk_heads of a tensor [rows, heads, D], checked against the sizes given."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    dt = t.dtype
+    if dt is not torch.float16 and dt is not torch.float32 or dtypes and dt not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes or (torch.float16, torch.float32)))}, got {dt}")
+    shape = t.shape
+    if len(shape) != 3 or (rows is not None and shape[0] != rows) or (heads is not None and shape[1] != heads) or \
+            (D is not None and shape[2] != D):
+        raise ValueError(f"{name} must have shape [{'rows' if rows is None else rows}, "
+                         f"{'heads' if heads is None else heads}, {'D' if D is None else D}], got {tuple(shape)}")
+    return qk_heads(t.data_ptr(), *t.stride(), 1 if dt is torch.float16 else 0)
+
+
+def _int32_arg(t, name, shape):
+    """The address of a contiguous int32 tensor of this shape (None entries: any size)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _seqs_arg(rows, pages, kv_len, q_start):
+    nseq = kv_len.shape[0] if getattr(kv_len, "shape", None) else None
+    return qk_kv_seqs(rows, nseq or 0, pages.shape[1] if getattr(pages, "ndim", 0) == 2 else 0,
+                      None if q_start is None else _int32_arg(q_start, "q_start", (None if nseq is None else nseq + 1,)),
+                      _int32_arg(kv_len, "kv_len", (None,)), _int32_arg(pages, "pages", (nseq, None)))
+
+
+def _one_device(named):
+    """The CUDA device that all of the named tensors (None: absent) are on."""
+    dev = None
+    for name, t in named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA (HIP) device tensor, is on {t.device}")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"all tensors must be on one device, got {dev} and {name} on {t.device}")
+    return dev
+
+
+def _elsewhere(dev, stream):
+    """None where ``dev`` and ``stream`` are the current ones, else a context in which they are."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+    both = contextlib.ExitStack()
+    both.enter_context(torch.cuda.device(dev))
+    both.enter_context(torch.cuda.stream(stream))
+    return both
+
+
+class Rope:
+    """Norm and rotation of query and key heads (qk_rope): inv_freq float32
+    [rot_dim / 2] (None: no rotation), q_norm / k_norm float32 [D] (None: no
+    norm)."""
+
+    def __init__(self, inv_freq=None, interleaved: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6):
+        import torch
+        self.named = (("inv_freq", inv_freq), ("q_norm", q_norm), ("k_norm", k_norm))
+        for name, t in self.named:
+            if t is not None:
+                _need(t, name, torch.float32)
+                if t.dim() != 1:
+                    raise ValueError(f"{name} must have one dimension, has {t.dim()}")
+        self.D = {t.numel() for t in (q_norm, k_norm) if t is not None}
+        p = [None if t is None else t.data_ptr() for t in (q_norm, k_norm, inv_freq)]
+        self._c = qk_rope(*p, None, eps, 0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved))
+
+    def arg(self, D, positions, rows):
+        if self.D - {D}:
+            raise ValueError(f"q_norm and k_norm must have {D} elements, have {sorted(self.D)}")
+        if positions is None:
+            return self._c
+        c = qk_rope()
+        ctypes.pointer(c)[0] = self._c
+        c.positions = _int32_arg(positions, "positions", (rows,))
+        return c
+
+
+class KVCache:
+    """One layer's paged 4-bit cache (qk_kv_cache): num_pages pages of
+    page_size positions.  pool: uint8 device tensor of num_pages *
+    qk_kv_page_bytes(...) bytes (None: allocated here)."""
+
+    def __init__(self, num_pages: int, n_kv_heads: int, head_dim: int, page_size: int = 64, device="cuda", pool=None):
+        import torch
+        pb = qk_kv_page_bytes(head_dim, n_kv_heads, page_size)
+        if pb < 0 or not 1 <= num_pages < 1 << 31:
+            raise QKError(QK_EINVAL_SHAPE, "KVCache")
+        if pool is None:
+            pool = torch.empty((num_pages, pb), dtype=torch.uint8, device=device)
+        _need(pool, "pool", torch.uint8, numel=num_pages * pb)
+        self.pool, self.page_bytes = pool, pb
+        self.num_pages, self.n_kv_heads, self.head_dim, self.page_size = num_pages, n_kv_heads, head_dim, page_size
+        self._c = qk_kv_cache(pool.data_ptr(), num_pages, n_kv_heads, head_dim, page_size)
+
+
+def norm_rope(rope: Rope, positions, q, k=None, q_out=None, k_out=None, stream=None):
+    """Norm and rotation of q [rows, heads, D] and k [rows, kv heads, D]
+    (either may be None) at ``positions`` (int32 [rows]); returns (q_out,
+    k_out), float16 contiguous unless given (they may be q and k)."""
+    import torch
+    x = q if q is not None else k
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("q or k must be a tensor [rows, heads, D]")
+    rows, _, D = x.shape
+    a = [None if t is None else _heads_arg(t, n, rows, None, D) for n, t in (("q", q), ("k", k))]
+    r = rope.arg(D, positions, rows)
+    dev = _one_device((("q", q), ("k", k), ("positions", positions), ("q_out", q_out), ("k_out", k_out), *rope.named))
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return norm_rope(rope, positions, q, k, q_out, k_out)
+    outs = []
+    for n, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
+        if t is None:
+            if o is not None:
+                raise ValueError(f"{n} without its input")
+            outs.append((None, None))
+            continue
+        if o is None:
+            o = torch.empty(t.shape, dtype=torch.float16, device=dev)
+        outs.append((o, _heads_arg(o, n, *t.shape)))
+    rc = qk_norm_rope(r, rows, D, 0 if q is None else q.shape[1], a[0], outs[0][1], 0 if k is None else k.shape[1],
+                      a[1], outs[1][1], torch.cuda.current_stream(dev).cuda_stream)
+    if rc != QK_OK:
+        raise QKError(rc, "qk_norm_rope")
+    return outs[0][0], outs[1][0]
+
+
+def kv_append(cache: KVCache, k, v, pages, kv_len, q_start=None, q=None, rope: Rope | None = None, positions=None,
+              q_out=None, stream=None):
+    """Keys and values [rows, kv heads, D] of new rows into the cache (see
+    qk_kv_seqs: pages int32 [nseq, max_pages], kv_len int32 [nseq], q_start
+    int32 [nseq + 1] or None), keys -- and the queries q [rows, heads, D] --
+    normed and rotated by ``rope``; returns q_out (float16 unless given; None
+    without q)."""
+    import torch
+    D = cache.head_dim
+    ka = _heads_arg(k, "k", None, cache.n_kv_heads, D)
+    rows = k.shape[0]
+    va = _heads_arg(v, "v", rows, cache.n_kv_heads, D)
+    qa = None if q is None else _heads_arg(q, "q", rows, None, D)
+    seqs = _seqs_arg(rows, pages, kv_len, q_start)
+    if rope is None and positions is not None:
+        raise ValueError("positions without a rope")
+    r = None if rope is None else rope.arg(D, positions, rows)
+    dev = _one_device((("k", k), ("v", v), ("pages", pages), ("kv_len", kv_len), ("q_start", q_start), ("q", q),
+                       ("q_out", q_out), ("pool", cache.pool), ("positions", positions),
+                       *(() if rope is None else rope.named)))
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return kv_append(cache, k, v, pages, kv_len, q_start, q, rope, positions, q_out)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        oa = None
+    else:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.float16, device=dev)
+        oa = _heads_arg(q_out, "q_out", *q.shape)
+    rc = qk_kv_append(cache._c, seqs, r, ka, va, 0 if q is None else q.shape[1], qa, oa,
+                      torch.cuda.current_stream(dev).cuda_stream)
+    if rc != QK_OK:
+        raise QKError(rc, "qk_kv_append")
+    return q_out
+
+
+def kv_read(cache: KVCache, rows: int, pages, kv_len, q_start=None, k_out=None, v_out=None, stream=None):
+    """What the cache holds at the rows' positions: (k, v), float32
+    [rows, kv heads, D] unless given."""
+    import torch
+    seqs = _seqs_arg(rows, pages, kv_len, q_start)
+    shape = (rows, cache.n_kv_heads, cache.head_dim)
+    dev = _one_device((("pages", pages), ("kv_len", kv_len), ("q_start", q_start), ("pool", cache.pool),
+                       ("k_out", k_out), ("v_out", v_out)))
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return kv_read(cache, rows, pages, kv_len, q_start, k_out, v_out)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.float32, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.float32, device=dev)
+    rc = qk_kv_read(cache._c, seqs, _heads_arg(k_out, "k_out", *shape), _heads_arg(v_out, "v_out", *shape),
+                    torch.cuda.current_stream(dev).cuda_stream)
+    if rc != QK_OK:
+        raise QKError(rc, "qk_kv_read")
+    return k_out, v_out
+
+
+def kv_attn(cache: KVCache, q, pages, kv_len, q_start=None, scale: float | None = None, window: int = 0, out=None,
+            workspace=None, stream=None):
+    """Attention of q (float16 [rows, heads, D]) over the rows' sequences;
+    scale None: D ** -0.5; window 0: none.  Returns out, float16 contiguous
+    unless given.  workspace: uint8 device tensor of at least
+    qk_kv_attn_workspace_bytes bytes (None: allocated for the call)."""
+    import torch
+    D = cache.head_dim
+    qa = _heads_arg(q, "q", None, None, D, (torch.float16,))
+    rows, heads = q.shape[0], q.shape[1]
+    seqs = _seqs_arg(rows, pages, kv_len, q_start)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
+    dev = _one_device((("q", q), ("pages", pages), ("kv_len", kv_len), ("q_start", q_start), ("out", out),
+                       ("pool", cache.pool), ("workspace", workspace)))
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return kv_attn(cache, q, pages, kv_len, q_start, scale, window, out, workspace)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float16, device=dev)
+    oa = _heads_arg(out, "out", rows, heads, D)
+    if workspace is None:
+        need = qk_kv_attn_workspace_bytes(cache._c, seqs, heads)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    rc = qk_kv_attn(cache._c, seqs, heads, qa, oa, D ** -0.5 if scale is None else scale, window,
+                    None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+                    torch.cuda.current_stream(dev).cuda_stream)
+    if rc != QK_OK:
+        raise QKError(rc, "qk_kv_attn")
+    return out

@@ -104,4 +104,40 @@ hipError_t launch_dequant(int type, const void *W, void *out, int64_t N, int64_t
 // GGUF rows -> PLANAR rows (type without the flag).
 hipError_t launch_repack(int type, const void *W, void *Wp, int64_t N, int64_t K, hipStream_t stream);
 
+// ---- the attention side (qk_kv.hip): views and arrays as in the C ABI
+struct Heads {
+    void *p;
+    int64_t row, head, elem;
+    int f16;
+};
+struct KvCache {
+    uint8_t *pool;
+    int64_t num_pages;
+    int hkv, D, ps_log2;
+};
+struct KvSeqs {
+    int rows, nseq, max_pages;
+    const int32_t *q_start, *kv_len, *pages;
+};
+struct RowPrep {  // norm + rotation of qk_norm_rope / qk_kv_append
+    const float *q_norm, *k_norm, *inv_freq;
+    const int32_t *positions;
+    float eps;
+    int rot_dim, interleaved;
+};
+// Bytes of one head's keys (or values) on a page, and of a page.
+constexpr int64_t kv_block_bytes(int D, int ps) { return (int64_t)ps * D / 8 * 5; }
+constexpr int64_t kv_page_bytes(int D, int hkv, int ps) { return 2 * hkv * kv_block_bytes(D, ps); }
+
+// q and k heads through norm and rotation; with a cache, k and v into it
+// (k_out then unused), without one k to k_out.
+hipError_t launch_kv_rows(const KvCache *cache, const KvSeqs &seqs, const RowPrep &prep, int D, int hq, const Heads &q,
+                          const Heads &q_out, int hkv, const Heads &k, const Heads &v, const Heads &k_out,
+                          hipStream_t stream);
+hipError_t launch_kv_read(const KvCache &cache, const KvSeqs &seqs, const Heads &k_out, const Heads &v_out,
+                          hipStream_t stream);
+int64_t kv_attn_workspace(const KvCache &cache, const KvSeqs &seqs, int hq);
+hipError_t launch_kv_attn(const KvCache &cache, const KvSeqs &seqs, int hq, const Heads &q, const Heads &out,
+                          float scale, int window, void *workspace, hipStream_t stream);
+
 }  // namespace qk
