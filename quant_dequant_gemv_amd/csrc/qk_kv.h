@@ -26,6 +26,8 @@ template <int D> struct KvLayout {
     __device__ static int v_piece(int p, int w, int l) { return ((((p >> 2) * VW + w) * 16 + l) * 4 + (p & 3)) * VB; }
 };
 
+__device__ __forceinline__ int clamp_row(const KvSeqs &q, int v) { return min(max(v, 0), q.rows); }
+
 // Sequence of row t (nseq where it belongs to none) and its first row and row
 // count; one wave, every lane gets the same answer.  The starts are compared
 // 64 at a time: the number of starts at or before t is the sequence's place.
@@ -42,7 +44,7 @@ __device__ __forceinline__ RowSeq row_seq(const KvSeqs &q, int t, int lane) {
     }
     const int s = cnt - 1;
     if (s < 0 || s >= q.nseq) return {q.nseq, 0, 0};
-    const int first = q.q_start[s], end = q.q_start[s + 1];
+    const int first = clamp_row(q, q.q_start[s]), end = clamp_row(q, q.q_start[s + 1]);
     if (t < first || t >= end) return {q.nseq, 0, 0};  // only for starts that decrease
     return {s, first, end - first};
 }
