@@ -36,7 +36,6 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
-constexpr int AW = 4;            // waves of a workgroup
 constexpr int MAX_SPLIT = 256;   // splits of a sequence
 constexpr float M_NONE = -3e38f; // running maximum before any visible position
 constexpr float GROW = 2.f;      // a probability may reach 2^GROW before the maximum is moved
@@ -50,7 +49,11 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
     const h2 v = {(_Float16)a, (_Float16)b};
     return __builtin_bit_cast(uint32_t, v);
 }
-// N dwords (N even) from an address aligned to min(4N, 16)
+// the value of the lane 8 columns on, in a row of 16 lanes
+__device__ __forceinline__ float row_half_swap(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 0xf, 0xf, true));
+}
+// N dwords from an address aligned to min(4N, 16)
 template <int N> __device__ __forceinline__ void load(uint32_t *r, const uint8_t *p) {
     if constexpr (N == 1) {
         r[0] = *reinterpret_cast<const uint32_t *>(p);
@@ -83,6 +86,7 @@ struct AttnArgs {
     Heads q, out;
     int hq, grp, window, nsplit, ntiles, per_split;
     float scale;
+    int qvec;            // query rows are whole 16-byte pieces
     float *o;            // partial outputs [unit][RT][D], unit = (tile * hkv + head) * nsplit + split
     float2 *ml;          // running maximum and sum [unit][RT]
 };
@@ -93,7 +97,7 @@ template <int RT> __device__ __forceinline__ int tile_base(const AttnArgs &a, in
 
 // Visible range and splits of a tile whose s, j, first, n are set.
 template <int RT> __device__ __forceinline__ void tile_range(const AttnArgs &a, Tile &t) {
-    const int64_t len = a.sq.kv_len[t.s];
+    const int64_t len = __builtin_amdgcn_readfirstlane(a.sq.kv_len[t.s]);
     t.p0 = len - t.n;
     const int r0 = t.j * RT, r1 = min(r0 + RT, t.n * a.grp) - 1;
     const int64_t pmin = t.p0 + r0 / a.grp, pmax = t.p0 + r1 / a.grp;
@@ -125,6 +129,10 @@ template <int RT> __device__ __forceinline__ bool find_tile(const AttnArgs &a, i
         t.first = clamp_row(a.sq, a.sq.q_start[t.s]);
         t.n = clamp_row(a.sq, a.sq.q_start[t.s + 1]) - t.first;
         t.j = b - tile_base<RT>(a, t.first, t.s);
+        t.s = __builtin_amdgcn_readfirstlane(t.s);
+        t.first = __builtin_amdgcn_readfirstlane(t.first);
+        t.n = __builtin_amdgcn_readfirstlane(t.n);
+        t.j = __builtin_amdgcn_readfirstlane(t.j);
         if (t.n <= 0 || t.j < 0 || (int64_t)t.j * RT >= (int64_t)t.n * a.grp) return false;
     }
     tile_range<RT>(a, t);
@@ -136,70 +144,181 @@ __device__ __forceinline__ void store_out(const Heads &o, int64_t i, float v) {
     else reinterpret_cast<float *>(o.p)[i] = v;
 }
 
-// One workgroup: a tile of 16 MT query rows, one KV head, one split of the
+// Variants.  PAIR: tiles of 8 query rows, each twice among the 16 columns --
+// columns 0..7 for the lower half of the groups, 8..15 for the upper -- so a
+// lane keeps the steps of half of the groups and one fma scales two.  One
+// score instruction then takes 16 dimensions of group p and 16 of group
+// p + G/2 (the other half's query operand is 0), two make both sums, and the
+// halves are added once per tile.  Otherwise tiles of 16 MT rows.
+template <int MT, bool PAIR> struct Form {
+    static constexpr int RT = PAIR ? 8 : 16 * MT;
+    static constexpr int AW = PAIR ? 8 : 4;  // waves of a workgroup
+};
+
+// One workgroup: a tile of query rows, one KV head, one split of the
 // positions; its waves take tiles of 32 positions in turn and join at the end.
-template <int D, int MT>
-__global__ void __launch_bounds__(64 * AW, MT == 1 ? 2 : 1) kv_attn_kernel(AttnArgs a) {
+template <int D, int MT, bool PAIR>
+__global__ void __launch_bounds__(PAIR ? 512 : 256, MT == 1 ? 2 : 1) kv_attn_kernel(AttnArgs a) {
     using L = KvLayout<D>;
-    constexpr int G = L::G, RT = 16 * MT, NT = D / 16, OP = D + 4;
+    constexpr int G = L::G, RT = Form<MT, PAIR>::RT, AW = Form<MT, PAIR>::AW, NT = D / 16, OP = D + 4;
+    constexpr int RC = PAIR ? 8 : 16;     // rows side by side in a wave's columns
+    constexpr int GL = PAIR ? G / 2 : G;  // groups whose steps a lane keeps
     constexpr int VD = D >= 128 ? 4 : 2;  // dwords of a lane's four value pieces
-    __shared__ float4 red4[AW * 16 * OP / 4];
+    constexpr bool AHEAD = PAIR || D < 256;  // the next tile's loads under this tile's work (registers permitting)
+    __shared__ float4 red4[AW * RC * OP / 4];
     __shared__ float2 st[AW][RT];
     float *red = reinterpret_cast<float *>(red4);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, quad = lane >> 4;
+    const int hc = PAIR ? col >> 3 : 0;   // half of the groups, by column
     const int hk = blockIdx.x % a.c.hkv, bs = blockIdx.x / a.c.hkv;
     const int split = bs % a.nsplit, tile = bs / a.nsplit;
     Tile t;
     if (!find_tile<RT>(a, tile, lane, t) || split >= t.ns) return;
     const int R = t.n * a.grp;
+    const int64_t cap = (int64_t)a.sq.max_pages << a.c.ps_log2;
+
+    const int64_t nt = t.t1 - t.t0;
+    const int x0 = __builtin_amdgcn_readfirstlane((int)(t.t0 + nt * split / t.ns));
+    const int x1 = __builtin_amdgcn_readfirstlane((int)(t.t0 + nt * (split + 1) / t.ns));
+    const int32_t *table = a.sq.pages + (int64_t)t.s * a.sq.max_pages;
+    const int tsh = a.c.ps_log2 - 5;
+    const int64_t pstride = 2 * a.c.hkv * L::block(a.c.ps_log2);
+    const uint8_t *pool = a.c.pool + (int64_t)hk * 2 * L::block(a.c.ps_log2);
+    // Pages of the wave's next 64 tiles, one a lane: a page number is then a
+    // register, not a load that the tile's loads would wait behind.  A page
+    // that is not held is -1.
+    int ahead = 0;
+    auto look_ahead = [&](int x) {
+        const int64_t at = min((int64_t)x + AW * lane, (int64_t)x1 - 1);
+        const int page = table[at >> tsh];
+        ahead = page >= 0 && page < a.c.num_pages ? page : -1;
+    };
+
+    uint32_t kc[2][G], kd[2][2 * GL], km[2][G / 2], vc[2][L::VW][VD], vd[2][2 * GL], vm[2][2];
+    // a lane's offsets inside a tile; the tile's own place is uniform
+    const uint32_t at_kc = col * L::ROW + (PAIR ? (quad & 1) * 4 * G + (quad >> 1) * 2 * G : quad * 4 * G);
+    const uint32_t at_d = quad * 8 * G + hc * 4 * G, at_km = col * 2 * G;
+    const uint32_t at_vc = (quad * L::VW * 16 + col) * 4 * VD, at_vm = (quad * G + min(col, G - 1)) * 8;
+    const int d_off = L::d_off(a.c.ps_log2), m_off = L::m_off(a.c.ps_log2);
+    auto load_k = [&](int page, int x) {
+        const int p0 = (x & ((1 << tsh) - 1)) << 5;  // of the page
+        const uint8_t *kb = pool + page * pstride, *c = kb + p0 * L::ROW, *d = kb + d_off + p0 * 2 * G,
+                      *m = kb + m_off + p0 * 2 * G;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if constexpr (PAIR) {
+                load<G / 2>(kc[u], c + at_kc + u * 16 * L::ROW);
+                load<G / 2>(kc[u] + G / 2, c + at_kc + u * 16 * L::ROW + 8 * G);
+            } else {
+                load<G>(kc[u], c + at_kc + u * 16 * L::ROW);
+            }
+            load<2 * GL>(kd[u], d + at_d + u * 32 * G);
+            load<G / 2>(km[u], m + at_km + u * 32 * G);
+        }
+    };
+    auto load_v = [&](int page, int x) {
+        const int p0 = (x & ((1 << tsh) - 1)) << 5;
+        const uint8_t *vb = pool + page * pstride + L::block(a.c.ps_log2);
+        const uint8_t *c = vb + p0 * L::ROW, *d = vb + d_off + p0 * 2 * G, *m = vb + m_off + p0 * 2 * G;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int w = 0; w < L::VW; ++w) load<VD>(vc[u][w], c + at_vc + (u * 4 * L::VW + w) * 64 * VD);
+            load<2 * GL>(vd[u], d + at_d + u * 32 * G);
+            load<2>(vm[u], m + at_vm + u * 32 * G);
+        }
+    };
+    int x = x0 + wave, page = -1;
+    if (x < x1) look_ahead(x);
 
     // query rows as the second operand, scaled by a power of two per row so
     // that neither they nor their sixteenths are subnormal
     u4 qf[MT][G], qs[MT];
     float sc1[MT], sc2[MT];
     int lim[MT], low[MT];
-    const int64_t cap = (int64_t)a.sq.max_pages << a.c.ps_log2;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        const int r = t.j * RT + mt * 16 + col, rr = min(r, R - 1), tok = rr / a.grp;
+        const int r = t.j * RT + mt * 16 + (col & (RC - 1)), rr = min(r, R - 1), tok = rr / a.grp;
         const int64_t pos = t.p0 + tok;
         lim[mt] = (int)max((int64_t)-1, min(pos, cap - 1));
         low[mt] = a.window ? (int)min(max((int64_t)0, pos - a.window + 1), (int64_t)INT32_MAX) : 0;
         const _Float16 *src = reinterpret_cast<const _Float16 *>(a.q.p) + (int64_t)(t.first + tok) * a.q.row +
                               (int64_t)(hk * a.grp + rr % a.grp) * a.q.head;
+        // operand i of a lane: 8 dimensions from `dim(i)` on, or zeros
+        const bool mine = !PAIR || (quad >> 1) == hc;
+        auto dim = [&](int i) {
+            return PAIR ? 32 * ((i >> 1) + hc * (G / 2)) + 16 * (i & 1) + 8 * (quad & 1) : 32 * i + 8 * quad;
+        };
         float v[G][8], mx = 0.f;
 #pragma unroll
-        for (int g = 0; g < G; ++g)
+        for (int i = 0; i < G; ++i) {
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                v[g][n] = (float)src[(int64_t)(32 * g + 8 * quad + n) * a.q.elem];
-                mx = fmaxf(mx, fabsf(v[g][n]));
+            for (int n = 0; n < 8; ++n) v[i][n] = 0.f;
+            if (mine) {
+                if (a.qvec) {
+                    const h8 w = *reinterpret_cast<const h8 *>(src + dim(i));
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) v[i][n] = (float)w[n];
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) v[i][n] = (float)src[(int64_t)(dim(i) + n) * a.q.elem];
+                }
             }
+        }
+        if (mt == 0 && x < x1) {  // the first tile's loads, before the queries are waited for
+            page = __builtin_amdgcn_readlane(ahead, 0);
+            if (AHEAD) {
+                load_k(max(page, 0), x);
+                load_v(max(page, 0), x);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+            for (int n = 0; n < 8; ++n) mx = fmaxf(mx, fabsf(v[i][n]));
+        if (PAIR) mx = fmaxf(mx, __shfl_xor(mx, 8));
         mx = fmaxf(mx, __shfl_xor(mx, 16));
         mx = fmaxf(mx, __shfl_xor(mx, 32));
         // mx * 2^e in [2^9, 2^10); infinite, NaN or zero rows as they are
-        const int e = mx > 0.f && mx < 1e30f ? 10 - (int)((__float_as_uint(mx) >> 23) - 126) : 0;
+        const int e = mx > 0.f && mx < 1e30f ? 136 - (int)(__float_as_uint(mx) >> 23) : 0;
         const float f = __uint_as_float((uint32_t)(127 + e) << 23), inv = __uint_as_float((uint32_t)(127 - e) << 23);
         sc2[mt] = a.scale * 1.44269504088896340736f * inv;
         sc1[mt] = sc2[mt] * 16777216.f;
         uint32_t sums[4] = {0, 0, 0, 0};
+        float half = 0.f;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
+        for (int i = 0; i < G; ++i) {
             float s = 0.f;
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-                v[g][n] *= f;
-                s += v[g][n];
+                v[i][n] *= f;
+                s += v[i][n];
             }
-            s += __shfl_xor(s, 16);
-            s += __shfl_xor(s, 32);
             // nibbles 0 and 4, 1 and 5, 2 and 6, 3 and 7: the odd ones' codes come 16 times too large
-            qf[mt][g] = u4{pack(v[g][0], v[g][4]), pack(v[g][1] * 0.0625f, v[g][5] * 0.0625f), pack(v[g][2], v[g][6]),
-                           pack(v[g][3] * 0.0625f, v[g][7] * 0.0625f)};
-            const _Float16 hi = (_Float16)s;
-            const _Float16 w = quad == 0 ? hi : quad == 1 ? (_Float16)(s - (float)hi) : (_Float16)0.f;
-            sums[g >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, w) << (16 * (g & 1));
+            qf[mt][i] = u4{pack(v[i][0], v[i][4]), pack(v[i][1] * 0.0625f, v[i][5] * 0.0625f), pack(v[i][2], v[i][6]),
+                           pack(v[i][3] * 0.0625f, v[i][7] * 0.0625f)};
+            // the group's sum as two fp16 terms, in two quads
+            if (PAIR && (i & 1) == 0) {
+                half = s;
+                continue;
+            }
+            if (PAIR) s += half;
+            s += __shfl_xor(s, 16);
+            if (!PAIR) s += __shfl_xor(s, 32);
+            const _Float16 hi = (_Float16)s, lo = (_Float16)(s - (float)hi);
+            const int term = PAIR ? quad & 1 : quad;
+            const _Float16 w = mine && term == 0 ? hi : mine && term == 1 ? lo : (_Float16)0.f;
+            const uint32_t bits = __builtin_bit_cast(uint16_t, w);
+            if constexpr (PAIR) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int g = (i >> 1) + h * (G / 2);
+                    sums[g >> 1] |= (hc == h ? bits : 0u) << (16 * (g & 1));
+                }
+            } else {
+                sums[i >> 1] |= bits << (16 * (i & 1));
+            }
         }
         qs[mt] = u4{sums[0], sums[1], sums[2], sums[3]};
     }
@@ -219,73 +338,47 @@ __global__ void __launch_bounds__(64 * AW, MT == 1 ? 2 : 1) kv_attn_kernel(AttnA
         l[mt] = 0.f;
     }
 
-    const int64_t nt = t.t1 - t.t0;
-    const int64_t x0 = t.t0 + nt * split / t.ns, x1 = t.t0 + nt * (split + 1) / t.ns;
-    const int32_t *table = a.sq.pages + (int64_t)t.s * a.sq.max_pages;
-    const int tsh = a.c.ps_log2 - 5;
-    const int64_t pstride = 2 * a.c.hkv * L::block(a.c.ps_log2);
-    const uint8_t *pool = a.c.pool + (int64_t)hk * 2 * L::block(a.c.ps_log2);
-    auto page_of = [&](int64_t x) { return x < x1 ? table[x >> tsh] : -1; };
-
-    for (int64_t x = x0 + wave; x < x1; x += AW) {
-        const int page = page_of(x);
-        if (page < 0 || page >= a.c.num_pages) continue;
-        const uint8_t *kb = pool + page * pstride, *vb = kb + L::block(a.c.ps_log2);
-        const int p0 = (int)(x & ((1 << tsh) - 1)) << 5;  // of the page
-        uint32_t kc[2][G], kd[2][2 * G], km[2][G / 2], vc[2][L::VW][VD], vd[2][2 * G], vm[2][2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int pc = p0 + 16 * u + col, pq = (p0 >> 2) + 4 * u + quad;
-            load<G>(kc[u], kb + pc * L::ROW + quad * 4 * G);
-            load<2 * G>(kd[u], kb + L::d_off(a.c.ps_log2) + pq * 8 * G);
-            load<G / 2>(km[u], kb + L::m_off(a.c.ps_log2) + pc * 2 * G);
+    // Keys of the next tile are asked for when this tile's are used up, and
+    // values when this tile's are: each comes in under the other half's work.
+    // A page that is not held is read as page 0 and counts for nothing; behind
+    // the last tile the same tile is asked for again.
+    for (int k = 1; x < x1; ++k, x += AW) {
+        const bool live = page >= 0;
+        int nx = x, np = page;
+        if (x + AW < x1) {
+            nx = x + AW;
+            if ((k & 63) == 0) look_ahead(nx);
+            np = __builtin_amdgcn_readlane(ahead, k & 63);
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int pq = (p0 >> 2) + 4 * u + quad;
-#pragma unroll
-            for (int w = 0; w < L::VW; ++w) load<VD>(vc[u][w], vb + ((pq * L::VW + w) * 16 + col) * 4 * VD);
-            load<2 * G>(vd[u], vb + L::d_off(a.c.ps_log2) + pq * 8 * G);
-            load<2>(vm[u], vb + L::m_off(a.c.ps_log2) + (pq * G + min(col, G - 1)) * 8);
-        }
-        // places that hold nothing yet: whatever their bytes say, the step and the minimum are 0
-        if (x * 32 + 32 > held) {
-            const int left = (int)(held - x * 32);
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int p = 16 * u + 4 * quad + 2 * k;
-                    const uint32_t mask = (p < left ? 0xffffu : 0u) | (p + 1 < left ? 0xffff0000u : 0u);
-#pragma unroll
-                    for (int g = 0; g < G; ++g) vd[u][2 * g + k] &= mask;
-                    vm[u][k] &= mask;
-                }
+        if (!AHEAD) {
+            load_k(max(page, 0), x);
+            load_v(max(page, 0), x);
         }
 
         // scores
         float z[MT][2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            f4 s[MT];
+            f4 s[MT], acc[MT];
             u4 mo = {0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < G / 2; ++i) mo[i] = km[u][i];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                s[mt] = mfma(mo, qs[mt], f4{0.f, 0.f, 0.f, 0.f});
-                s[mt] *= sc2[mt];
-            }
-            f4 acc[MT];
+            for (int mt = 0; mt < MT; ++mt) s[mt] = mfma(mo, qs[mt], f4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const uint32_t w = kc[u][g], w8 = w >> 8;
-                const u4 ko = {w & 0x000f000fu, w & 0x00f000f0u, w8 & 0x000f000fu, w8 & 0x00f000f0u};
+            for (int g = 0; g < GL; ++g) {
+                u4 ko[2];
+#pragma unroll
+                for (int i = 0; i < (PAIR ? 2 : 1); ++i) {
+                    const uint32_t w = kc[u][g + i * (G / 2)], w8 = w >> 8;
+                    ko[i] = u4{w & 0x000f000fu, w & 0x00f000f0u, w8 & 0x000f000fu, w8 & 0x00f000f0u};
+                }
                 const float d0 = lo_f(kd[u][2 * g]), d1 = hi_f(kd[u][2 * g]), d2 = lo_f(kd[u][2 * g + 1]),
                             d3 = hi_f(kd[u][2 * g + 1]);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const f4 r = mfma(ko, qf[mt][g], f4{0.f, 0.f, 0.f, 0.f});
+                    f4 r = mfma(ko[0], qf[mt][PAIR ? 2 * g : g], f4{0.f, 0.f, 0.f, 0.f});
+                    if constexpr (PAIR) r = mfma(ko[1], qf[mt][2 * g + 1], r);
                     if (g == 0) acc[mt] = f4{d0 * r.x, d1 * r.y, d2 * r.z, d3 * r.w};
                     else
                         acc[mt] = f4{fmaf(d0, r.x, acc[mt].x), fmaf(d1, r.y, acc[mt].y), fmaf(d2, r.z, acc[mt].z),
@@ -295,10 +388,19 @@ __global__ void __launch_bounds__(64 * AW, MT == 1 ? 2 : 1) kv_attn_kernel(AttnA
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z[mt][u][i] = fmaf(acc[mt][i], sc1[mt], s[mt][i]);
+                for (int i = 0; i < 4; ++i) {
+                    float y = fmaf(acc[mt][i], sc1[mt], s[mt][i] * sc2[mt]);
+                    if constexpr (PAIR) y += row_half_swap(y);
+                    z[mt][u][i] = y;
+                }
         }
-        if (x * 32 < all_lo || x * 32 + 31 > all_hi) {
-            const int base = (int)(x * 32) + 4 * quad;
+        if (AHEAD) {
+            __builtin_amdgcn_sched_barrier(0);
+            load_k(max(np, 0), nx);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (!live || x * 32 < all_lo || x * 32 + 31 > all_hi) {
+            const int base = x * 32 + 4 * quad;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -306,7 +408,7 @@ __global__ void __launch_bounds__(64 * AW, MT == 1 ? 2 : 1) kv_attn_kernel(AttnA
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int p = base + 16 * u + i;
-                        z[mt][u][i] = p <= lim[mt] && p >= low[mt] ? z[mt][u][i] : -INFINITY;
+                        z[mt][u][i] = live && p <= lim[mt] && p >= low[mt] ? z[mt][u][i] : -INFINITY;
                     }
         }
 
@@ -330,16 +432,30 @@ __global__ void __launch_bounds__(64 * AW, MT == 1 ? 2 : 1) kv_attn_kernel(AttnA
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float p0 = __builtin_amdgcn_exp2f(z[mt][u][2 * k] - m[mt]);
-                    const float p1 = __builtin_amdgcn_exp2f(z[mt][u][2 * k + 1] - m[mt]);
+                for (int k2 = 0; k2 < 2; ++k2) {
+                    const float p0 = __builtin_amdgcn_exp2f(z[mt][u][2 * k2] - m[mt]);
+                    const float p1 = __builtin_amdgcn_exp2f(z[mt][u][2 * k2 + 1] - m[mt]);
                     l[mt] += p0 + p1;
-                    ph[mt][u][k] = pack(p0, p1);
-                    pl[mt][u][k] = pack(p0 - lo_f(ph[mt][u][k]), p1 - hi_f(ph[mt][u][k]));
+                    ph[mt][u][k2] = pack(p0, p1);
+                    pl[mt][u][k2] = pack(p0 - lo_f(ph[mt][u][k2]), p1 - hi_f(ph[mt][u][k2]));
                 }
         }
 
-        // values
+        // values; of places that hold nothing yet, whatever their bytes say,
+        // the step and the minimum are 0
+        if (!live || x * 32 + 32 > held) {
+            const int left = live ? (int)(held - x * 32) : 0;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int k2 = 0; k2 < 2; ++k2) {
+                    const int p = 16 * u + 4 * quad + 2 * k2;
+                    const uint32_t mask = (p < left ? 0xffffu : 0u) | (p + 1 < left ? 0xffff0000u : 0u);
+#pragma unroll
+                    for (int g = 0; g < GL; ++g) vd[u][2 * g + k2] &= mask;
+                    vm[u][k2] &= mask;
+                }
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const u4 mo = {vm[0][0], vm[0][1], vm[1][0], vm[1][1]};
@@ -347,64 +463,78 @@ __global__ void __launch_bounds__(64 * AW, MT == 1 ? 2 : 1) kv_attn_kernel(AttnA
             om[mt] = mfma(mo, u4{pl[mt][0][0], pl[mt][0][1], pl[mt][1][0], pl[mt][1][1]}, om[mt]);
         }
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            u4 v0, v1;  // dimensions 32g .. 32g+15 and 32g+16 .. 32g+31 (those 16 times too large)
+        for (int gl = 0; gl < GL; ++gl) {
+            u4 hi[MT], lo[MT];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t w;
-                    if constexpr (D == 64) {
-                        w = vc[u][0][k] >> (8 * g);
-                    } else {
-                        const uint32_t sel = 0x0c040c00u + 0x00010001u * (uint32_t)(g & 3);
-                        w = __builtin_amdgcn_perm(vc[u][g >> 2][2 * k + 1], vc[u][g >> 2][2 * k], sel);
-                    }
-                    v0[2 * u + k] = w & 0x000f000fu;
-                    v1[2 * u + k] = w & 0x00f000f0u;
-                }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                u4 hi, lo;
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const h2 d = __builtin_bit_cast(h2, vd[u][2 * g + k]);
-                        const h2 p = __builtin_bit_cast(h2, ph[mt][u][k]), q = __builtin_bit_cast(h2, pl[mt][u][k]);
-                        const h2 x2 = p * d;
-                        const h2 r = __builtin_elementwise_fma(p, d, -x2);
-                        hi[2 * u + k] = __builtin_bit_cast(uint32_t, x2);
-                        lo[2 * u + k] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(q, d, r));
+                    for (int k2 = 0; k2 < 2; ++k2) {
+                        const h2 d = __builtin_bit_cast(h2, vd[u][2 * gl + k2]);
+                        const h2 p = __builtin_bit_cast(h2, ph[mt][u][k2]), q = __builtin_bit_cast(h2, pl[mt][u][k2]);
+                        const h2 y = p * d;
+                        const h2 r = __builtin_elementwise_fma(p, d, -y);
+                        hi[mt][2 * u + k2] = __builtin_bit_cast(uint32_t, y);
+                        lo[mt][2 * u + k2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(q, d, r));
                     }
-                o[mt][2 * g] = mfma(v0, hi, o[mt][2 * g]);
-                o[mt][2 * g + 1] = mfma(v1, hi, o[mt][2 * g + 1]);
-                o[mt][2 * g] = mfma(v0, lo, o[mt][2 * g]);
-                o[mt][2 * g + 1] = mfma(v1, lo, o[mt][2 * g + 1]);
+#pragma unroll
+            for (int h = 0; h < (PAIR ? 2 : 1); ++h) {
+                const int g = gl + h * (G / 2);
+                u4 v0, v1;  // dimensions 32g .. 32g+15 and 32g+16 .. 32g+31 (those 16 times too large)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int k2 = 0; k2 < 2; ++k2) {
+                        uint32_t w;
+                        if constexpr (D == 64) {
+                            w = vc[u][0][k2] >> (8 * g);
+                        } else {
+                            const uint32_t sel = 0x0c040c00u + 0x00010001u * (uint32_t)(g & 3);
+                            w = __builtin_amdgcn_perm(vc[u][g >> 2][2 * k2 + 1], vc[u][g >> 2][2 * k2], sel);
+                        }
+                        v0[2 * u + k2] = w & 0x000f000fu;
+                        v1[2 * u + k2] = w & 0x00f000f0u;
+                    }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    o[mt][2 * g] = mfma(v0, hi[mt], o[mt][2 * g]);
+                    o[mt][2 * g + 1] = mfma(v1, hi[mt], o[mt][2 * g + 1]);
+                    o[mt][2 * g] = mfma(v0, lo[mt], o[mt][2 * g]);
+                    o[mt][2 * g + 1] = mfma(v1, lo[mt], o[mt][2 * g + 1]);
+                }
             }
         }
+        if (AHEAD) {
+            __builtin_amdgcn_sched_barrier(0);
+            load_v(max(np, 0), nx);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        page = np;
     }
 
-    // join the waves: common maximum, then sums through LDS, 16 rows at a time
+    // join the waves: common maximum, then sums through LDS, RC rows at a time
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         l[mt] += __shfl_xor(l[mt], 16);
         l[mt] += __shfl_xor(l[mt], 32);
-        if (quad == 0) st[wave][mt * 16 + col] = make_float2(m[mt], l[mt]);
+        if (quad == 0 && hc == 0) st[wave][mt * 16 + col] = make_float2(m[mt], l[mt]);
     }
     __syncthreads();
     const int64_t unit = ((int64_t)tile * a.c.hkv + hk) * a.nsplit + split;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        float mx = st[0][mt * 16 + col].x;
+        const int row0 = col & (RC - 1);
+        float mx = st[0][mt * 16 + row0].x;
 #pragma unroll
-        for (int w = 1; w < AW; ++w) mx = fmaxf(mx, st[w][mt * 16 + col].x);
+        for (int w = 1; w < AW; ++w) mx = fmaxf(mx, st[w][mt * 16 + row0].x);
         const float f = __builtin_amdgcn_exp2f(m[mt] - mx);
-        float *mine = red + (wave * 16 + col) * OP;
+        float *mine = red + (wave * RC + row0) * OP;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             // the group's minima term: row g of om, held by quad g / 4
             const float mg = __shfl(om[mt][g & 3], (g >> 2) * 16 + col);
+            if (PAIR && hc != g / (G / 2)) continue;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const f4 v = o[mt][2 * g + k];
@@ -414,13 +544,13 @@ __global__ void __launch_bounds__(64 * AW, MT == 1 ? 2 : 1) kv_attn_kernel(AttnA
             }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < 16 * D / 4; i += 64 * AW) {
+        for (int i = threadIdx.x; i < RC * D / 4; i += 64 * AW) {
             const int row = i / (D / 4), c4 = i % (D / 4), r = t.j * RT + mt * 16 + row;
             if (r >= R) continue;
             float4 s = *reinterpret_cast<const float4 *>(red + row * OP + 4 * c4);
 #pragma unroll
             for (int w = 1; w < AW; ++w) {
-                const float4 v = *reinterpret_cast<const float4 *>(red + (w * 16 + row) * OP + 4 * c4);
+                const float4 v = *reinterpret_cast<const float4 *>(red + (w * RC + row) * OP + 4 * c4);
                 s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
             }
             float mm = st[0][mt * 16 + row].x, ll = 0.f;
@@ -500,18 +630,19 @@ __global__ void __launch_bounds__(256) kv_attn_join_kernel(AttnArgs a) {
 
 // Launch shape: from sizes alone (the lengths are on the device).
 struct Shape {
-    int mt, ntiles, nsplit, per_split;
+    int rt, ntiles, nsplit, per_split;
 };
 Shape attn_shape(const KvCache &c, const KvSeqs &sq, int hq) {
     const int grp = hq / c.hkv;
     Shape s;
-    s.mt = c.D < 256 && (int64_t)sq.rows * grp > (int64_t)16 * sq.nseq ? 2 : 1;
-    const int RT = 16 * s.mt;
-    const int64_t n = sq.rows / sq.nseq;
-    s.ntiles = (int)(sq.q_start ? (int64_t)sq.rows * grp / RT + sq.nseq : sq.nseq * ((n * grp + RT - 1) / RT));
+    const int64_t n = sq.rows / sq.nseq, per_seq = ((int64_t)sq.rows * grp + sq.nseq - 1) / sq.nseq;
+    s.rt = per_seq <= 8 ? 8 : per_seq <= 16 || c.D == 256 ? 16 : 32;
+    s.ntiles = (int)(sq.q_start ? (int64_t)sq.rows * grp / s.rt + sq.nseq : sq.nseq * ((n * grp + s.rt - 1) / s.rt));
     const int64_t most = ((int64_t)sq.max_pages << c.ps_log2) / 32;  // tiles of 32 positions
-    s.per_split = 2 * AW;
-    int64_t ns = 2 * device_cus() / ((int64_t)s.ntiles * c.hkv);
+    const int64_t base = (int64_t)s.ntiles * c.hkv, aw = s.rt == 8 ? 8 : 4;
+    const int64_t slots = s.rt == 8 ? device_cus() : 2 * device_cus();
+    s.per_split = (int)(2 * aw);
+    int64_t ns = slots / base;
     ns = std::min<int64_t>(ns, (most + s.per_split - 1) / s.per_split);
     s.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(ns, MAX_SPLIT));
     return s;
@@ -522,31 +653,39 @@ Shape attn_shape(const KvCache &c, const KvSeqs &sq, int hq) {
 int64_t kv_attn_workspace(const KvCache &c, const KvSeqs &sq, int hq) {
     const Shape s = attn_shape(c, sq, hq);
     if (s.nsplit == 1) return 0;
-    return (int64_t)s.ntiles * c.hkv * s.nsplit * 16 * s.mt * (4 * c.D + 8);
+    return (int64_t)s.ntiles * c.hkv * s.nsplit * s.rt * (4 * c.D + 8);
 }
 
 hipError_t launch_kv_attn(const KvCache &c, const KvSeqs &seqs, int hq, const Heads &q, const Heads &out, float scale,
                           int window, void *workspace, hipStream_t st) {
     const Shape s = attn_shape(c, seqs, hq);
-    AttnArgs a{c, seqs, q, out, hq, hq / c.hkv, window, s.nsplit, s.ntiles, s.per_split, scale, nullptr, nullptr};
+    AttnArgs a{c, seqs, q, out, hq, hq / c.hkv, window, s.nsplit, s.ntiles, s.per_split, scale, 0, nullptr, nullptr};
+    a.qvec = q.elem == 1 && q.row % 8 == 0 && q.head % 8 == 0 && ((uintptr_t)q.p & 15) == 0;
     if (s.nsplit > 1) {
         a.o = (float *)workspace;
-        a.ml = (float2 *)(a.o + (int64_t)s.ntiles * c.hkv * s.nsplit * 16 * s.mt * c.D);
+        a.ml = (float2 *)(a.o + (int64_t)s.ntiles * c.hkv * s.nsplit * s.rt * c.D);
     }
     const int64_t blocks = (int64_t)s.ntiles * c.hkv * s.nsplit;
     auto go = [&](auto kern, auto join) -> hipError_t {
-        hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * AW), 0, st, a);
+        hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(s.rt == 8 ? 512 : 256), 0, st, a);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || s.nsplit == 1) return e;
         hipLaunchKernelGGL(join, dim3((unsigned)(seqs.rows * hq)), dim3(256), 0, st, a);
         return hipGetLastError();
     };
 #define QK_ATTN(D)                                                                                    \
-    return s.mt == 1 ? go(kv_attn_kernel<D, 1>, kv_attn_join_kernel<D, 16>)                           \
-                     : go(kv_attn_kernel<D, 2>, kv_attn_join_kernel<D, 32>)
-    if (c.D == 64) QK_ATTN(64);
-    if (c.D == 128) QK_ATTN(128);
-    return go(kv_attn_kernel<256, 1>, kv_attn_join_kernel<256, 16>);
+    if (s.rt == 8) return go(kv_attn_kernel<D, 1, true>, kv_attn_join_kernel<D, 8>);                  \
+    if (s.rt == 16) return go(kv_attn_kernel<D, 1, false>, kv_attn_join_kernel<D, 16>)
+    if (c.D == 256) {
+        QK_ATTN(256);
+        return hipErrorInvalidValue;  // (no shape of 32 rows for D = 256)
+    }
+    if (c.D == 128) {
+        QK_ATTN(128);
+        return go(kv_attn_kernel<128, 2, false>, kv_attn_join_kernel<128, 32>);
+    }
+    QK_ATTN(64);
+    return go(kv_attn_kernel<64, 2, false>, kv_attn_join_kernel<64, 32>);
 #undef QK_ATTN
 }
 
