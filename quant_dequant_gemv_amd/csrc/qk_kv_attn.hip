@@ -69,74 +69,102 @@ template <int N> __device__ __forceinline__ void load(uint32_t *r, const uint8_t
     }
 }
 
-// Query rows of a sequence, its heads of one KV head side by side: row r is
-// token r / grp, head r % grp of the group.  Tiles of RT rows; a sequence's
-// tiles are numbered from first * grp / RT + s, so that every tile of every
-// sequence has a number of its own without a sum over the sequences.
-struct Tile {
-    int s, j;            // sequence, tile of it
-    int first, n;        // its rows in the call
-    int64_t p0;          // position of its first row
-    int64_t t0, t1;      // tiles of 32 positions that some row sees
-    int ns;              // splits that have work (at least 1)
-};
+// Work.  Query rows of a sequence, its heads of one KV head side by side: row
+// r is token r / grp, head r % grp of the group, in tiles of RT rows.  A
+// tile's positions are cut into splits of about `chunk` tiles of 32, where
+// chunk shares the whole call's work out over the compute units -- from the
+// lengths themselves (at most one split more a tile), so neither a page table made for longer contexts nor a
+// batch of unlike lengths leaves units idle.  A work item is one (tile,
+// split); a sequence's items follow those of the sequences before it.
 struct AttnArgs {
     KvCache c;
     KvSeqs sq;
     Heads q, out;
-    int hq, grp, window, nsplit, ntiles, per_split;
+    int hq, grp, window;
+    int target;          // items per KV head to share the work out to (0: no splits)
+    int min_chunk;       // tiles of 32 positions that a split has at least
+    int nitems;          // items per KV head at most
     float scale;
     int qvec;            // query rows are whole 16-byte pieces
-    float *o;            // partial outputs [unit][RT][D], unit = (tile * hkv + head) * nsplit + split
-    float2 *ml;          // running maximum and sum [unit][RT]
+    float *o;            // partial outputs [item * hkv + head][RT][D]
+    float2 *ml;          // running maximum and sum [item * hkv + head][RT]
+};
+struct Item {
+    int s, j, split, ns; // sequence, tile of it, split, splits of the sequence's tiles
+    int first, n, len;   // the sequence's rows in the call, and its length
+    int id0;             // item of the tile's first split
 };
 
-template <int RT> __device__ __forceinline__ int tile_base(const AttnArgs &a, int first, int s) {
-    return (int)((int64_t)first * a.grp / RT) + s;
-}
-
-// Visible range and splits of a tile whose s, j, first, n are set.
-template <int RT> __device__ __forceinline__ void tile_range(const AttnArgs &a, Tile &t) {
-    const int64_t len = __builtin_amdgcn_readfirstlane(a.sq.kv_len[t.s]);
-    t.p0 = len - t.n;
-    const int r0 = t.j * RT, r1 = min(r0 + RT, t.n * a.grp) - 1;
-    const int64_t pmin = t.p0 + r0 / a.grp, pmax = t.p0 + r1 / a.grp;
-    const int64_t end = min(pmax + 1, (int64_t)a.sq.max_pages << a.c.ps_log2);
-    const int64_t begin = a.window ? max((int64_t)0, pmin - a.window + 1) : 0;
-    t.t0 = begin >> 5;
-    t.t1 = end > begin ? (end + 31) >> 5 : t.t0;
-    const int64_t nt = t.t1 - t.t0;
-    t.ns = (int)max((int64_t)1, min((int64_t)a.nsplit, (nt + a.per_split - 1) / a.per_split));
-}
-
-// The tile of number b, or false if it is none.  One wave, uniform.
-template <int RT> __device__ __forceinline__ bool find_tile(const AttnArgs &a, int b, int lane, Tile &t) {
-    if (!a.sq.q_start) {
-        t.n = a.sq.rows / a.sq.nseq;
-        const int per = (t.n * a.grp + RT - 1) / RT;
-        t.s = b / per;
-        t.j = b % per;
-        t.first = t.s * t.n;
-    } else {
-        int cnt = 0;
-        for (int i0 = 0; i0 < a.sq.nseq; i0 += 64) {
-            const int i = min(i0 + lane, a.sq.nseq - 1);
-            const int base = tile_base<RT>(a, clamp_row(a.sq, a.sq.q_start[i]), i);
-            cnt += __popcll(__ballot(i0 + lane < a.sq.nseq && base <= b));
+// One wave, uniform results.  by_row: the tile `j` of sequence `want`;
+// otherwise the item number `want`.  false: there is none.
+template <int RT> __device__ __forceinline__ bool find_item(const AttnArgs &a, int want, bool by_row, int j, int lane,
+                                                            Item &it) {
+    struct Seq { int first, n, len, tiles, span; };
+    const int even = a.sq.q_start ? 0 : a.sq.rows / a.sq.nseq;
+    auto seq = [&](int s0) {
+        const int s = min(s0 + lane, a.sq.nseq - 1);
+        Seq v;
+        if (a.sq.q_start) {
+            v.first = clamp_row(a.sq, a.sq.q_start[s]);
+            v.n = max(clamp_row(a.sq, a.sq.q_start[s + 1]) - v.first, 0);
+        } else {
+            v.first = s * even;
+            v.n = even;
         }
-        if (!cnt) return false;
-        t.s = cnt - 1;
-        t.first = clamp_row(a.sq, a.sq.q_start[t.s]);
-        t.n = clamp_row(a.sq, a.sq.q_start[t.s + 1]) - t.first;
-        t.j = b - tile_base<RT>(a, t.first, t.s);
-        t.s = __builtin_amdgcn_readfirstlane(t.s);
-        t.first = __builtin_amdgcn_readfirstlane(t.first);
-        t.n = __builtin_amdgcn_readfirstlane(t.n);
-        t.j = __builtin_amdgcn_readfirstlane(t.j);
-        if (t.n <= 0 || t.j < 0 || (int64_t)t.j * RT >= (int64_t)t.n * a.grp) return false;
+        v.len = a.sq.kv_len[s];
+        v.tiles = s0 + lane < a.sq.nseq ? (int)(((int64_t)v.n * a.grp + RT - 1) / RT) : 0;
+        // tiles of 32 positions that the rows of its last tile see, about
+        const int64_t end = min((int64_t)v.len, (int64_t)a.sq.max_pages << a.c.ps_log2);
+        const int64_t seen = a.window ? min(end, (int64_t)a.window + min(v.n, RT / a.grp + 2)) : end;
+        v.span = (int)((max(seen, (int64_t)0) + 31) >> 5);
+        return v;
+    };
+    const Seq head = seq(0);  // (read once where one round has them all)
+    int64_t work = (int64_t)head.tiles * head.span;
+    for (int s0 = 64; s0 < a.sq.nseq; s0 += 64) {
+        const Seq v = seq(s0);
+        work += (int64_t)v.tiles * v.span;
     }
-    tile_range<RT>(a, t);
-    return true;
+    if (a.sq.nseq > 1)
+        for (int i = 1; i < 64; i <<= 1) work += __shfl_xor(work, i);
+    else
+        work = (int64_t)__builtin_amdgcn_readfirstlane(head.tiles) * __builtin_amdgcn_readfirstlane(head.span);
+    const int chunk = a.target ? (int)max((int64_t)a.min_chunk, (work + a.target - 1) / a.target) : INT32_MAX;
+    int before = 0;
+    for (int s0 = 0; s0 < a.sq.nseq; s0 += 64) {
+        const Seq v = s0 ? seq(s0) : head;
+        const int ns = min(MAX_SPLIT, max(1, v.span / chunk + (v.span % chunk ? 1 : 0)));
+        int sum = v.tiles * ns;
+        if (a.sq.nseq > 1)
+            for (int i = 1; i < 64; i <<= 1) {
+                const int up = __shfl_up(sum, i);
+                sum += lane >= i ? up : 0;
+            }
+        int at;
+        if (by_row) {
+            at = want - s0;
+            if (at < 0 || at > 63) at = -1;
+        } else {
+            const uint64_t past = __ballot(before + sum > want);
+            at = past ? __builtin_ctzll(past) : -1;
+        }
+        if (at >= 0) {
+            it.s = s0 + at;
+            it.ns = __builtin_amdgcn_readlane(ns, at);
+            it.first = __builtin_amdgcn_readlane(v.first, at);
+            it.n = __builtin_amdgcn_readlane(v.n, at);
+            it.len = __builtin_amdgcn_readlane(v.len, at);
+            const int tiles = __builtin_amdgcn_readlane(v.tiles, at);
+            const int id = before + __builtin_amdgcn_readlane(sum, at) - tiles * it.ns;
+            it.j = by_row ? j : (want - id) / it.ns;
+            it.split = by_row ? 0 : (want - id) % it.ns;
+            it.id0 = id + it.j * it.ns;
+            // (always so, but for starts that decrease)
+            return it.s < a.sq.nseq && it.j >= 0 && it.j < tiles && it.id0 >= 0 && it.id0 + it.ns <= a.nitems;
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    return false;
 }
 
 __device__ __forceinline__ void store_out(const Heads &o, int64_t i, float v) {
@@ -152,19 +180,19 @@ __device__ __forceinline__ void store_out(const Heads &o, int64_t i, float v) {
 // halves are added once per tile.  Otherwise tiles of 16 MT rows.
 template <int MT, bool PAIR> struct Form {
     static constexpr int RT = PAIR ? 8 : 16 * MT;
-    static constexpr int AW = PAIR ? 8 : 4;  // waves of a workgroup
 };
+// Waves of a workgroup.
+constexpr int waves(int D, int rt) { return D == 256 && rt == 8 ? 8 : 4; }
 
 // One workgroup: a tile of query rows, one KV head, one split of the
 // positions; its waves take tiles of 32 positions in turn and join at the end.
 template <int D, int MT, bool PAIR>
-__global__ void __launch_bounds__(PAIR ? 512 : 256, MT == 1 ? 2 : 1) kv_attn_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), MT == 1 ? 2 : 1) kv_attn_kernel(AttnArgs a) {
     using L = KvLayout<D>;
-    constexpr int G = L::G, RT = Form<MT, PAIR>::RT, AW = Form<MT, PAIR>::AW, NT = D / 16, OP = D + 4;
+    constexpr int G = L::G, RT = Form<MT, PAIR>::RT, AW = waves(D, RT), NT = D / 16, OP = D + 4;
     constexpr int RC = PAIR ? 8 : 16;     // rows side by side in a wave's columns
     constexpr int GL = PAIR ? G / 2 : G;  // groups whose steps a lane keeps
     constexpr int VD = D >= 128 ? 4 : 2;  // dwords of a lane's four value pieces
-    constexpr bool AHEAD = PAIR || D < 256;  // the next tile's loads under this tile's work (registers permitting)
     __shared__ float4 red4[AW * RC * OP / 4];
     __shared__ float2 st[AW][RT];
     float *red = reinterpret_cast<float *>(red4);
@@ -172,15 +200,15 @@ __global__ void __launch_bounds__(PAIR ? 512 : 256, MT == 1 ? 2 : 1) kv_attn_ker
     const int col = lane & 15, quad = lane >> 4;
     const int hc = PAIR ? col >> 3 : 0;   // half of the groups, by column
     const int hk = blockIdx.x % a.c.hkv, bs = blockIdx.x / a.c.hkv;
-    const int split = bs % a.nsplit, tile = bs / a.nsplit;
-    Tile t;
-    if (!find_tile<RT>(a, tile, lane, t) || split >= t.ns) return;
+    Item t;
+    if (!find_item<RT>(a, bs, false, 0, lane, t)) return;
     const int R = t.n * a.grp;
     const int64_t cap = (int64_t)a.sq.max_pages << a.c.ps_log2;
-
-    const int64_t nt = t.t1 - t.t0;
-    const int x0 = __builtin_amdgcn_readfirstlane((int)(t.t0 + nt * split / t.ns));
-    const int x1 = __builtin_amdgcn_readfirstlane((int)(t.t0 + nt * (split + 1) / t.ns));
+    // positions of the tile's first and last row, and the split's tiles of 32
+    const int64_t p0 = (int64_t)t.len - t.n, pmin = p0 + t.j * RT / a.grp, pmax = p0 + (min(t.j * RT + RT, R) - 1) / a.grp;
+    const int64_t end = min(pmax + 1, cap), begin = a.window ? max((int64_t)0, pmin - a.window + 1) : 0;
+    const int64_t tb = begin >> 5, nt = end > begin ? ((end + 31) >> 5) - tb : 0;
+    const int x0 = (int)(tb + nt * t.split / t.ns), x1 = (int)(tb + nt * (t.split + 1) / t.ns);
     const int32_t *table = a.sq.pages + (int64_t)t.s * a.sq.max_pages;
     const int tsh = a.c.ps_log2 - 5;
     const int64_t pstride = 2 * a.c.hkv * L::block(a.c.ps_log2);
@@ -240,7 +268,7 @@ __global__ void __launch_bounds__(PAIR ? 512 : 256, MT == 1 ? 2 : 1) kv_attn_ker
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         const int r = t.j * RT + mt * 16 + (col & (RC - 1)), rr = min(r, R - 1), tok = rr / a.grp;
-        const int64_t pos = t.p0 + tok;
+        const int64_t pos = p0 + tok;
         lim[mt] = (int)max((int64_t)-1, min(pos, cap - 1));
         low[mt] = a.window ? (int)min(max((int64_t)0, pos - a.window + 1), (int64_t)INT32_MAX) : 0;
         const _Float16 *src = reinterpret_cast<const _Float16 *>(a.q.p) + (int64_t)(t.first + tok) * a.q.row +
@@ -268,10 +296,8 @@ __global__ void __launch_bounds__(PAIR ? 512 : 256, MT == 1 ? 2 : 1) kv_attn_ker
         }
         if (mt == 0 && x < x1) {  // the first tile's loads, before the queries are waited for
             page = __builtin_amdgcn_readlane(ahead, 0);
-            if (AHEAD) {
-                load_k(max(page, 0), x);
-                load_v(max(page, 0), x);
-            }
+            load_k(max(page, 0), x);
+            load_v(max(page, 0), x);
         }
 #pragma unroll
         for (int i = 0; i < G; ++i)
@@ -323,19 +349,18 @@ __global__ void __launch_bounds__(PAIR ? 512 : 256, MT == 1 ? 2 : 1) kv_attn_ker
         qs[mt] = u4{sums[0], sums[1], sums[2], sums[3]};
     }
     // (wave-uniform) tiles that every row sees whole, and positions that hold something
-    const int64_t all_lo = a.window ? max((int64_t)0, t.p0 + (min(t.j * RT + RT, R) - 1) / a.grp - a.window + 1) : 0;
-    const int64_t all_hi = min(t.p0 + (int64_t)(t.j * RT / a.grp), cap - 1);
-    const int64_t held = min(t.p0 + t.n, cap);
+    const int64_t all_lo = a.window ? max((int64_t)0, pmax - a.window + 1) : 0, all_hi = min(pmin, cap - 1);
+    const int64_t held = min((int64_t)t.len, cap);
 
     f4 o[MT][NT], om[MT];
-    float m[MT], l[MT];
+    float m[MT], grow[MT];  // the maximum so far; how far a score may pass it before it moves (M_NONE: no score yet)
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) o[mt][i] = f4{0.f, 0.f, 0.f, 0.f};
         om[mt] = f4{0.f, 0.f, 0.f, 0.f};
-        m[mt] = M_NONE;
-        l[mt] = 0.f;
+        m[mt] = 0.f;
+        grow[mt] = M_NONE;
     }
 
     // Keys of the next tile are asked for when this tile's are used up, and
@@ -350,10 +375,6 @@ __global__ void __launch_bounds__(PAIR ? 512 : 256, MT == 1 ? 2 : 1) kv_attn_ker
             if ((k & 63) == 0) look_ahead(nx);
             np = __builtin_amdgcn_readlane(ahead, k & 63);
         }
-        if (!AHEAD) {
-            load_k(max(page, 0), x);
-            load_v(max(page, 0), x);
-        }
 
         // scores
         float z[MT][2][4];
@@ -364,7 +385,10 @@ __global__ void __launch_bounds__(PAIR ? 512 : 256, MT == 1 ? 2 : 1) kv_attn_ker
 #pragma unroll
             for (int i = 0; i < G / 2; ++i) mo[i] = km[u][i];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) s[mt] = mfma(mo, qs[mt], f4{0.f, 0.f, 0.f, 0.f});
+            for (int mt = 0; mt < MT; ++mt) {
+                s[mt] = mfma(mo, qs[mt], f4{0.f, 0.f, 0.f, 0.f});
+                acc[mt] = f4{0.f, 0.f, 0.f, 0.f};
+            }
 #pragma unroll
             for (int g = 0; g < GL; ++g) {
                 u4 ko[2];
@@ -379,26 +403,23 @@ __global__ void __launch_bounds__(PAIR ? 512 : 256, MT == 1 ? 2 : 1) kv_attn_ker
                 for (int mt = 0; mt < MT; ++mt) {
                     f4 r = mfma(ko[0], qf[mt][PAIR ? 2 * g : g], f4{0.f, 0.f, 0.f, 0.f});
                     if constexpr (PAIR) r = mfma(ko[1], qf[mt][2 * g + 1], r);
-                    if (g == 0) acc[mt] = f4{d0 * r.x, d1 * r.y, d2 * r.z, d3 * r.w};
-                    else
-                        acc[mt] = f4{fmaf(d0, r.x, acc[mt].x), fmaf(d1, r.y, acc[mt].y), fmaf(d2, r.z, acc[mt].z),
-                                     fmaf(d3, r.w, acc[mt].w)};
+                    acc[mt] = f4{fmaf(d0, r.x, acc[mt].x), fmaf(d1, r.y, acc[mt].y), fmaf(d2, r.z, acc[mt].z),
+                                 fmaf(d3, r.w, acc[mt].w)};
                 }
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float y = fmaf(acc[mt][i], sc1[mt], s[mt][i] * sc2[mt]);
+                    // less the maximum so far (each half of the columns takes half of it)
+                    float y = fmaf(acc[mt][i], sc1[mt], fmaf(s[mt][i], sc2[mt], PAIR ? -0.5f * m[mt] : -m[mt]));
                     if constexpr (PAIR) y += row_half_swap(y);
                     z[mt][u][i] = y;
                 }
         }
-        if (AHEAD) {
-            __builtin_amdgcn_sched_barrier(0);
-            load_k(max(np, 0), nx);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        __builtin_amdgcn_sched_barrier(0);
+        load_k(max(np, 0), nx);
+        __builtin_amdgcn_sched_barrier(0);
         if (!live || x * 32 < all_lo || x * 32 + 31 > all_hi) {
             const int base = x * 32 + 4 * quad;
 #pragma unroll
@@ -419,23 +440,26 @@ __global__ void __launch_bounds__(PAIR ? 512 : 256, MT == 1 ? 2 : 1) kv_attn_ker
             float mx = z[mt][0][0];
 #pragma unroll
             for (int i = 1; i < 8; ++i) mx = fmaxf(mx, z[mt][i >> 2][i & 3]);
-            if (__any(mx > m[mt] + GROW)) {
+            if (__any(mx > grow[mt])) {
                 mx = fmaxf(mx, __shfl_xor(mx, 16));
                 mx = fmaxf(mx, __shfl_xor(mx, 32));
-                const float mn = fmaxf(mx, m[mt]), al = __builtin_amdgcn_exp2f(m[mt] - mn);
-                m[mt] = mn;
-                l[mt] *= al;
+                const bool fresh = grow[mt] == M_NONE, some = mx > M_NONE;
+                const float up = fresh ? (some ? mx : 0.f) : fmaxf(mx, 0.f);
+                const float al = fresh ? 0.f : __builtin_amdgcn_exp2f(-up);
+                m[mt] += up;
+                if (some) grow[mt] = GROW;
                 om[mt] *= al;
 #pragma unroll
                 for (int i = 0; i < NT; ++i) o[mt][i] *= al;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[mt][i >> 2][i & 3] -= up;
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int k2 = 0; k2 < 2; ++k2) {
-                    const float p0 = __builtin_amdgcn_exp2f(z[mt][u][2 * k2] - m[mt]);
-                    const float p1 = __builtin_amdgcn_exp2f(z[mt][u][2 * k2 + 1] - m[mt]);
-                    l[mt] += p0 + p1;
+                    const float p0 = __builtin_amdgcn_exp2f(z[mt][u][2 * k2]);
+                    const float p1 = __builtin_amdgcn_exp2f(z[mt][u][2 * k2 + 1]);
                     ph[mt][u][k2] = pack(p0, p1);
                     pl[mt][u][k2] = pack(p0 - lo_f(ph[mt][u][k2]), p1 - hi_f(ph[mt][u][k2]));
                 }
@@ -458,7 +482,9 @@ __global__ void __launch_bounds__(PAIR ? 512 : 256, MT == 1 ? 2 : 1) kv_attn_ker
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const u4 mo = {vm[0][0], vm[0][1], vm[1][0], vm[1][1]};
+            // row G of the minima is ones: its sum is the softmax's
+            u4 mo = {vm[0][0], vm[0][1], vm[1][0], vm[1][1]};
+            if (col == G) mo = u4{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
             om[mt] = mfma(mo, u4{ph[mt][0][0], ph[mt][0][1], ph[mt][1][0], ph[mt][1][1]}, om[mt]);
             om[mt] = mfma(mo, u4{pl[mt][0][0], pl[mt][0][1], pl[mt][1][0], pl[mt][1][1]}, om[mt]);
         }
@@ -505,23 +531,21 @@ __global__ void __launch_bounds__(PAIR ? 512 : 256, MT == 1 ? 2 : 1) kv_attn_ker
                 }
             }
         }
-        if (AHEAD) {
-            __builtin_amdgcn_sched_barrier(0);
-            load_v(max(np, 0), nx);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        __builtin_amdgcn_sched_barrier(0);
+        load_v(max(np, 0), nx);
+        __builtin_amdgcn_sched_barrier(0);
         page = np;
     }
 
     // join the waves: common maximum, then sums through LDS, RC rows at a time
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        l[mt] += __shfl_xor(l[mt], 16);
-        l[mt] += __shfl_xor(l[mt], 32);
-        if (quad == 0 && hc == 0) st[wave][mt * 16 + col] = make_float2(m[mt], l[mt]);
+        const float sum = om[mt][G & 3];  // row G, in quad G / 4
+        if (grow[mt] == M_NONE) m[mt] = M_NONE;
+        if (quad == G / 4 && hc == 0) st[wave][mt * 16 + col] = make_float2(m[mt], sum);
     }
     __syncthreads();
-    const int64_t unit = ((int64_t)tile * a.c.hkv + hk) * a.nsplit + split;
+    const int64_t unit = ((int64_t)bs) * a.c.hkv + hk;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         const int row0 = col & (RC - 1);
@@ -585,19 +609,11 @@ __global__ void __launch_bounds__(256) kv_attn_join_kernel(AttnArgs a) {
     const RowSeq rs = row_seq(a.sq, row, lane);
     if (rs.s >= a.sq.nseq) return;
     const int hk = h / a.grp, r = (row - rs.first) * a.grp + h % a.grp;
-    Tile t;
-    t.s = rs.s;
-    t.first = rs.first;
-    t.n = rs.n;
-    t.j = r / RT;
-    tile_range<RT>(a, t);
+    Item t;
+    if (!find_item<RT>(a, rs.s, true, r / RT, lane, t) || t.ns == 1) return;  // (one split: written already)
     const int ns = t.ns;
-    if (ns == 1) return;  // written already
-    const int64_t tile = a.sq.q_start ? tile_base<RT>(a, clamp_row(a.sq, rs.first), rs.s) + t.j
-                                      : (int64_t)rs.s * ((rs.n * a.grp + RT - 1) / RT) + t.j;
-    if (tile >= a.ntiles) return;
-    const int64_t unit = (tile * a.c.hkv + hk) * a.nsplit;
-    const float2 v = tid < ns ? a.ml[(unit + tid) * RT + r % RT] : make_float2(M_NONE, 0.f);
+    auto unit = [&](int s) { return ((int64_t)(t.id0 + s) * a.c.hkv + hk) * RT + r % RT; };
+    const float2 v = tid < ns ? a.ml[unit(tid)] : make_float2(M_NONE, 0.f);
     float mx = v.x;
     for (int i = 1; i < 64; i <<= 1) mx = fmaxf(mx, __shfl_xor(mx, i));
     if (lane == 0) mx_s[wave] = mx;
@@ -615,7 +631,7 @@ __global__ void __launch_bounds__(256) kv_attn_join_kernel(AttnArgs a) {
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 8
     for (int s = wave; s < ns; s += 4) {
-        const float *p = a.o + ((unit + s) * RT + r % RT) * D + lane * E;
+        const float *p = a.o + unit(s) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(wt[s], p[e], acc[e]);
     }
@@ -630,21 +646,22 @@ __global__ void __launch_bounds__(256) kv_attn_join_kernel(AttnArgs a) {
 
 // Launch shape: from sizes alone (the lengths are on the device).
 struct Shape {
-    int rt, ntiles, nsplit, per_split;
+    int rt, target, min_chunk, nitems;
 };
 Shape attn_shape(const KvCache &c, const KvSeqs &sq, int hq) {
     const int grp = hq / c.hkv;
     Shape s;
     const int64_t n = sq.rows / sq.nseq, per_seq = ((int64_t)sq.rows * grp + sq.nseq - 1) / sq.nseq;
-    s.rt = per_seq <= 8 ? 8 : per_seq <= 16 || c.D == 256 ? 16 : 32;
-    s.ntiles = (int)(sq.q_start ? (int64_t)sq.rows * grp / s.rt + sq.nseq : sq.nseq * ((n * grp + s.rt - 1) / s.rt));
+    s.rt = per_seq <= 8 || c.D == 256 ? 8 : per_seq <= 16 ? 16 : 32;
+    const int64_t tiles = sq.q_start ? (int64_t)sq.rows * grp / s.rt + std::min(sq.nseq, sq.rows)
+                                     : sq.nseq * ((n * grp + s.rt - 1) / s.rt);
+    const int aw = waves(c.D, s.rt);
+    s.min_chunk = 2 * aw;
     const int64_t most = ((int64_t)sq.max_pages << c.ps_log2) / 32;  // tiles of 32 positions
-    const int64_t base = (int64_t)s.ntiles * c.hkv, aw = s.rt == 8 ? 8 : 4;
-    const int64_t slots = s.rt == 8 ? device_cus() : 2 * device_cus();
-    s.per_split = (int)(2 * aw);
-    int64_t ns = slots / base;
-    ns = std::min<int64_t>(ns, (most + s.per_split - 1) / s.per_split);
-    s.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(ns, MAX_SPLIT));
+    const int64_t slots = (int64_t)device_cus() * (c.D == 256 ? 8 : 12) / aw;  // workgroups that fit at once
+    const int64_t share = slots * (sq.nseq > 1 ? 2 : 1) / c.hkv - tiles;
+    s.target = most > s.min_chunk && share > tiles ? (int)share : 0;
+    s.nitems = (int)(tiles + s.target);
     return s;
 }
 
@@ -652,34 +669,29 @@ Shape attn_shape(const KvCache &c, const KvSeqs &sq, int hq) {
 
 int64_t kv_attn_workspace(const KvCache &c, const KvSeqs &sq, int hq) {
     const Shape s = attn_shape(c, sq, hq);
-    if (s.nsplit == 1) return 0;
-    return (int64_t)s.ntiles * c.hkv * s.nsplit * s.rt * (4 * c.D + 8);
+    return s.target ? (int64_t)s.nitems * c.hkv * s.rt * (4 * c.D + 8) : 0;
 }
 
 hipError_t launch_kv_attn(const KvCache &c, const KvSeqs &seqs, int hq, const Heads &q, const Heads &out, float scale,
                           int window, void *workspace, hipStream_t st) {
     const Shape s = attn_shape(c, seqs, hq);
-    AttnArgs a{c, seqs, q, out, hq, hq / c.hkv, window, s.nsplit, s.ntiles, s.per_split, scale, 0, nullptr, nullptr};
+    AttnArgs a{c, seqs, q, out, hq, hq / c.hkv, window, s.target, s.min_chunk, s.nitems, scale, 0, nullptr, nullptr};
     a.qvec = q.elem == 1 && q.row % 8 == 0 && q.head % 8 == 0 && ((uintptr_t)q.p & 15) == 0;
-    if (s.nsplit > 1) {
+    if (s.target) {
         a.o = (float *)workspace;
-        a.ml = (float2 *)(a.o + (int64_t)s.ntiles * c.hkv * s.nsplit * s.rt * c.D);
+        a.ml = (float2 *)(a.o + (int64_t)s.nitems * c.hkv * s.rt * c.D);
     }
-    const int64_t blocks = (int64_t)s.ntiles * c.hkv * s.nsplit;
     auto go = [&](auto kern, auto join) -> hipError_t {
-        hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(s.rt == 8 ? 512 : 256), 0, st, a);
+        hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)s.nitems * c.hkv)), dim3(64 * waves(c.D, s.rt)), 0, st, a);
         hipError_t e = hipGetLastError();
-        if (e != hipSuccess || s.nsplit == 1) return e;
+        if (e != hipSuccess || !s.target) return e;
         hipLaunchKernelGGL(join, dim3((unsigned)(seqs.rows * hq)), dim3(256), 0, st, a);
         return hipGetLastError();
     };
 #define QK_ATTN(D)                                                                                    \
     if (s.rt == 8) return go(kv_attn_kernel<D, 1, true>, kv_attn_join_kernel<D, 8>);                  \
     if (s.rt == 16) return go(kv_attn_kernel<D, 1, false>, kv_attn_join_kernel<D, 16>)
-    if (c.D == 256) {
-        QK_ATTN(256);
-        return hipErrorInvalidValue;  // (no shape of 32 rows for D = 256)
-    }
+    if (c.D == 256) return go(kv_attn_kernel<256, 1, true>, kv_attn_join_kernel<256, 8>);
     if (c.D == 128) {
         QK_ATTN(128);
         return go(kv_attn_kernel<128, 2, false>, kv_attn_join_kernel<128, 32>);
