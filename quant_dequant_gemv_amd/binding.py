@@ -485,30 +485,45 @@ class Chain:
 # Heads are tensors [rows, heads, D] of any strides >= 0, float16 or float32:
 # y of a GEMV is y.view(heads, D, ncols).permute(2, 0, 1).  Work runs, and
 # what a helper allocates is allocated, on the tensors' device and on
-# ``stream`` (None: that device's current stream).
+# ``stream`` (None: that device's current stream).  These calls are a few
+# microseconds on the device, so what is right is found right in a few steps
+# here, and put into words only where it is not.
 
-def _heads_arg(t, name, rows=None, heads=None, D=None, dtypes=None):
-    """The qk_heads of a tensor [rows, heads, D], checked against the sizes given."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+_torch = _f16 = None  # set by the first KVCache or Rope, which every call here takes: torch, {float16: 1, float32: 0}
+
+
+def _start():
+    global _torch, _f16
+    if _torch is None:
+        import torch
+        load_library()
+        _f16 = {torch.float16: 1, torch.float32: 0}
+        _torch = torch
+    return _torch
+
+
+def _heads_arg(t, name, rows=None, heads=None, D=None):
+    """The qk_heads of a tensor [rows, heads, D], checked against the sizes given (None: any)."""
+    try:
+        f16 = _f16[t.dtype]
+        r, h, d = t.shape
+        if (rows is None or r == rows) and (heads is None or h == heads) and (D is None or d == D):
+            return qk_heads(t.data_ptr(), *t.stride(), f16)
+    except (AttributeError, KeyError, ValueError):
+        pass
+    if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    dt = t.dtype
-    if dt is not torch.float16 and dt is not torch.float32 or dtypes and dt not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes or (torch.float16, torch.float32)))}, got {dt}")
-    shape = t.shape
-    if len(shape) != 3 or (rows is not None and shape[0] != rows) or (heads is not None and shape[1] != heads) or \
-            (D is not None and shape[2] != D):
-        raise ValueError(f"{name} must have shape [{'rows' if rows is None else rows}, "
-                         f"{'heads' if heads is None else heads}, {'D' if D is None else D}], got {tuple(shape)}")
-    return qk_heads(t.data_ptr(), *t.stride(), 1 if dt is torch.float16 else 0)
+    if t.dtype not in _f16:
+        raise TypeError(f"{name} must be torch.float16 or torch.float32, got {t.dtype}")
+    want = ["rows" if rows is None else rows, "heads" if heads is None else heads, "D" if D is None else D]
+    raise ValueError(f"{name} must have shape [{', '.join(map(str, want))}], got {tuple(t.shape)}")
 
 
 def _int32_arg(t, name, shape):
     """The address of a contiguous int32 tensor of this shape (None entries: any size)."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype is not torch.int32:
+    if t.dtype is not _torch.int32:
         raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
     if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
         raise ValueError(f"{name} must have shape {list(shape)}, got {tuple(t.shape)}")
@@ -518,42 +533,57 @@ def _int32_arg(t, name, shape):
 
 
 def _seqs_arg(rows, pages, kv_len, q_start):
-    nseq = kv_len.shape[0] if getattr(kv_len, "shape", None) else None
-    return qk_kv_seqs(rows, nseq or 0, pages.shape[1] if getattr(pages, "ndim", 0) == 2 else 0,
-                      None if q_start is None else _int32_arg(q_start, "q_start", (None if nseq is None else nseq + 1,)),
-                      _int32_arg(kv_len, "kv_len", (None,)), _int32_arg(pages, "pages", (nseq, None)))
+    i32 = _torch.int32
+    try:
+        nseq, = kv_len.shape
+        n, mp = pages.shape
+        if kv_len.dtype is i32 and pages.dtype is i32 and n == nseq and kv_len.is_contiguous() and \
+                pages.is_contiguous():
+            if q_start is None:
+                return qk_kv_seqs(rows, nseq, mp, None, kv_len.data_ptr(), pages.data_ptr())
+            if q_start.dtype is i32 and q_start.shape == (nseq + 1,) and q_start.is_contiguous():
+                return qk_kv_seqs(rows, nseq, mp, q_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr())
+    except (AttributeError, ValueError):
+        pass
+    _int32_arg(kv_len, "kv_len", (None,))
+    nseq = kv_len.shape[0]
+    _int32_arg(pages, "pages", (nseq, None))
+    _int32_arg(q_start, "q_start", (nseq + 1,))
+    raise ValueError("bad sequences")
 
 
-def _one_device(named):
-    """The CUDA device that all of the named tensors (None: absent) are on."""
-    dev = None
-    for name, t in named:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA (HIP) device tensor, is on {t.device}")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"all tensors must be on one device, got {dev} and {name} on {t.device}")
-    return dev
+def _one_device(*tensors, names):
+    """The index of the CUDA device that all of the tensors (None: absent) are on."""
+    dev = tensors[0].get_device()
+    if dev >= 0:
+        for t in tensors:
+            if t is not None and t.get_device() != dev:
+                break
+        else:
+            return dev
+    _same_cuda_device(**dict(zip(names.split(), tensors)))
+    raise ValueError("all tensors must be on one device")
 
 
 def _elsewhere(dev, stream):
-    """None where ``dev`` and ``stream`` are the current ones, else a context in which they are."""
-    import contextlib
-
-    import torch
+    """None where device ``dev`` and ``stream`` are the current ones, else a context in which they are."""
+    torch = _torch
     if stream is None:
-        return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        return None if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+    import contextlib
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
     both = contextlib.ExitStack()
     both.enter_context(torch.cuda.device(dev))
     both.enter_context(torch.cuda.stream(stream))
     return both
+
+
+def _current(dev):
+    """The handle of a device's current stream."""
+    return _torch._C._cuda_getCurrentRawStream(dev)
 
 
 class Rope:
@@ -562,9 +592,9 @@ class Rope:
     norm)."""
 
     def __init__(self, inv_freq=None, interleaved: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6):
-        import torch
-        self.named = (("inv_freq", inv_freq), ("q_norm", q_norm), ("k_norm", k_norm))
-        for name, t in self.named:
+        torch = _start()
+        self.tensors = (inv_freq, q_norm, k_norm)
+        for name, t in zip(("inv_freq", "q_norm", "k_norm"), self.tensors):
             if t is not None:
                 _need(t, name, torch.float32)
                 if t.dim() != 1:
@@ -574,12 +604,12 @@ class Rope:
         self._c = qk_rope(*p, None, eps, 0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved))
 
     def arg(self, D, positions, rows):
-        if self.D - {D}:
+        """The qk_rope of one call."""
+        if self.D and self.D != {D}:
             raise ValueError(f"q_norm and k_norm must have {D} elements, have {sorted(self.D)}")
         if positions is None:
             return self._c
-        c = qk_rope()
-        ctypes.pointer(c)[0] = self._c
+        c = qk_rope.from_buffer_copy(self._c)
         c.positions = _int32_arg(positions, "positions", (rows,))
         return c
 
@@ -590,7 +620,7 @@ class KVCache:
     qk_kv_page_bytes(...) bytes (None: allocated here)."""
 
     def __init__(self, num_pages: int, n_kv_heads: int, head_dim: int, page_size: int = 64, device="cuda", pool=None):
-        import torch
+        torch = _start()
         pb = qk_kv_page_bytes(head_dim, n_kv_heads, page_size)
         if pb < 0 or not 1 <= num_pages < 1 << 31:
             raise QKError(QK_EINVAL_SHAPE, "KVCache")
@@ -606,32 +636,30 @@ def norm_rope(rope: Rope, positions, q, k=None, q_out=None, k_out=None, stream=N
     """Norm and rotation of q [rows, heads, D] and k [rows, kv heads, D]
     (either may be None) at ``positions`` (int32 [rows]); returns (q_out,
     k_out), float16 contiguous unless given (they may be q and k)."""
-    import torch
-    x = q if q is not None else k
-    if not isinstance(x, torch.Tensor) or x.dim() != 3:
-        raise ValueError("q or k must be a tensor [rows, heads, D]")
-    rows, _, D = x.shape
-    a = [None if t is None else _heads_arg(t, n, rows, None, D) for n, t in (("q", q), ("k", k))]
+    torch = _torch
+    qa = None if q is None else _heads_arg(q, "q")
+    rows, hq, D = (None, 0, None) if q is None else q.shape
+    ka = None if k is None and q is not None else _heads_arg(k, "k", rows, None, D)
+    hk = 0
+    if ka is not None:
+        rows, hk, D = k.shape
     r = rope.arg(D, positions, rows)
-    dev = _one_device((("q", q), ("k", k), ("positions", positions), ("q_out", q_out), ("k_out", k_out), *rope.named))
+    dev = _one_device(q if q is not None else k, k, positions, q_out, k_out, *rope.tensors,
+                      names="q k positions q_out k_out inv_freq q_norm k_norm")
     if (ctx := _elsewhere(dev, stream)) is not None:
         with ctx:
             return norm_rope(rope, positions, q, k, q_out, k_out)
-    outs = []
-    for n, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
-        if t is None:
-            if o is not None:
-                raise ValueError(f"{n} without its input")
-            outs.append((None, None))
-            continue
-        if o is None:
-            o = torch.empty(t.shape, dtype=torch.float16, device=dev)
-        outs.append((o, _heads_arg(o, n, *t.shape)))
-    rc = qk_norm_rope(r, rows, D, 0 if q is None else q.shape[1], a[0], outs[0][1], 0 if k is None else k.shape[1],
-                      a[1], outs[1][1], torch.cuda.current_stream(dev).cuda_stream)
+    if q is None and q_out is not None or k is None and k_out is not None:
+        raise ValueError("an output without its input")
+    if q is not None and q_out is None:
+        q_out = torch.empty((rows, hq, D), dtype=torch.float16, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty((rows, hk, D), dtype=torch.float16, device=k.device)
+    rc = _lib.qk_norm_rope(r, rows, D, hq, qa, None if q is None else _heads_arg(q_out, "q_out", rows, hq, D), hk, ka,
+                      None if k is None else _heads_arg(k_out, "k_out", rows, hk, D), _current(dev))
     if rc != QK_OK:
         raise QKError(rc, "qk_norm_rope")
-    return outs[0][0], outs[1][0]
+    return q_out, k_out
 
 
 def kv_append(cache: KVCache, k, v, pages, kv_len, q_start=None, q=None, rope: Rope | None = None, positions=None,
@@ -641,32 +669,35 @@ def kv_append(cache: KVCache, k, v, pages, kv_len, q_start=None, q=None, rope: R
     int32 [nseq + 1] or None), keys -- and the queries q [rows, heads, D] --
     normed and rotated by ``rope``; returns q_out (float16 unless given; None
     without q)."""
-    import torch
-    D = cache.head_dim
-    ka = _heads_arg(k, "k", None, cache.n_kv_heads, D)
+    torch = _torch
+    D, hk = cache.head_dim, cache.n_kv_heads
+    ka = _heads_arg(k, "k", None, hk, D)
     rows = k.shape[0]
-    va = _heads_arg(v, "v", rows, cache.n_kv_heads, D)
+    va = _heads_arg(v, "v", rows, hk, D)
     qa = None if q is None else _heads_arg(q, "q", rows, None, D)
     seqs = _seqs_arg(rows, pages, kv_len, q_start)
-    if rope is None and positions is not None:
-        raise ValueError("positions without a rope")
-    r = None if rope is None else rope.arg(D, positions, rows)
-    dev = _one_device((("k", k), ("v", v), ("pages", pages), ("kv_len", kv_len), ("q_start", q_start), ("q", q),
-                       ("q_out", q_out), ("pool", cache.pool), ("positions", positions),
-                       *(() if rope is None else rope.named)))
+    if rope is not None:
+        r = rope.arg(D, positions, rows)
+        dev = _one_device(k, v, pages, kv_len, q_start, q, q_out, cache.pool, positions, *rope.tensors,
+                          names="k v pages kv_len q_start q q_out pool positions inv_freq q_norm k_norm")
+    else:
+        if positions is not None:
+            raise ValueError("positions without a rope")
+        r = None
+        dev = _one_device(k, v, pages, kv_len, q_start, q, q_out, cache.pool,
+                          names="k v pages kv_len q_start q q_out pool")
     if (ctx := _elsewhere(dev, stream)) is not None:
         with ctx:
             return kv_append(cache, k, v, pages, kv_len, q_start, q, rope, positions, q_out)
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out without q")
-        oa = None
-    else:
+    hq, oa = 0, None
+    if q is not None:
+        hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.float16, device=dev)
-        oa = _heads_arg(q_out, "q_out", *q.shape)
-    rc = qk_kv_append(cache._c, seqs, r, ka, va, 0 if q is None else q.shape[1], qa, oa,
-                      torch.cuda.current_stream(dev).cuda_stream)
+            q_out = torch.empty((rows, hq, D), dtype=torch.float16, device=q.device)
+        oa = _heads_arg(q_out, "q_out", rows, hq, D)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rc = _lib.qk_kv_append(cache._c, seqs, r, ka, va, hq, qa, oa, _current(dev))
     if rc != QK_OK:
         raise QKError(rc, "qk_kv_append")
     return q_out
@@ -675,20 +706,19 @@ def kv_append(cache: KVCache, k, v, pages, kv_len, q_start=None, q=None, rope: R
 def kv_read(cache: KVCache, rows: int, pages, kv_len, q_start=None, k_out=None, v_out=None, stream=None):
     """What the cache holds at the rows' positions: (k, v), float32
     [rows, kv heads, D] unless given."""
-    import torch
+    torch = _torch
     seqs = _seqs_arg(rows, pages, kv_len, q_start)
     shape = (rows, cache.n_kv_heads, cache.head_dim)
-    dev = _one_device((("pages", pages), ("kv_len", kv_len), ("q_start", q_start), ("pool", cache.pool),
-                       ("k_out", k_out), ("v_out", v_out)))
+    dev = _one_device(pages, kv_len, q_start, cache.pool, k_out, v_out, names="pages kv_len q_start pool k_out v_out")
     if (ctx := _elsewhere(dev, stream)) is not None:
         with ctx:
             return kv_read(cache, rows, pages, kv_len, q_start, k_out, v_out)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.float32, device=dev)
+        k_out = torch.empty(shape, dtype=torch.float32, device=pages.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.float32, device=dev)
-    rc = qk_kv_read(cache._c, seqs, _heads_arg(k_out, "k_out", *shape), _heads_arg(v_out, "v_out", *shape),
-                    torch.cuda.current_stream(dev).cuda_stream)
+        v_out = torch.empty(shape, dtype=torch.float32, device=pages.device)
+    rc = _lib.qk_kv_read(cache._c, seqs, _heads_arg(k_out, "k_out", *shape), _heads_arg(v_out, "v_out", *shape),
+                    _current(dev))
     if rc != QK_OK:
         raise QKError(rc, "qk_kv_read")
     return k_out, v_out
@@ -700,28 +730,30 @@ def kv_attn(cache: KVCache, q, pages, kv_len, q_start=None, scale: float | None 
     scale None: D ** -0.5; window 0: none.  Returns out, float16 contiguous
     unless given.  workspace: uint8 device tensor of at least
     qk_kv_attn_workspace_bytes bytes (None: allocated for the call)."""
-    import torch
+    torch = _torch
     D = cache.head_dim
-    qa = _heads_arg(q, "q", None, None, D, (torch.float16,))
-    rows, heads = q.shape[0], q.shape[1]
+    qa = _heads_arg(q, "q", None, None, D)
+    if not qa.f16:
+        raise TypeError(f"q must be torch.float16, got {q.dtype}")
+    rows, heads, _ = q.shape
     seqs = _seqs_arg(rows, pages, kv_len, q_start)
-    if workspace is not None:
-        _need(workspace, "workspace", torch.uint8)
-    dev = _one_device((("q", q), ("pages", pages), ("kv_len", kv_len), ("q_start", q_start), ("out", out),
-                       ("pool", cache.pool), ("workspace", workspace)))
+    dev = _one_device(q, pages, kv_len, q_start, out, cache.pool, workspace,
+                      names="q pages kv_len q_start out pool workspace")
     if (ctx := _elsewhere(dev, stream)) is not None:
         with ctx:
             return kv_attn(cache, q, pages, kv_len, q_start, scale, window, out, workspace)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float16, device=dev)
+        out = torch.empty((rows, heads, D), dtype=torch.float16, device=q.device)
     oa = _heads_arg(out, "out", rows, heads, D)
+    c = cache._c
     if workspace is None:
-        need = qk_kv_attn_workspace_bytes(cache._c, seqs, heads)
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    rc = qk_kv_attn(cache._c, seqs, heads, qa, oa, D ** -0.5 if scale is None else scale, window,
-                    None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-                    torch.cuda.current_stream(dev).cuda_stream)
+        need = _lib.qk_kv_attn_workspace_bytes(c, seqs, heads)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+    else:
+        _need(workspace, "workspace", torch.uint8)
+        ws, need = workspace, workspace.numel()
+    rc = _lib.qk_kv_attn(c, seqs, heads, qa, oa, D ** -0.5 if scale is None else scale, window,
+                    None if ws is None else ws.data_ptr(), max(need, 0), _current(dev))
     if rc != QK_OK:
         raise QKError(rc, "qk_kv_attn")
     return out
