@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "qk_kv.h"
 
 namespace qk {
@@ -21,195 +23,282 @@ __device__ __forceinline__ void wave_sync() {
 __device__ __forceinline__ float load_head(const Heads &x, int64_t i) {
     return x.f16 ? (float)reinterpret_cast<const _Float16 *>(x.p)[i] : reinterpret_cast<const float *>(x.p)[i];
 }
-__device__ __forceinline__ void store_head(const Heads &x, int64_t i, double v) {
-    if (x.f16) reinterpret_cast<_Float16 *>(x.p)[i] = (_Float16)(float)v;
-    else reinterpret_cast<float *>(x.p)[i] = (float)v;
+__device__ __forceinline__ void store_head(const Heads &x, int64_t i, float v) {
+    if (x.f16) reinterpret_cast<_Float16 *>(x.p)[i] = (_Float16)v;
+    else reinterpret_cast<float *>(x.p)[i] = v;
 }
 
-template <int D> struct WaveLds {
-    double x[D];           // a normed row, for the pairs of the rotation
-    double2 trig[D / 2];   // (cos, sin) of the row's angles
-    uint8_t code[D];
+// A lane has 4 consecutive dimensions of a head, so a wave has HPW = 256 / D
+// heads of one kind side by side, and a group of 32 dimensions is 8 lanes.
+constexpr int lanes_of(int D) { return D / 4; }
+
+// v of the lane `CTRL` away inside a row of 16 lanes (a DPP pattern: no LDS)
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL> __device__ __forceinline__ double dpp(double v) {
+    const uint2 w = __builtin_bit_cast(uint2, v);
+    const uint2 r = make_uint2(__builtin_amdgcn_update_dpp(0, (int)w.x, CTRL, 0xf, 0xf, true),
+                               __builtin_amdgcn_update_dpp(0, (int)w.y, CTRL, 0xf, 0xf, true));
+    return __builtin_bit_cast(double, r);
+}
+constexpr int SWAP1 = 0xB1, SWAP2 = 0x4E, MIRROR8 = 0x141, MIRROR16 = 0x140;  // quad_perm [1,0,3,2], [2,3,0,1]; half row, row
+
+// Sum over the lanes of a head: every lane gets it.
+template <int LPH> __device__ __forceinline__ double head_sum(double v) {
+    v += dpp<SWAP1>(v);
+    v += dpp<SWAP2>(v);
+    v += dpp<MIRROR8>(v);
+    v += dpp<MIRROR16>(v);
+    if (LPH > 16) v += __shfl_xor(v, 16);
+    if (LPH > 32) v += __shfl_xor(v, 32);
+    return v;
+}
+
+// x[0..3] = elements i0 .. i0+3 at element index `base` of a view.
+__device__ __forceinline__ void load4(const Heads &s, int64_t base, bool vec, float x[4]) {
+    if (vec && s.f16) {
+        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+        const h4 v = *reinterpret_cast<const h4 *>(reinterpret_cast<const _Float16 *>(s.p) + base);
+        for (int e = 0; e < 4; ++e) x[e] = (float)v[e];
+    } else if (vec) {
+        const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(s.p) + base);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = load_head(s, base + e * s.elem);
+    }
+}
+__device__ __forceinline__ void store4(const Heads &s, int64_t base, bool vec, const float x[4]) {
+    if (vec && s.f16) {
+        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<h4 *>(reinterpret_cast<_Float16 *>(s.p) + base) =
+            h4{(_Float16)x[0], (_Float16)x[1], (_Float16)x[2], (_Float16)x[3]};
+    } else if (vec) {
+        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(s.p) + base) = make_float4(x[0], x[1], x[2], x[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) store_head(s, base + e * s.elem, x[e]);
+    }
+}
+
+struct RowsArgs {
+    KvCache c;
+    KvSeqs sq;
+    RowPrep rp;
+    int hq, hkv, cached;
+    Heads q, qo, k, v, ko;
+    int vq, vqo, vk, vv, vko;  // the view's heads are whole 4-element pieces
+    int per, chunks;           // groups of HPW heads a wave takes, waves of a row
 };
 
-// One wave: E = D/64 consecutive dimensions a lane, groups of 32/E lanes.  A
-// row's angles are the same for all its heads, so a wave takes `per` heads of
-// one row and computes them once.
+// Norm, rotation and grouping in registers.  The pair of a rotated dimension
+// is in the same lane (interleaved) or, the normed value depending on its own
+// element alone, loaded a second time from where it lies (an L1 hit): nothing
+// but the row's sines and cosines passes LDS, once for all heads of the wave.
 template <int D>
-__global__ void __launch_bounds__(64 * WAVES)
-kv_rows_kernel(KvCache c, KvSeqs sq, RowPrep rp, int hq, Heads q, Heads qo, int hkv, Heads k, Heads v, Heads ko,
-               int cached, int per, int chunks) {
-    constexpr int E = D / 64;
+__global__ void __launch_bounds__(64 * WAVES) kv_rows_kernel(RowsArgs a) {
+    constexpr int LPH = lanes_of(D), HPW = 64 / LPH;
     using L = KvLayout<D>;
-    __shared__ WaveLds<D> lds[WAVES];
-    const int lane = threadIdx.x & 63;
-    WaveLds<D> &w = lds[threadIdx.x >> 6];
-    const int64_t unit = (int64_t)blockIdx.x * WAVES + (threadIdx.x >> 6);
-    const int64_t t64 = unit / chunks;
+    __shared__ double2 trig_s[WAVES][D / 2];
+    const KvCache &c = a.c;
+    const KvSeqs &sq = a.sq;
+    const RowPrep &rp = a.rp;
+    const int lane = threadIdx.x & 63, li = lane & (LPH - 1), sub = lane / LPH;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    double2 *trig = trig_s[wave];
+    const int64_t unit = (int64_t)blockIdx.x * WAVES + wave;
+    const int64_t t64 = unit / a.chunks;
     if (t64 >= sq.rows) return;
-    const int t = (int)t64, h0 = (int)(unit % chunks) * per;
+    const int t = (int)t64, g0 = (int)(unit % a.chunks) * a.per;
+    const int gq = (a.hq + HPW - 1) / HPW, gk = (a.hkv + HPW - 1) / HPW;
+    const int g1 = min(g0 + a.per, gq + gk * (a.cached ? 2 : 1));
 
     int64_t pos = 0;   // the row's place in its sequence
     int page = -1;
-    if (cached) {
+    if (a.cached) {
         const RowSeq r = row_seq(sq, t, lane);
         if (r.s >= sq.nseq) return;
         pos = (int64_t)sq.kv_len[r.s] - r.n + (t - r.first);
         page = kv_page(c, sq, r.s, pos);
     }
-    const int half = rp.rot_dim / 2;
-    if (half) {
+    const int half = rp.rot_dim / 2, i0 = 4 * li;
+    double cs[4] = {1, 1, 1, 1}, sn[4] = {0, 0, 0, 0};  // of the lane's dimensions, the sine with the pair's sign
+    int other = 0;                                      // where the pairs of its dimensions lie, from its own
+    if (half && g0 < gq + gk) {
         const double p = rp.positions ? (double)rp.positions[t] : (double)pos;
         for (int j = lane; j < half; j += 64) {
-            double sn, cs;
-            sincos(p * (double)rp.inv_freq[j], &sn, &cs);
-            w.trig[j] = make_double2(cs, sn);
+            double s1, c1;
+            sincos(p * (double)rp.inv_freq[j], &s1, &c1);
+            trig[j] = make_double2(c1, s1);
         }
         wave_sync();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + e;
+            if (i >= rp.rot_dim) continue;
+            const bool second = rp.interleaved ? e & 1 : i >= half;
+            const double2 w = trig[rp.interleaved ? i >> 1 : second ? i - half : i];
+            cs[e] = w.x;
+            sn[e] = second ? w.y : -w.y;
+        }
     }
+    // pairs in another lane: four of them side by side where half is a multiple of 4
+    const bool apart = half && !rp.interleaved;
+    other = i0 < half ? half : -half;
 
-    const int total = hq + hkv * (cached ? 2 : 1), h1 = min(h0 + per, total);
-    for (int h = h0; h < h1; ++h) {
-        const int kind = h < hq ? 0 : h < hq + hkv ? 1 : 2;  // query, key, value head
-        const Heads &src = kind == 0 ? q : kind == 1 ? k : v;
-        const int hh = kind == 0 ? h : kind == 1 ? h - hq : h - hq - hkv;
-        if (kind && cached && page < 0) continue;
-        const int64_t base = t * src.row + hh * src.head + (int64_t)(lane * E) * src.elem;
-        float f[E];
+    for (int gi = g0; gi < g1; ++gi) {
+        const int kind = gi < gq ? 0 : gi < gq + gk ? 1 : 2;  // query, key, value heads
+        if (kind && a.cached && page < 0) continue;
+        const Heads &src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+        const bool vec = kind == 0 ? a.vq : kind == 1 ? a.vk : a.vv;
+        const int count = kind == 0 ? a.hq : a.hkv;
+        const int h = (gi - (kind == 0 ? 0 : kind == 1 ? gq : gq + gk)) * HPW + sub;
+        const bool on = h < count;
+        const int64_t base = t * src.row + (on ? h : count - 1) * src.head;
+        float f[4];
+        load4(src, base + i0 * src.elem, vec, f);
+        if (kind < 2 && (half || rp.q_norm || rp.k_norm)) {
+            double x[4], y[4] = {0, 0, 0, 0};  // the lane's dimensions, and their pairs
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = load_head(src, base + e * src.elem);
-        double x[E];
+            for (int e = 0; e < 4; ++e) x[e] = f[e];
+            if (apart) {
+                float fo[4] = {0, 0, 0, 0};
+                if (vec && (half & 3) == 0) {
+                    if (i0 < rp.rot_dim) load4(src, base + (i0 + other) * src.elem, true, fo);
+                } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = f[e];
-        if (kind < 2) {
+                    for (int e = 0; e < 4; ++e)
+                        if (i0 + e < rp.rot_dim)
+                            fo[e] = load_head(src, base + (i0 + e + (i0 + e < half ? half : -half)) * src.elem);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = fo[e];
+            }
             const float *nw = kind == 0 ? rp.q_norm : rp.k_norm;
             if (nw) {
                 double ss = 0;
 #pragma unroll
-                for (int e = 0; e < E; ++e) ss = fma(x[e], x[e], ss);
+                for (int e = 0; e < 4; ++e) ss = fma(x[e], x[e], ss);
+                const double r = rsqrt(head_sum<LPH>(ss) * (1.0 / D) + (double)rp.eps);
 #pragma unroll
-                for (int m = 1; m < 64; m <<= 1) ss += __shfl_xor(ss, m);
-                const double r = 1.0 / sqrt(ss * (1.0 / D) + (double)rp.eps);
-#pragma unroll
-                for (int e = 0; e < E; ++e) x[e] = x[e] * r * (double)nw[lane * E + e];
-            }
-            if (half) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) w.x[lane * E + e] = x[e];
-                wave_sync();
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int i = lane * E + e;
-                    if (i < rp.rot_dim) {
-                        const int j = rp.interleaved ? i >> 1 : i < half ? i : i - half;
-                        const bool second = rp.interleaved ? i & 1 : i >= half;
-                        const int o = rp.interleaved ? i ^ 1 : second ? i - half : i + half;
-                        const double2 cs = w.trig[j];
-                        x[e] = second ? w.x[o] * cs.y + x[e] * cs.x : x[e] * cs.x - w.x[o] * cs.y;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const int i = i0 + e;
+                    x[e] = x[e] * (r * (double)nw[i]);
+                    if (apart && i < rp.rot_dim) y[e] = y[e] * (r * (double)nw[i < half ? i + half : i - half]);
                 }
-                wave_sync();
             }
-            if (kind == 0 || !cached) {
-                const Heads &dst = kind == 0 ? qo : ko;
-                const int64_t ob = t * dst.row + hh * dst.head + (int64_t)(lane * E) * dst.elem;
+            if (rp.interleaved) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) store_head(dst, ob + e * dst.elem, x[e]);
-                continue;
+                for (int e = 0; e < 4; ++e) y[e] = x[e ^ 1];
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                f[e] = (float)(half && i0 + e < rp.rot_dim ? fma(y[e], sn[e], x[e] * cs[e]) : x[e]);
+        }
+        if (kind == 0 || !a.cached) {
+            const Heads &dst = kind == 0 ? a.qo : a.ko;
+            if (on) store4(dst, t * dst.row + h * dst.head + i0 * dst.elem, kind == 0 ? a.vqo : a.vko, f);
+            continue;
         }
         // groups of 32 dimensions, in fp32 from the rounded row
-        float lo = 65504.f, hi = -65504.f;
+        float lo, hi;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float y = (float)x[e];
-            f[e] = y != y ? 0.f : fminf(fmaxf(y, -65504.f), 65504.f);
-            lo = fminf(lo, f[e]);
-            hi = fmaxf(hi, f[e]);
+        for (int e = 0; e < 4; ++e) {
+            f[e] = f[e] != f[e] ? 0.f : fminf(fmaxf(f[e], -65504.f), 65504.f);
+            lo = e ? fminf(lo, f[e]) : f[e];
+            hi = e ? fmaxf(hi, f[e]) : f[e];
         }
-#pragma unroll
-        for (int m = 1; m < 32 / E; m <<= 1) {
-            lo = fminf(lo, __shfl_xor(lo, m));
-            hi = fmaxf(hi, __shfl_xor(hi, m));
-        }
+        lo = fminf(lo, dpp<SWAP1>(lo)); hi = fmaxf(hi, dpp<SWAP1>(hi));
+        lo = fminf(lo, dpp<SWAP2>(lo)); hi = fmaxf(hi, dpp<SWAP2>(hi));
+        lo = fminf(lo, dpp<MIRROR8>(lo)); hi = fmaxf(hi, dpp<MIRROR8>(hi));
         const _Float16 mh = (_Float16)lo;
         const _Float16 dh = (_Float16)((hi - (float)mh) / 15.f);
         const float mf = (float)mh, df = (float)dh;
+        uint32_t code[4];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
+        for (int e = 0; e < 4; ++e) {
             const float z = df > 0.f ? rintf((f[e] - mf) / df) : 0.f;
-            w.code[lane * E + e] = (uint8_t)fminf(fmaxf(z, 0.f), 15.f);
+            code[e] = (uint32_t)fminf(fmaxf(z, 0.f), 15.f);
         }
-        wave_sync();
-        uint8_t *blk = c.pool + ((int64_t)page * hkv + hh) * 2 * L::block(c.ps_log2) +
+        uint8_t *blk = c.pool + ((int64_t)page * a.hkv + (on ? h : 0)) * 2 * L::block(c.ps_log2) +
                        (kind == 2 ? L::block(c.ps_log2) : 0);
-        const int p = (int)(pos & ((1 << c.ps_log2) - 1)), g = lane * E / 32;
-        if (lane % (32 / E) == 0) {
+        const int p = (int)(pos & ((1 << c.ps_log2) - 1)), g = li >> 3;
+        if (on && (li & 7) == 0) {
             reinterpret_cast<_Float16 *>(blk + L::d_off(c.ps_log2))[L::by4(p, g)] = dh;
             reinterpret_cast<_Float16 *>(blk + L::m_off(c.ps_log2))[kind == 1 ? p * L::G + g : L::by4(p, g)] = mh;
         }
         if (kind == 1) {
-            if (lane < D / 8) {
-                const uint2 b = *reinterpret_cast<const uint2 *>(w.code + 32 * (lane % L::G) + 8 * (lane / L::G));
-                uint32_t word = 0;
-#pragma unroll
-                for (int n = 0; n < 8; ++n) word |= (((n < 4 ? b.x : b.y) >> (8 * (n & 3))) & 15u) << (4 * n);
-                reinterpret_cast<uint32_t *>(blk + p * L::ROW)[lane] = word;
+            // half of word (a, g), a = li / 2 % 4
+            const uint32_t w = code[0] | code[1] << 4 | code[2] << 8 | code[3] << 12;
+            if (on)
+                *reinterpret_cast<uint16_t *>(blk + p * L::ROW + 4 * (((li >> 1) & 3) * L::G + g) + 2 * (li & 1)) = (uint16_t)w;
+        } else {
+            // nibble n = li / 4 % 8 of pieces l = 4 (li % 4) + e: four words that the lanes of equal li % 4 (and
+            // equal li / 32) have a nibble of each; every exchange halves what a lane still works on
+            const int n = (li >> 2) & (L::VN - 1);
+            const bool b2 = li & 4, b3 = li & 8;
+            const uint32_t s0 = code[0] << (4 * n), s1 = code[1] << (4 * n), s2 = code[2] << (4 * n), s3 = code[3] << (4 * n);
+            uint32_t w0 = (b2 ? s2 : s0) | __shfl_xor(b2 ? s0 : s2, 4), w1 = (b2 ? s3 : s1) | __shfl_xor(b2 ? s1 : s3, 4);
+            uint32_t w = (b3 ? w1 : w0) | __shfl_xor(b3 ? w0 : w1, 8);
+            if (D > 64) w |= __shfl_xor(w, 16);
+            const int l = 4 * (li & 3) + 2 * b2 + b3;
+            uint8_t *o = blk + L::v_piece(p, li >> 5, l);
+            if (on && (D == 64 || (li & 16) == 0)) {
+                if (D == 64) *reinterpret_cast<uint16_t *>(o) = (uint16_t)w;
+                else *reinterpret_cast<uint32_t *>(o) = w;
             }
-        } else if (lane < 16 * L::VW) {
-            const uint8_t *src8 = w.code + 128 * (lane >> 4) + (lane & 15);
-            uint32_t word = 0;
-#pragma unroll
-            for (int n = 0; n < L::VN; ++n) word |= (uint32_t)src8[16 * n] << (4 * n);
-            uint8_t *o = blk + L::v_piece(p, lane >> 4, lane & 15);
-            if (D == 64) *reinterpret_cast<uint16_t *>(o) = (uint16_t)word;
-            else *reinterpret_cast<uint32_t *>(o) = word;
         }
-        wave_sync();
     }
 }
 
-// One wave per (row, KV head), keys and values.
+// Keys and values of HPW heads of a row: a wave.
 template <int D>
-__global__ void __launch_bounds__(64 * WAVES) kv_read_kernel(KvCache c, KvSeqs sq, Heads ko, Heads vo) {
-    constexpr int E = D / 64;
+__global__ void __launch_bounds__(64 * WAVES) kv_read_kernel(KvCache c, KvSeqs sq, Heads ko, Heads vo, int vko, int vvo) {
+    constexpr int LPH = lanes_of(D), HPW = 64 / LPH;
     using L = KvLayout<D>;
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, li = lane & (LPH - 1);
+    const int per_row = (c.hkv + HPW - 1) / HPW;
     const int64_t unit = (int64_t)blockIdx.x * WAVES + (threadIdx.x >> 6);
-    const int64_t t64 = unit / c.hkv;
+    const int64_t t64 = unit / per_row;
     if (t64 >= sq.rows) return;
-    const int t = (int)t64, h = (int)(unit % c.hkv);
+    const int t = (int)t64, h = (int)(unit % per_row) * HPW + lane / LPH;
     const RowSeq r = row_seq(sq, t, lane);
-    if (r.s >= sq.nseq) return;
+    if (r.s >= sq.nseq || h >= c.hkv) return;
     const int64_t pos = (int64_t)sq.kv_len[r.s] - r.n + (t - r.first);
     const int page = kv_page(c, sq, r.s, pos);
     const uint8_t *blk = c.pool + ((int64_t)max(page, 0) * c.hkv + h) * 2 * L::block(c.ps_log2);
-    const int p = (int)(pos & ((1 << c.ps_log2) - 1));
+    const int p = (int)(pos & ((1 << c.ps_log2) - 1)), g = li >> 3;
     for (int kind = 0; kind < 2; ++kind, blk += L::block(c.ps_log2)) {
         const Heads &dst = kind ? vo : ko;
         if (!dst.p) continue;
+        float y[4] = {0, 0, 0, 0};
+        if (page >= 0) {
+            const float dh = (float)reinterpret_cast<const _Float16 *>(blk + L::d_off(c.ps_log2))[L::by4(p, g)];
+            const float mh =
+                (float)reinterpret_cast<const _Float16 *>(blk + L::m_off(c.ps_log2))[kind ? L::by4(p, g) : p * L::G + g];
+            uint32_t code[4];
+            if (kind == 0) {
+                const uint32_t w =
+                    *reinterpret_cast<const uint16_t *>(blk + p * L::ROW + 4 * (((li >> 1) & 3) * L::G + g) + 2 * (li & 1));
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int i = lane * E + e, g = i >> 5;
-            float y = 0.f;
-            if (page >= 0) {
-                const _Float16 dh = reinterpret_cast<const _Float16 *>(blk + L::d_off(c.ps_log2))[L::by4(p, g)];
-                const _Float16 mh =
-                    reinterpret_cast<const _Float16 *>(blk + L::m_off(c.ps_log2))[kind ? L::by4(p, g) : p * L::G + g];
-                int at, n;
-                if (kind == 0) {
-                    n = i & 7;
-                    at = p * L::ROW + 4 * (((i >> 3) & 3) * L::G + g) + (n >> 1);
-                } else {
-                    n = (i >> 4) & (L::VN - 1);
-                    at = L::v_piece(p, D == 64 ? 0 : i >> 7, i & 15) + (n >> 1);
-                }
-                const int code = (blk[at] >> (4 * (n & 1))) & 15;
-                y = fmaf((float)code, (float)dh, (float)mh);
+                for (int e = 0; e < 4; ++e) code[e] = (w >> (4 * e)) & 15u;
+            } else {
+                const int n = (li >> 2) & (L::VN - 1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    code[e] = (blk[L::v_piece(p, li >> 5, 4 * (li & 3) + e) + (n >> 1)] >> (4 * (n & 1))) & 15u;
             }
-            store_head(dst, t * dst.row + h * dst.head + (int64_t)i * dst.elem, y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = fmaf((float)code[e], dh, mh);
         }
+        store4(dst, t * dst.row + h * dst.head + 4 * li * dst.elem, kind ? vvo : vko, y);
     }
+}
+
+// Heads whose dimensions are whole pieces of 4 elements, aligned as such.
+int whole4(const Heads &x) {
+    return x.p && x.elem == 1 && x.row % 4 == 0 && x.head % 4 == 0 && ((uintptr_t)x.p & (x.f16 ? 7 : 15)) == 0;
 }
 
 }  // namespace
@@ -217,14 +306,16 @@ __global__ void __launch_bounds__(64 * WAVES) kv_read_kernel(KvCache c, KvSeqs s
 hipError_t launch_kv_rows(const KvCache *cache, const KvSeqs &seqs, const RowPrep &prep, int D, int hq, const Heads &q,
                           const Heads &qo, int hkv, const Heads &k, const Heads &v, const Heads &ko,
                           hipStream_t st) {
-    const KvCache c = cache ? *cache : KvCache{nullptr, 0, 0, D, 0};
-    const int total = hq + hkv * (cache ? 2 : 1);
-    const int per = 1, chunks = (total + per - 1) / per;
-    const int64_t blocks = ((int64_t)seqs.rows * chunks + WAVES - 1) / WAVES;
-    auto go = [&](auto kern) {
-        hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * WAVES), 0, st, c, seqs, prep, hq, q, qo, hkv, k, v,
-                           ko, cache ? 1 : 0, per, chunks);
-    };
+    const int hpw = 256 / D, gq = (hq + hpw - 1) / hpw, gk = (hkv + hpw - 1) / hpw;
+    const int total = gq + gk * (cache ? 2 : 1);
+    RowsArgs a{cache ? *cache : KvCache{nullptr, 0, 0, D, 0}, seqs, prep, hq, hkv, cache ? 1 : 0, q, qo, k, v, ko,
+               whole4(q), whole4(qo), whole4(k), whole4(v), whole4(ko), 1, 1};
+    // Few rows: a wave for every group of heads.  Many: a row's groups share
+    // the row's sines and cosines, as far as 16 waves a unit are left.
+    a.per = (int)std::max<int64_t>(1, std::min<int64_t>(total, (int64_t)seqs.rows * total / (16 * device_cus())));
+    a.chunks = (total + a.per - 1) / a.per;
+    const int64_t blocks = ((int64_t)seqs.rows * a.chunks + WAVES - 1) / WAVES;
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * WAVES), 0, st, a); };
     if (D == 64) go(kv_rows_kernel<64>);
     else if (D == 128) go(kv_rows_kernel<128>);
     else go(kv_rows_kernel<256>);
@@ -232,9 +323,10 @@ hipError_t launch_kv_rows(const KvCache *cache, const KvSeqs &seqs, const RowPre
 }
 
 hipError_t launch_kv_read(const KvCache &c, const KvSeqs &seqs, const Heads &ko, const Heads &vo, hipStream_t st) {
-    const int64_t blocks = ((int64_t)seqs.rows * c.hkv + WAVES - 1) / WAVES;
+    const int hpw = 256 / c.D;
+    const int64_t blocks = ((int64_t)seqs.rows * ((c.hkv + hpw - 1) / hpw) + WAVES - 1) / WAVES;
     auto go = [&](auto kern) {
-        hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * WAVES), 0, st, c, seqs, ko, vo);
+        hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * WAVES), 0, st, c, seqs, ko, vo, whole4(ko), whole4(vo));
     };
     if (c.D == 64) go(kv_read_kernel<64>);
     else if (c.D == 128) go(kv_read_kernel<128>);
