@@ -178,8 +178,10 @@ int log2_of(int v) {
     return n;
 }
 
-qk::Heads to_heads(const qk_heads *x) {
-    return x ? qk::Heads{x->p, x->row, x->head, x->elem, x->f16} : qk::Heads{nullptr, 0, 0, 0, 0};
+// (the stride of a dimension of size 1 says nothing: 0)
+qk::Heads to_heads(const qk_heads *x, int64_t rows, int64_t heads) {
+    if (!x) return qk::Heads{nullptr, 0, 0, 0, 0};
+    return qk::Heads{x->p, rows == 1 ? 0 : x->row, heads == 1 ? 0 : x->head, x->elem, x->f16};
 }
 qk::KvCache to_cache(const qk_kv_cache *c) {
     return qk::KvCache{(uint8_t *)c->pool, c->num_pages, c->n_kv_heads, c->head_dim, log2_of(c->page_size)};
@@ -382,8 +384,9 @@ int qk_norm_rope(const qk_rope *rope, int rows, int head_dim, int n_heads, const
     for (int i = 0; i < nin; ++i)
         if (spans_meet(sqo, in[i]) || spans_meet(sko, in[i])) return QK_EINVAL_PTR;
     const qk::KvSeqs seqs{rows, 1, 0, nullptr, nullptr, nullptr};
-    return launched(qk::launch_kv_rows(nullptr, seqs, to_prep(rope), head_dim, hq, to_heads(q), to_heads(q_out), hk,
-                                       to_heads(k), to_heads(nullptr), to_heads(k_out), (hipStream_t)stream));
+    return launched(qk::launch_kv_rows(nullptr, seqs, to_prep(rope), head_dim, hq, to_heads(q, rows, hq),
+                                       to_heads(q_out, rows, hq), hk, to_heads(k, rows, hk), to_heads(nullptr, 0, 0),
+                                       to_heads(k_out, rows, hk), (hipStream_t)stream));
 }
 
 int qk_kv_append(const qk_kv_cache *cache, const qk_kv_seqs *seqs, const qk_rope *rope, const qk_heads *k,
@@ -409,8 +412,9 @@ int qk_kv_append(const qk_kv_cache *cache, const qk_kv_seqs *seqs, const qk_rope
     if (spans_meet(pool, sq) || spans_meet(pool, sqo) || (q && !same_view(q, q_out) && spans_meet(sqo, sq)))
         return QK_EINVAL_PTR;
     const qk::KvCache c = to_cache(cache);
-    return launched(qk::launch_kv_rows(&c, to_seqs(seqs), to_prep(rope), D, hq, to_heads(q), to_heads(q_out), hk,
-                                       to_heads(k), to_heads(v), to_heads(nullptr), (hipStream_t)stream));
+    return launched(qk::launch_kv_rows(&c, to_seqs(seqs), to_prep(rope), D, hq, to_heads(q, rows, hq),
+                                       to_heads(q_out, rows, hq), hk, to_heads(k, rows, hk), to_heads(v, rows, hk),
+                                       to_heads(nullptr, 0, 0), (hipStream_t)stream));
 }
 
 int qk_kv_read(const qk_kv_cache *cache, const qk_kv_seqs *seqs, const qk_heads *k_out, const qk_heads *v_out,
@@ -429,7 +433,7 @@ int qk_kv_read(const qk_kv_cache *cache, const qk_kv_seqs *seqs, const qk_heads 
     for (int i = 0; i < nin; ++i)
         if (spans_meet(sk, in[i]) || spans_meet(sv, in[i])) return QK_EINVAL_PTR;
     if (spans_meet(sk, sv)) return QK_EINVAL_PTR;
-    return launched(qk::launch_kv_read(to_cache(cache), to_seqs(seqs), to_heads(k_out), to_heads(v_out),
+    return launched(qk::launch_kv_read(to_cache(cache), to_seqs(seqs), to_heads(k_out, rows, hk), to_heads(v_out, rows, hk),
                                        (hipStream_t)stream));
 }
 
@@ -470,7 +474,7 @@ int qk_kv_attn(const qk_kv_cache *cache, const qk_kv_seqs *seqs, int n_heads, co
     for (int i = 0; i < nin; ++i)
         if (spans_meet(so, in[i]) || spans_meet(ws, in[i])) return QK_EINVAL_PTR;
     if (spans_meet(so, ws)) return QK_EINVAL_PTR;
-    return launched(qk::launch_kv_attn(c, sqs, n_heads, to_heads(q), to_heads(out), scale, window, workspace,
+    return launched(qk::launch_kv_attn(c, sqs, n_heads, to_heads(q, rows, n_heads), to_heads(out, rows, n_heads), scale, window, workspace,
                                        (hipStream_t)stream));
 }
 
