@@ -184,10 +184,13 @@ template <int MT, bool PAIR> struct Form {
 // Waves of a workgroup.
 constexpr int waves(int D, int rt) { return D == 256 && rt == 8 ? 8 : 4; }
 
+// Waves a SIMD has to have room for.
+constexpr int occupancy(int D, int rt) { return D == 256 ? 2 : D == 128 ? (rt == 32 ? 1 : 2) : 2; }
+
 // One workgroup: a tile of query rows, one KV head, one split of the
 // positions; its waves take tiles of 32 positions in turn and join at the end.
 template <int D, int MT, bool PAIR>
-__global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), MT == 1 ? 2 : 1) kv_attn_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D, PAIR ? 8 : 16 * MT)) kv_attn_kernel(AttnArgs a) {
     using L = KvLayout<D>;
     constexpr int G = L::G, RT = Form<MT, PAIR>::RT, AW = waves(D, RT), NT = D / 16, OP = D + 4;
     constexpr int RC = PAIR ? 8 : 16;     // rows side by side in a wave's columns
@@ -363,6 +366,9 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), MT == 1 ? 2
         grow[mt] = M_NONE;
     }
 
+    float minus1 = -1.f;
+    asm("" : "+s"(minus1));
+
     // Keys of the next tile are asked for when this tile's are used up, and
     // values when this tile's are: each comes in under the other half's work.
     // A page that is not held is read as page 0 and counts for nothing; behind
@@ -461,7 +467,9 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), MT == 1 ? 2
                     const float p0 = __builtin_amdgcn_exp2f(z[mt][u][2 * k2]);
                     const float p1 = __builtin_amdgcn_exp2f(z[mt][u][2 * k2 + 1]);
                     ph[mt][u][k2] = pack(p0, p1);
-                    pl[mt][u][k2] = pack(p0 - lo_f(ph[mt][u][k2]), p1 - hi_f(ph[mt][u][k2]));
+                    // (opaque, so that the residual is one mixed fma on the packed pair and not three conversions)
+                    asm("" : "+v"(ph[mt][u][k2]));
+                    pl[mt][u][k2] = pack(fmaf(lo_f(ph[mt][u][k2]), minus1, p0), fmaf(hi_f(ph[mt][u][k2]), minus1, p1));
                 }
         }
 
