@@ -49,6 +49,11 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
     const h2 v = {(_Float16)a, (_Float16)b};
     return __builtin_bit_cast(uint32_t, v);
 }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ h2 half_pair(float v) { return h2{(_Float16)v, (_Float16)v}; }
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(h2, a), __builtin_bit_cast(h2, b), c, false);
+}
 // the value of the lane 8 columns on, in a row of 16 lanes
 __device__ __forceinline__ float row_half_swap(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 0xf, 0xf, true));
@@ -69,6 +74,21 @@ template <int N> __device__ __forceinline__ void load(uint32_t *r, const uint8_t
     }
 }
 
+// Inclusive sums over the lanes of a wave (DPP: rows of 16, then across rows).
+template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t lanes_below(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <typename T> __device__ __forceinline__ T scan(T v) {
+    auto step = [&](auto from) { v += __builtin_bit_cast(T, from(__builtin_bit_cast(uint32_t, v))); };
+    step([](uint32_t w) { return lanes_below<0x111, 0xf>(w); });
+    step([](uint32_t w) { return lanes_below<0x112, 0xf>(w); });
+    step([](uint32_t w) { return lanes_below<0x114, 0xf>(w); });
+    step([](uint32_t w) { return lanes_below<0x118, 0xf>(w); });
+    step([](uint32_t w) { return lanes_below<0x142, 0xa>(w); });
+    step([](uint32_t w) { return lanes_below<0x143, 0xc>(w); });
+    return v;
+}
+
 // Work.  Query rows of a sequence, its heads of one KV head side by side: row
 // r is token r / grp, head r % grp of the group, in tiles of RT rows.  A
 // tile's positions are cut into splits of about `chunk` tiles of 32, where
@@ -83,6 +103,7 @@ struct AttnArgs {
     int hq, grp, window;
     int target;          // items per KV head to share the work out to (0: no splits)
     int min_chunk;       // tiles of 32 positions that a split has at least
+    float per_target;    // 1 / target and a little
     int nitems;          // items per KV head at most
     float scale;
     int qvec;            // query rows are whole 16-byte pieces
@@ -120,26 +141,21 @@ template <int RT> __device__ __forceinline__ bool find_item(const AttnArgs &a, i
         return v;
     };
     const Seq head = seq(0);  // (read once where one round has them all)
-    int64_t work = (int64_t)head.tiles * head.span;
+    // the call's work in fp32, and chunk at least work / target whatever that rounds
+    float work = (float)head.tiles * (float)head.span;
     for (int s0 = 64; s0 < a.sq.nseq; s0 += 64) {
         const Seq v = seq(s0);
-        work += (int64_t)v.tiles * v.span;
+        work += (float)v.tiles * (float)v.span;
     }
-    if (a.sq.nseq > 1)
-        for (int i = 1; i < 64; i <<= 1) work += __shfl_xor(work, i);
-    else
-        work = (int64_t)__builtin_amdgcn_readfirstlane(head.tiles) * __builtin_amdgcn_readfirstlane(head.span);
-    const int chunk = a.target ? (int)max((int64_t)a.min_chunk, (work + a.target - 1) / a.target) : INT32_MAX;
+    if (a.sq.nseq > 1) work = scan(work);
+    work = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, work), a.sq.nseq > 1 ? 63 : 0));
+    const int chunk = a.target ? max(a.min_chunk, (int)fminf(work * a.per_target, 1e9f) + 1) : INT32_MAX;
     int before = 0;
     for (int s0 = 0; s0 < a.sq.nseq; s0 += 64) {
         const Seq v = s0 ? seq(s0) : head;
         const int ns = min(MAX_SPLIT, max(1, v.span / chunk + (v.span % chunk ? 1 : 0)));
         int sum = v.tiles * ns;
-        if (a.sq.nseq > 1)
-            for (int i = 1; i < 64; i <<= 1) {
-                const int up = __shfl_up(sum, i);
-                sum += lane >= i ? up : 0;
-            }
+        if (a.sq.nseq > 1) sum = scan(sum);
         int at;
         if (by_row) {
             at = want - s0;
@@ -281,19 +297,18 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
         auto dim = [&](int i) {
             return PAIR ? 32 * ((i >> 1) + hc * (G / 2)) + 16 * (i & 1) + 8 * (quad & 1) : 32 * i + 8 * quad;
         };
-        float v[G][8], mx = 0.f;
+        u4 raw[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-#pragma unroll
-            for (int n = 0; n < 8; ++n) v[i][n] = 0.f;
+            raw[i] = u4{0, 0, 0, 0};
             if (mine) {
                 if (a.qvec) {
-                    const h8 w = *reinterpret_cast<const h8 *>(src + dim(i));
-#pragma unroll
-                    for (int n = 0; n < 8; ++n) v[i][n] = (float)w[n];
+                    raw[i] = *reinterpret_cast<const u4 *>(src + dim(i));
                 } else {
+                    h8 w;
 #pragma unroll
-                    for (int n = 0; n < 8; ++n) v[i][n] = (float)src[(int64_t)(dim(i) + n) * a.q.elem];
+                    for (int n = 0; n < 8; ++n) w[n] = src[(int64_t)(dim(i) + n) * a.q.elem];
+                    raw[i] = __builtin_bit_cast(u4, w);
                 }
             }
         }
@@ -302,31 +317,42 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
             load_k(max(page, 0), x);
             load_v(max(page, 0), x);
         }
+        // row norm N: scaled by 2^e to N in [2^9, 2^10), its largest element is
+        // in [2^5, 2^10); infinite, NaN or zero rows as they are
+        float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < G; ++i)
 #pragma unroll
-            for (int n = 0; n < 8; ++n) mx = fmaxf(mx, fabsf(v[i][n]));
-        if (PAIR) mx = fmaxf(mx, __shfl_xor(mx, 8));
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        // mx * 2^e in [2^9, 2^10); infinite, NaN or zero rows as they are
-        const int e = mx > 0.f && mx < 1e30f ? 136 - (int)(__float_as_uint(mx) >> 23) : 0;
-        const float f = __uint_as_float((uint32_t)(127 + e) << 23), inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        sc2[mt] = a.scale * 1.44269504088896340736f * inv;
+            for (int k = 0; k < 4; ++k) ss = dot2(raw[i][k], raw[i][k], ss);
+        if (PAIR) ss += __shfl_xor(ss, 8);
+        ss += __shfl_xor(ss, 16);
+        ss += __shfl_xor(ss, 32);
+        const int e = ss > 0.f && ss < 1e30f ? 9 - (((int)(__float_as_uint(ss) >> 23) - 127) >> 1) : 0;
+        const float f = pow2(e);
+        sc2[mt] = a.scale * 1.44269504088896340736f * pow2(-e);
         sc1[mt] = sc2[mt] * 16777216.f;
+        const h2 f1 = half_pair(pow2(min(e, 15))), f2 = half_pair(pow2(e - min(e, 15))), f16th = half_pair(0.0625f);
+        const bool twice = __any(e > 15);  // (fp16 ends at 2^15)
         uint32_t sums[4] = {0, 0, 0, 0};
         float half = 0.f;
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             float s = 0.f;
+            uint32_t w[4];
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                v[i][n] *= f;
-                s += v[i][n];
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t two = raw[i][k];
+                s = dot2(two, 0x3c003c00u, s);
+                h2 y = __builtin_bit_cast(h2, two) * f1;
+                if (twice) y *= f2;
+                w[k] = __builtin_bit_cast(uint32_t, y);
             }
+            s *= f;
             // nibbles 0 and 4, 1 and 5, 2 and 6, 3 and 7: the odd ones' codes come 16 times too large
-            qf[mt][i] = u4{pack(v[i][0], v[i][4]), pack(v[i][1] * 0.0625f, v[i][5] * 0.0625f), pack(v[i][2], v[i][6]),
-                           pack(v[i][3] * 0.0625f, v[i][7] * 0.0625f)};
+            auto pair = [&](uint32_t x, uint32_t y, uint32_t sel) { return __builtin_amdgcn_perm(y, x, sel); };
+            auto sixteenth = [&](uint32_t x) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, x) * f16th); };
+            qf[mt][i] = u4{pair(w[0], w[2], 0x05040100u), sixteenth(pair(w[0], w[2], 0x07060302u)),
+                           pair(w[1], w[3], 0x05040100u), sixteenth(pair(w[1], w[3], 0x07060302u))};
             // the group's sum as two fp16 terms, in two quads
             if (PAIR && (i & 1) == 0) {
                 half = s;
@@ -337,8 +363,8 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
             if (!PAIR) s += __shfl_xor(s, 32);
             const _Float16 hi = (_Float16)s, lo = (_Float16)(s - (float)hi);
             const int term = PAIR ? quad & 1 : quad;
-            const _Float16 w = mine && term == 0 ? hi : mine && term == 1 ? lo : (_Float16)0.f;
-            const uint32_t bits = __builtin_bit_cast(uint16_t, w);
+            const _Float16 v = mine && term == 0 ? hi : mine && term == 1 ? lo : (_Float16)0.f;
+            const uint32_t bits = __builtin_bit_cast(uint16_t, v);
             if constexpr (PAIR) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -565,14 +591,14 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             // the group's minima term: row g of om, held by quad g / 4
-            const float mg = __shfl(om[mt][g & 3], (g >> 2) * 16 + col);
+            const float mg = __shfl(om[mt][g & 3], (g >> 2) * 16 + col) * f;
             if (PAIR && hc != g / (G / 2)) continue;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const f4 v = o[mt][2 * g + k];
-                const float s = k ? 1048576.f : 16777216.f;  // 2^20, 2^24: the codes' units
+                const float s = (k ? 1048576.f : 16777216.f) * f;  // 2^20, 2^24: the codes' units
                 *reinterpret_cast<float4 *>(mine + 32 * g + 16 * k + 4 * quad) =
-                    make_float4(fmaf(v.x, s, mg) * f, fmaf(v.y, s, mg) * f, fmaf(v.z, s, mg) * f, fmaf(v.w, s, mg) * f);
+                    make_float4(fmaf(v.x, s, mg), fmaf(v.y, s, mg), fmaf(v.z, s, mg), fmaf(v.w, s, mg));
             }
         }
         __syncthreads();
@@ -683,7 +709,8 @@ int64_t kv_attn_workspace(const KvCache &c, const KvSeqs &sq, int hq) {
 hipError_t launch_kv_attn(const KvCache &c, const KvSeqs &seqs, int hq, const Heads &q, const Heads &out, float scale,
                           int window, void *workspace, hipStream_t st) {
     const Shape s = attn_shape(c, seqs, hq);
-    AttnArgs a{c, seqs, q, out, hq, hq / c.hkv, window, s.target, s.min_chunk, s.nitems, scale, 0, nullptr, nullptr};
+    AttnArgs a{c, seqs, q, out, hq, hq / c.hkv, window, s.target, s.min_chunk,
+               s.target ? 1.0001f / s.target : 0.f, s.nitems, scale, 0, nullptr, nullptr};
     a.qvec = q.elem == 1 && q.row % 8 == 0 && q.head % 8 == 0 && ((uintptr_t)q.p & 15) == 0;
     if (s.target) {
         a.o = (float *)workspace;
