@@ -648,6 +648,15 @@ __global__ void __launch_bounds__(256) kv_attn_join_kernel(AttnArgs a) {
     const int ns = t.ns;
     auto unit = [&](int s) { return ((int64_t)(t.id0 + s) * a.c.hkv + hk) * RT + r % RT; };
     const float2 v = tid < ns ? a.ml[unit(tid)] : make_float2(M_NONE, 0.f);
+    // the first splits' outputs are asked for before their weights are known
+    constexpr int FIRST = 16;
+    float first[FIRST][E];
+#pragma unroll
+    for (int i = 0; i < FIRST; ++i) {
+        const float *p = a.o + unit(min(wave + 4 * i, ns - 1)) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) first[i][e] = p[e];
+    }
     float mx = v.x;
     for (int i = 1; i < 64; i <<= 1) mx = fmaxf(mx, __shfl_xor(mx, i));
     if (lane == 0) mx_s[wave] = mx;
@@ -655,7 +664,7 @@ __global__ void __launch_bounds__(256) kv_attn_join_kernel(AttnArgs a) {
     mx = fmaxf(fmaxf(mx_s[0], mx_s[1]), fmaxf(mx_s[2], mx_s[3]));
     const float w = __builtin_amdgcn_exp2f(v.x - mx);
     float sum = tid < ns ? w * v.y : 0.f;
-    wt[tid] = w;
+    wt[tid] = tid < ns ? w : 0.f;
     for (int i = 1; i < 64; i <<= 1) sum += __shfl_xor(sum, i);
     if (lane == 0) sum_s[wave] = sum;
     __syncthreads();
@@ -663,8 +672,14 @@ __global__ void __launch_bounds__(256) kv_attn_join_kernel(AttnArgs a) {
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < FIRST; ++i) {
+        if (wave + 4 * i >= ns) break;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(wt[wave + 4 * i], first[i][e], acc[e]);
+    }
 #pragma unroll 8
-    for (int s = wave; s < ns; s += 4) {
+    for (int s = wave + 4 * FIRST; s < ns; s += 4) {
         const float *p = a.o + unit(s) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(wt[s], p[e], acc[e]);
