@@ -281,7 +281,11 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
 
     // query rows as the second operand, scaled by a power of two per row so
     // that neither they nor their sixteenths are subnormal
-    u4 qf[MT][G], qs[MT];
+    // D = 256 in tiles of 16 rows: 32 registers too many, so from LDS
+    constexpr bool QLDS = D == 256 && !PAIR;
+    u4 *const ql = reinterpret_cast<u4 *>(red4);  // [G][64], the same for every wave
+    u4 qf[QLDS ? 1 : MT][QLDS ? 1 : G], qs[MT];
+    int qat = lane;
     float sc1[MT], sc2[MT];
     int lim[MT], low[MT];
 #pragma unroll
@@ -314,8 +318,10 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
         }
         if (mt == 0 && x < x1) {  // the first tile's loads, before the queries are waited for
             page = __builtin_amdgcn_readlane(ahead, 0);
-            load_k(max(page, 0), x);
-            load_v(max(page, 0), x);
+            if (!QLDS) {
+                load_k(max(page, 0), x);
+                load_v(max(page, 0), x);
+            }
         }
         // row norm N: scaled by 2^e to N in [2^9, 2^10), its largest element is
         // in [2^5, 2^10); infinite, NaN or zero rows as they are
@@ -351,8 +357,13 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
             // nibbles 0 and 4, 1 and 5, 2 and 6, 3 and 7: the odd ones' codes come 16 times too large
             auto pair = [&](uint32_t x, uint32_t y, uint32_t sel) { return __builtin_amdgcn_perm(y, x, sel); };
             auto sixteenth = [&](uint32_t x) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, x) * f16th); };
-            qf[mt][i] = u4{pair(w[0], w[2], 0x05040100u), sixteenth(pair(w[0], w[2], 0x07060302u)),
-                           pair(w[1], w[3], 0x05040100u), sixteenth(pair(w[1], w[3], 0x07060302u))};
+            const u4 op = u4{pair(w[0], w[2], 0x05040100u), sixteenth(pair(w[0], w[2], 0x07060302u)),
+                             pair(w[1], w[3], 0x05040100u), sixteenth(pair(w[1], w[3], 0x07060302u))};
+            if constexpr (QLDS) {
+                if (wave == 0) ql[i * 64 + lane] = op;
+            } else {
+                qf[mt][i] = op;
+            }
             // the group's sum as two fp16 terms, in two quads
             if (PAIR && (i & 1) == 0) {
                 half = s;
@@ -392,6 +403,11 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
         grow[mt] = M_NONE;
     }
 
+    if (QLDS) __syncthreads();
+    auto query = [&](int mt, int i) {
+        if constexpr (QLDS) return ql[i * 64 + qat];
+        else return qf[mt][i];
+    };
     float minus1 = -1.f;
     asm("" : "+s"(minus1));
 
@@ -406,6 +422,12 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
             nx = x + AW;
             if ((k & 63) == 0) look_ahead(nx);
             np = __builtin_amdgcn_readlane(ahead, k & 63);
+        }
+
+        if constexpr (QLDS) {
+            load_k(max(page, 0), x);
+            load_v(max(page, 0), x);
+            asm("" : "+v"(qat));  // read where they are used, not kept in registers
         }
 
         // scores
@@ -433,8 +455,8 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
                             d3 = hi_f(kd[u][2 * g + 1]);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    f4 r = mfma(ko[0], qf[mt][PAIR ? 2 * g : g], f4{0.f, 0.f, 0.f, 0.f});
-                    if constexpr (PAIR) r = mfma(ko[1], qf[mt][2 * g + 1], r);
+                    f4 r = mfma(ko[0], query(mt, PAIR ? 2 * g : g), f4{0.f, 0.f, 0.f, 0.f});
+                    if constexpr (PAIR) r = mfma(ko[1], query(mt, 2 * g + 1), r);
                     acc[mt] = f4{fmaf(d0, r.x, acc[mt].x), fmaf(d1, r.y, acc[mt].y), fmaf(d2, r.z, acc[mt].z),
                                  fmaf(d3, r.w, acc[mt].w)};
                 }
@@ -449,9 +471,11 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
                     z[mt][u][i] = y;
                 }
         }
-        __builtin_amdgcn_sched_barrier(0);
-        load_k(max(np, 0), nx);
-        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!QLDS) {
+            __builtin_amdgcn_sched_barrier(0);
+            load_k(max(np, 0), nx);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         if (!live || x * 32 < all_lo || x * 32 + 31 > all_hi) {
             const int base = x * 32 + 4 * quad;
 #pragma unroll
@@ -565,9 +589,11 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
                 }
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
-        load_v(max(np, 0), nx);
-        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!QLDS) {
+            __builtin_amdgcn_sched_barrier(0);
+            load_v(max(np, 0), nx);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         page = np;
     }
 
@@ -701,7 +727,7 @@ Shape attn_shape(const KvCache &c, const KvSeqs &sq, int hq) {
     const int grp = hq / c.hkv;
     Shape s;
     const int64_t n = sq.rows / sq.nseq, per_seq = ((int64_t)sq.rows * grp + sq.nseq - 1) / sq.nseq;
-    s.rt = per_seq <= 8 || c.D == 256 ? 8 : per_seq <= 16 ? 16 : 32;
+    s.rt = per_seq <= 8 ? 8 : per_seq < 1024 || c.D > 64 ? 16 : 32;
     const int64_t tiles = sq.q_start ? (int64_t)sq.rows * grp / s.rt + std::min(sq.nseq, sq.rows)
                                      : sq.nseq * ((n * grp + s.rt - 1) / s.rt);
     const int aw = waves(c.D, s.rt);
@@ -738,17 +764,15 @@ hipError_t launch_kv_attn(const KvCache &c, const KvSeqs &seqs, int hq, const He
         hipLaunchKernelGGL(join, dim3((unsigned)(seqs.rows * hq)), dim3(256), 0, st, a);
         return hipGetLastError();
     };
-#define QK_ATTN(D)                                                                                    \
-    if (s.rt == 8) return go(kv_attn_kernel<D, 1, true>, kv_attn_join_kernel<D, 8>);                  \
-    if (s.rt == 16) return go(kv_attn_kernel<D, 1, false>, kv_attn_join_kernel<D, 16>)
-    if (c.D == 256) return go(kv_attn_kernel<256, 1, true>, kv_attn_join_kernel<256, 8>);
-    if (c.D == 128) {
-        QK_ATTN(128);
-        return go(kv_attn_kernel<128, 2, false>, kv_attn_join_kernel<128, 32>);
-    }
-    QK_ATTN(64);
-    return go(kv_attn_kernel<64, 2, false>, kv_attn_join_kernel<64, 32>);
-#undef QK_ATTN
+    if (c.D == 256)
+        return s.rt == 8 ? go(kv_attn_kernel<256, 1, true>, kv_attn_join_kernel<256, 8>)
+                         : go(kv_attn_kernel<256, 1, false>, kv_attn_join_kernel<256, 16>);
+    if (c.D == 128)
+        return s.rt == 8 ? go(kv_attn_kernel<128, 1, true>, kv_attn_join_kernel<128, 8>)
+                         : go(kv_attn_kernel<128, 1, false>, kv_attn_join_kernel<128, 16>);
+    return s.rt == 8    ? go(kv_attn_kernel<64, 1, true>, kv_attn_join_kernel<64, 8>)
+           : s.rt == 16 ? go(kv_attn_kernel<64, 1, false>, kv_attn_join_kernel<64, 16>)
+                        : go(kv_attn_kernel<64, 2, false>, kv_attn_join_kernel<64, 32>);
 }
 
 }  // namespace qk
