@@ -38,6 +38,13 @@ typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 constexpr int MAX_SPLIT = 256;   // splits of a sequence
 constexpr float M_NONE = -3e38f; // running maximum before any visible position
+// Two codes in an fp16 pair, as they lie after a shift: code * 2^-21 (a
+// subnormal) and, 16 times that, code * 2^-17.  The sums inside a matrix
+// instruction are aligned by the operands' exponent fields, so a subnormal
+// that begins k bits below its field costs k bits of the sum: in the lowest
+// place (code * 2^-24) it was 2^-18 of the largest product, toward zero; here
+// it is 2^-21 and less.
+constexpr uint32_t EVEN = 0x00780078u, ODD = 0x07800780u;
 constexpr float GROW = 2.f;      // a probability may reach 2^GROW before the maximum is moved
 
 __device__ __forceinline__ f4 mfma(u4 a, u4 b, f4 c) {
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
         const int e = ss > 0.f && ss < 1e30f ? 9 - (((int)(__float_as_uint(ss) >> 23) - 127) >> 1) : 0;
         const float f = pow2(e);
         sc2[mt] = a.scale * 1.44269504088896340736f * pow2(-e);
-        sc1[mt] = sc2[mt] * 16777216.f;
+        sc1[mt] = sc2[mt] * 2097152.f;  // 2^21, the codes' unit
         const h2 f1 = half_pair(pow2(min(e, 15))), f2 = half_pair(pow2(e - min(e, 15))), f16th = half_pair(0.0625f);
         const bool twice = __any(e > 15);  // (fp16 ends at 2^15)
         uint32_t sums[4] = {0, 0, 0, 0};
@@ -448,8 +455,8 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
                 u4 ko[2];
 #pragma unroll
                 for (int i = 0; i < (PAIR ? 2 : 1); ++i) {
-                    const uint32_t w = kc[u][g + i * (G / 2)], w8 = w >> 8;
-                    ko[i] = u4{w & 0x000f000fu, w & 0x00f000f0u, w8 & 0x000f000fu, w8 & 0x00f000f0u};
+                    const uint32_t w = kc[u][g + i * (G / 2)], a0 = w << 3, a1 = w >> 5;
+                    ko[i] = u4{a0 & EVEN, a0 & ODD, a1 & EVEN, a1 & ODD};
                 }
                 const float d0 = lo_f(kd[u][2 * g]), d1 = hi_f(kd[u][2 * g]), d2 = lo_f(kd[u][2 * g + 1]),
                             d3 = hi_f(kd[u][2 * g + 1]);
@@ -572,13 +579,13 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
                     for (int k2 = 0; k2 < 2; ++k2) {
                         uint32_t w;
                         if constexpr (D == 64) {
-                            w = vc[u][0][k2] >> (8 * g);
+                            w = g ? vc[u][0][k2] >> 5 : vc[u][0][k2] << 3;
                         } else {
                             const uint32_t sel = 0x0c040c00u + 0x00010001u * (uint32_t)(g & 3);
-                            w = __builtin_amdgcn_perm(vc[u][g >> 2][2 * k2 + 1], vc[u][g >> 2][2 * k2], sel);
+                            w = __builtin_amdgcn_perm(vc[u][g >> 2][2 * k2 + 1], vc[u][g >> 2][2 * k2], sel) << 3;
                         }
-                        v0[2 * u + k2] = w & 0x000f000fu;
-                        v1[2 * u + k2] = w & 0x00f000f0u;
+                        v0[2 * u + k2] = w & EVEN;
+                        v1[2 * u + k2] = w & ODD;
                     }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
@@ -622,7 +629,7 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const f4 v = o[mt][2 * g + k];
-                const float s = (k ? 1048576.f : 16777216.f) * f;  // 2^20, 2^24: the codes' units
+                const float s = (k ? 131072.f : 2097152.f) * f;  // 2^17, 2^21: the codes' units
                 *reinterpret_cast<float4 *>(mine + 32 * g + 16 * k + 4 * quad) =
                     make_float4(fmaf(v.x, s, mg), fmaf(v.y, s, mg), fmaf(v.z, s, mg), fmaf(v.w, s, mg));
             }
