@@ -344,6 +344,167 @@ def test_attn_long_context():
             assert ((out[t, h] - want).abs() <= 2.0 ** -16 * (p @ vv[:end, h // 2].double().abs() + 10)).all()
 
 
+def test_attn_many_sequences():
+    """More sequences than a wave has lanes, some without rows or positions, tables far longer than they need."""
+    rng = np.random.default_rng(50)
+    nseq, D = 200, 64
+    ns = [int(x) for x in rng.integers(0, 4, nseq)]
+    kv_len = np.array([n + int(rng.integers(0, 90)) if n else 7 for n in ns], np.int32)
+    kv_len[5] = 96
+    c = kv_ref.Cache(rng, nseq, 3, 1, D, 32)
+    for s in range(0, nseq, 3):
+        c.spoil(s, int(kv_len[s]))
+    wide = np.full((nseq, 700), -1, np.int32)  # held pages, then nothing
+    wide[:, :3] = c.pages
+    wide[:, 3:] = rng.integers(0, c.num_pages, (nseq, 697))  # pages of others behind the end: never read
+    c.pages, c.held, c.mp = wide, np.ones((nseq, 700), bool), 700
+    q = rng.standard_normal((sum(ns), 3, D)).astype(np.float16)
+    check_attn(c, q, ns, kv_len, 0.125)
+    check_attn(c, q, ns, kv_len, 0.125, window=40)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attn_splits_with_windows_and_holes(D):
+    """Contexts that are shared out over workgroups, by a table of the right length and by one 30 times as long."""
+    rng = np.random.default_rng(60 + D)
+    c = kv_ref.Cache(rng, 2, 47, 1, D, 64, holes=[(0, 3, -1), (0, 20, -1), (1, 46, -1), (1, 0, -1)])
+    q = rng.standard_normal((5, 4, D)).astype(np.float16)
+    kv_len = np.array([2990, 3008], np.int32)
+    for window in (0, 1500, 70):
+        check_attn(c, q, [2, 3], kv_len, D ** -0.5, window=window)
+        check_attn(c, q[:4], [2, 2], kv_len, D ** -0.5, window=window, f32=True)
+    c.pages = np.concatenate([c.pages, np.full((2, 1400), -1, np.int32)], 1)
+    c.held = np.concatenate([c.held, np.zeros((2, 1400), bool)], 1)
+    c.mp += 1400
+    check_attn(c, q, [2, 3], kv_len, D ** -0.5, window=0)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("layout,dt", [("token", np.float16), ("column", np.float32), ("token", np.float32)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_many_rows(D, layout, dt, interleaved):
+    """Rows enough for a wave to take several heads of each: prepared alone, and appended."""
+    rng = np.random.default_rng(70 + D)
+    rows, hq, hkv, ps = 1203, 11, 5, 64
+    rope, f, (wq, wk) = make_rope(rng, D, D // 2, interleaved, True)
+    q, k, v = (rng.standard_normal((rows, h, D)).astype(dt) for h in (hq, hkv, hkv))
+    pos = np.arange(rows, dtype=np.int32) + 1000
+    qo, ko = binding.norm_rope(rope, dev(pos), strided(q, layout, dt), strided(k, layout, dt))
+    cache = binding.KVCache(20, hkv, D, ps, pool=torch.zeros(20, 2 * hkv * ps * D * 5 // 8, dtype=torch.uint8, device="cuda"))
+    pages, kv_len = dev(rng.permutation(20)[None, :19].astype(np.int32)), dev(np.array([rows], np.int32))
+    qa = binding.kv_append(cache, strided(k, layout, dt), strided(v, layout, dt), pages, kv_len, q=strided(q, layout, dt),
+                           rope=rope, positions=dev(pos))
+    rk, rv = binding.kv_read(cache, rows, pages, kv_len)
+    torch.cuda.synchronize()
+    kr = kv_ref.norm_rope(k, pos, f, interleaved, wk, 1e-5)
+    close_to_rounding(qo.cpu().numpy(), kv_ref.norm_rope(q, pos, f, interleaved, wq, 1e-5), np.float16)
+    close_to_rounding(ko.cpu().numpy(), kr, np.float16)
+    assert torch.equal(qo, qa)
+    assert np.array_equal(rk.cpu().numpy(), kv_ref.values(*kv_ref.quantise(kr.astype(np.float32))).astype(np.float32))
+    assert np.array_equal(rv.cpu().numpy(), kv_ref.values(*kv_ref.quantise(v.astype(np.float32))).astype(np.float32))
+
+
+def test_far_positions_and_wide_frequencies():
+    """Angles up to 2^31, and beyond where the exact reduction ends: still the cosine of the fp64 product."""
+    rng = np.random.default_rng(80)
+    f = np.array([1.0, 0.3, 1e-3, 123.5, 3e4, 0.0, 0.999999, 2.5e-7], np.float32)
+    rope = binding.Rope(dev(f))
+    pos = np.array([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 262139, 12345678], np.int32)
+    x = rng.standard_normal((7, 2, 64)).astype(np.float32)
+    got, _ = binding.norm_rope(rope, dev(pos), dev(x), q_out=torch.empty(7, 2, 64, device="cuda"))
+    torch.cuda.synchronize()
+    close_to_rounding(got.cpu().numpy(), kv_ref.norm_rope(x, pos, f), np.float32)
+
+
+def test_append_in_place_and_at_given_positions():
+    rng = np.random.default_rng(90)
+    D, rows = 128, 5
+    rope, f, (wq, wk) = make_rope(rng, D, 64, False, True)
+    q, k = (rng.standard_normal((rows, h, D)).astype(np.float32) for h in (6, 2))
+    pos = np.array([900, 3, 77, 5, 100000], np.int32)
+    cache = binding.KVCache(2, 2, D, 32)
+    pages, kv_len = dev(np.array([[1, 0]], np.int32)), dev(np.array([40], np.int32))
+    qd = dev(q)
+    same = binding.kv_append(cache, dev(k), dev(k), pages, kv_len, q=qd, q_out=qd, rope=rope, positions=dev(pos))
+    rk, _ = binding.kv_read(cache, rows, pages, kv_len)
+    torch.cuda.synchronize()
+    assert same is qd
+    close_to_rounding(qd.cpu().numpy(), kv_ref.norm_rope(q, pos, f, False, wq, 1e-5), np.float32)
+    kr = kv_ref.norm_rope(k, pos, f, False, wk, 1e-5).astype(np.float32)
+    assert np.array_equal(rk.cpu().numpy(), kv_ref.values(*kv_ref.quantise(kr)).astype(np.float32))
+
+
+def test_pool_beyond_four_gib():
+    """Pages whose byte offsets pass 32 bits: written, read back and attended to."""
+    rng = np.random.default_rng(100)
+    D, hkv, ps = 128, 8, 1024
+    pb = 2 * hkv * ps * D * 5 // 8  # 1.25 MiB
+    n = (1 << 32) // pb + 40
+    cache = binding.KVCache(n, hkv, D, ps)
+    cache.pool[:3] = 0
+    pages = np.array([[n - 1, 1, n - 20]], np.int32)
+    L = 2 * ps + 100
+    k, v = (rng.standard_normal((L, hkv, D)).astype(np.float32) for _ in range(2))
+    kv_len = np.array([L], np.int32)
+    binding.kv_append(cache, dev(k), dev(v), dev(pages), dev(kv_len))
+    rk, rv = binding.kv_read(cache, L, dev(pages), dev(kv_len))
+    c = kv_ref.Cache.__new__(kv_ref.Cache)
+    c.hkv, c.D, c.ps, c.mp, c.held = hkv, D, ps, 3, np.ones((1, 3), bool)
+    c.f = [tuple(np.concatenate([x, np.zeros((3 * ps - L,) + x.shape[1:], x.dtype)])[None] for x in kv_ref.quantise(t)) for t in (k, v)]
+    assert np.array_equal(rk.cpu().numpy(), c.kv()[0][0, :L].astype(np.float32))
+    assert np.array_equal(rv.cpu().numpy(), c.kv()[1][0, :L].astype(np.float32))
+    c.pages, c.num_pages = pages, n
+    q = rng.standard_normal((2, 16, D)).astype(np.float16)
+    check_attn(c, q, [2], kv_len, D ** -0.5, cache=cache)
+    assert not cache.pool[0].any() and not cache.pool[2].any()
+
+
+def test_calls_at_once():
+    """Host threads on streams of their own, each with its own workspace and cache: the bits of single calls."""
+    import threading
+    rng = np.random.default_rng(110)
+    jobs = []
+    for i, D in enumerate((64, 128, 256, 128)):
+        c = kv_ref.Cache(rng, 1, 40, 2, D, 64)
+        cache = binding.KVCache(c.num_pages, 2, D, 64, pool=dev(c.pool))
+        args = (cache, dev(rng.standard_normal((1 + i, 8, D)).astype(np.float16)), dev(c.pages), dev(np.array([2500 - i], np.int32)))
+        jobs.append((args, binding.kv_attn(*args)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        stream, (args, want) = torch.cuda.Stream(), jobs[i]
+        for _ in range(20):
+            got = binding.kv_attn(*args, stream=stream)
+            stream.synchronize()
+            if not torch.equal(got, want):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_workspace_of_the_caller():
+    rng = np.random.default_rng(120)
+    c = kv_ref.Cache(rng, 1, 40, 2, 128, 64)
+    cache = binding.KVCache(c.num_pages, 2, 128, 64, pool=dev(c.pool))
+    args = (cache, dev(rng.standard_normal((1, 8, 128)).astype(np.float16)), dev(c.pages), dev(np.array([2500], np.int32)))
+    want = binding.kv_attn(*args)
+    need = binding.qk_kv_attn_workspace_bytes(cache._c, binding._seqs_arg(1, args[2], args[3], None), 8)
+    assert need > 0
+    ws = torch.full((need + 64,), 0xff, dtype=torch.uint8, device="cuda")
+    for _ in range(2):  # whatever it held
+        assert torch.equal(binding.kv_attn(*args, workspace=ws[:need]), want)
+    torch.cuda.synchronize()
+    assert (ws[need:] == 0xff).all()
+    with pytest.raises(binding.QKError):
+        binding.kv_attn(*args, workspace=ws[: need - 16])
+
+
 # ------------------------------------------------------------------ together
 
 def test_a_layer_step_from_gemv_to_gemv():
