@@ -451,7 +451,43 @@ def device_info(torch):
             "memory_GB": round(p.total_memory / 1e9, 1), "hip": torch.version.hip}
 
 
-def run_stream(torch, launcher, warm=2, only=None, tokens=1):
+def attention_stream(torch, tensors, entries, groups, fused, context):
+    """The fused stream's launches with ("heads", (qk_kv_append arguments,
+    qk_kv_attn arguments)) behind every attention layer's q/k/v group.  The
+    token stands at position context - 1 of a filled cache: 24 query and 4 KV
+    heads of 256, 64 of them rotated, pages of 64 positions."""
+    from quant_dequant_gemv_amd import binding
+    hq, hkv, D, ps = 24, 4, 256, 64
+    n = -(-context // ps)
+    kv_len = torch.tensor([context], dtype=torch.int32, device="cuda")
+    pages = torch.randperm(n, device="cuda").int()[None].contiguous()
+    w = torch.ones(D, device="cuda")
+    rope = binding.Rope(1e7 ** (-torch.arange(32, device="cuda") / 32), q_norm=w, k_norm=w)
+    q_out = torch.empty(1, hq, D, dtype=torch.float16, device="cuda")
+    out, keep = [], [kv_len, pages, rope, q_out]
+    for step, idx in zip(fused, groups):
+        out.append(step)
+        if [entries[i]["name"] for i in idx] != ["attn_q", "attn_k", "attn_v"]:
+            continue
+        cache = binding.KVCache(n, hkv, D, ps)
+        fill = torch.randn(context, hkv, D, device="cuda")
+        binding.kv_append(cache, fill, fill, pages, kv_len)
+        q = tensors[idx[0]]["y"].view(hq, 2, D)[None, :, 0]  # (each head's gate behind it)
+        k, v = (tensors[i]["y"].view(1, hkv, D) for i in idx[1:])
+        x = tensors[idx[-1] + 1]["x"].view(1, hq, D)  # attn_output's, next in the stream
+        heads, seqs = binding._heads_arg, binding._seqs_arg(1, pages, kv_len, None)
+        need = binding.qk_kv_attn_workspace_bytes(cache._c, seqs, hq)
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+        keep += [cache, ws]
+        out.append(("heads", ((cache._c, seqs, rope.arg(D, None, 1), heads(k, "k"), heads(v, "v"), hq, heads(q, "q"),
+                               heads(q_out, "q_out")),
+                              (cache._c, seqs, hq, heads(q_out, "q_out"), heads(x, "x"), D ** -0.5, 0, ws.data_ptr(),
+                               need))))
+    out.append(("keep", keep))
+    return out
+
+
+def run_stream(torch, launcher, warm=2, only=None, tokens=1, context=32768):
     """448 GEMVs of one decode token, all weights resident, back to back on
     one stream: one launch per GEMV; one qk_gemv_batch launch per group of
     projections that read the same activations (256 launches); and the same
@@ -539,6 +575,22 @@ def run_stream(torch, launcher, warm=2, only=None, tokens=1):
     def one_token_fused_planar(st=None):
         run_fused(fused_planar, sh if st is None else st)
 
+    # the fused stream with the attention layers' own work between their
+    # projections: q and k normed and rotated, k and v appended to a 4-bit
+    # cache of `context` positions, attention into attn_output's x
+    attention = attention_stream(torch, tensors, entries, groups, fused, context) \
+        if only is not None and only.startswith("attention") else []
+
+    def one_token_attention(st=None):
+        h = sh if st is None else st
+        for kind, a in attention[:-1]:
+            if kind == "heads":
+                rc = lib.qk_kv_append(*a[0], h) or lib.qk_kv_attn(*a[1], h)
+                if rc != 0:
+                    raise binding.QKError(rc, "attention")
+            else:
+                run_fused([(kind, a)], h)
+
     # the same fused steps as one chain launch (qk_gemv_chain): one step per
     # group, a barrier between steps, each step's first weights issued before
     # its wait
@@ -623,11 +675,13 @@ def run_stream(torch, launcher, warm=2, only=None, tokens=1):
         # one variant, `tokens` tokens back to back after a warm-up (for a
         # kernel trace: the last tokens * launches dispatches are the timed ones)
         fns = {"launches": one_token, "batched": one_token_batched, "fused": one_token_fused,
-               "fused_planar": one_token_fused_planar, "chain": chain_token("chain"),
+               "fused_planar": one_token_fused_planar, "attention": one_token_attention, "chain": chain_token("chain"),
                "chain_planar": chain_token("chain_planar")}
         graph = only.endswith("_graph")
         fn = fns[only[:-6] if graph else only]
         launches = len(entries) if fn is one_token else 2 if only.startswith("chain") else len(groups)
+        if fn is one_token_attention:
+            launches += 3 * sum(kind == "heads" for kind, _ in attention)
         if graph:
             s2 = torch.cuda.Stream()
             gr = torch.cuda.CUDAGraph()
@@ -652,7 +706,8 @@ def run_stream(torch, launcher, warm=2, only=None, tokens=1):
         b.record(stream)
         torch.cuda.synchronize()
         sp = a.elapsed_time(b) * 1e-3 / tokens
-        return {"variant": only, "tokens": tokens, "launches_per_token": launches, "warm_tokens": warm,
+        more = {"context": context} if fn is one_token_attention else {}
+        return {"variant": only, **more, "tokens": tokens, "launches_per_token": launches, "warm_tokens": warm,
                 "token_ms": round(sp * 1e3, 4), "tok_s": round(1 / sp, 2)}
 
     span = spans_of(one_token)
@@ -693,10 +748,12 @@ def main():
     ap.add_argument("--no-cpu", action="store_true", help="skip the CPU oracle baseline")
     ap.add_argument("--stream-only", metavar="VARIANT",
                     choices=["launches", "launches_graph", "batched", "batched_graph", "fused", "fused_graph",
-                             "fused_planar", "fused_planar_graph", "chain", "chain_planar"],
+                             "fused_planar", "fused_planar_graph", "attention", "attention_graph", "chain",
+                             "chain_planar"],
                     help="only time this decode-stream variant for --tokens tokens (for a kernel trace); "
                          "prints its own JSON line instead of the benchmark's")
     ap.add_argument("--tokens", type=int, default=5)
+    ap.add_argument("--context", type=int, default=32768, help="cache positions of the attention variants")
     args = ap.parse_args()
 
     if args.gpus != 1 or int(os.environ.get("WORLD_SIZE", "1")) != 1:
@@ -712,7 +769,7 @@ def main():
         sys.exit(1)
     launcher = Launcher()
     if args.stream_only:
-        r = run_stream(torch, launcher, only=args.stream_only, tokens=args.tokens)
+        r = run_stream(torch, launcher, only=args.stream_only, tokens=args.tokens, context=args.context)
         r["device"] = device_info(torch)
         print(json.dumps(r))
         return
