@@ -229,8 +229,14 @@ __global__ void __launch_bounds__(64 * WAVES) kv_rows_kernel(RowsArgs a) {
                 }
             }
         }
-        for (int gi = ga; gi < gb; ++gi, h += HPW) {
-            if (gi + 1 < gb) fetch(h + HPW, nf, no);
+        double wd[4], wod[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            wd[e] = w[e];
+            wod[e] = wo[e];
+        }
+        // work on the heads in f and fo
+        auto one = [&](float *f, float *fo) {
             const bool on = h < count;
             if constexpr (kind < 2) {
                 double x[4], y[4];
@@ -246,21 +252,20 @@ __global__ void __launch_bounds__(64 * WAVES) kv_rows_kernel(RowsArgs a) {
                     const double r = rsqrt(head_sum<LPH>(ss) * (1.0 / D) + (double)rp.eps);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        x[e] *= r * (double)w[e];
-                        if (apart) y[e] *= r * (double)wo[e];
+                        x[e] *= r * wd[e];
+                        if (apart) y[e] *= r * wod[e];
                     }
                 }
-                if (half) {
+                if (turn) {
+                    double z[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const double o = apart ? y[e] : VEC || i0 + (e | 1) < rp.rot_dim ? x[e ^ 1] : 0.0;
-                        const double z = fma(o, sn[e], x[e] * cs[e]);
-                        f[e] = (float)((VEC ? turn : i0 + e < rp.rot_dim) ? z : x[e]);
-                    }
-                } else {
+                    for (int e = 0; e < 4; ++e) z[e] = fma(apart ? y[e] : x[e ^ 1], sn[e], x[e] * cs[e]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) f[e] = (float)x[e];
+                    for (int e = 0; e < 4; ++e)
+                        if (VEC || i0 + e < rp.rot_dim) x[e] = z[e];
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = (float)x[e];
             }
             if (!into) {
                 if (on) store4<VEC>(at(dst, t, h, i0), dst.elem, dst.f16, f);
@@ -316,11 +321,15 @@ __global__ void __launch_bounds__(64 * WAVES) kv_rows_kernel(RowsArgs a) {
                     }
                 }
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                f[e] = nf[e];
-                fo[e] = no[e];
-            }
+        };
+        for (int gi = ga; gi < gb; gi += 2) {
+            if (gi + 1 < gb) fetch(h + HPW, nf, no);
+            one(f, fo);
+            h += HPW;
+            if (gi + 1 >= gb) break;
+            if (gi + 2 < gb) fetch(h + HPW, f, fo);
+            one(nf, no);
+            h += HPW;
         }
     };
     heads(std::integral_constant<int, 0>{}, a.q, a.qo, a.hq, 0, gq);
