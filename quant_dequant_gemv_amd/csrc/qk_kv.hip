@@ -9,7 +9,7 @@
 #include "qk_kv.h"
 
 namespace qk {
-namespace {
+namespace rows {
 
 constexpr int WAVES = 4;
 
@@ -388,7 +388,9 @@ bool whole4(const Heads &x) {
     return x.p && x.elem == 1 && x.row % 4 == 0 && x.head % 4 == 0 && ((uintptr_t)x.p & (x.f16 ? 7 : 15)) == 0;
 }
 
-}  // namespace
+}  // namespace rows
+
+using namespace rows;
 
 hipError_t launch_kv_rows(const KvCache *cache, const KvSeqs &seqs, const RowPrep &prep, int D, int hq, const Heads &q,
                           const Heads &qo, int hkv, const Heads &k, const Heads &v, const Heads &ko,

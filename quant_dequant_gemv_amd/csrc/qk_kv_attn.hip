@@ -28,7 +28,7 @@
 #include "qk_kv.h"
 
 namespace qk {
-namespace {
+namespace attn {
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
@@ -747,7 +747,9 @@ Shape attn_shape(const KvCache &c, const KvSeqs &sq, int hq) {
     return s;
 }
 
-}  // namespace
+}  // namespace attn
+
+using namespace attn;
 
 int64_t kv_attn_workspace(const KvCache &c, const KvSeqs &sq, int hq) {
     const Shape s = attn_shape(c, sq, hq);
