@@ -372,7 +372,8 @@ int qk_repack(int type, const void *W, void *Wp, int64_t N, int64_t K, void *str
  * y of a GEMV with N = heads*D rows and ncols columns, a row of q per column:
  * {y, 1, D*ncols, ncols, 0}.  Elements of an output must not coincide: sorted
  * by stride, each stride covers the extent of the smaller ones
- * (QK_EINVAL_SHAPE).
+ * (QK_EINVAL_SHAPE).  rows x heads (of all views of a call together) is at
+ * most 2^25.
  */
 typedef struct qk_heads {
     void *p;
@@ -506,9 +507,10 @@ int qk_kv_read(const qk_kv_cache *cache, const qk_kv_seqs *seqs, const qk_heads 
  *
  *   n_heads    query heads, a multiple of n_kv_heads, at most 4096
  *   q          rows x n_heads x D, fp16 (QK_EINVAL_TYPE otherwise)
- *   out        rows x n_heads x D, fp16 or fp32; the x of the next GEMV is
- *              {x, 1, D*ncols, ncols, 1}
- *   scale      finite
+ *   out        rows x n_heads x D, fp16 or fp32, overlapping nothing the
+ *              call reads; the x of the next GEMV is {x, 1, D*ncols, ncols, 1}
+ *   scale      |scale| <= 2^64
+ *   window     >= 0; 0: none
  *   workspace  qk_kv_attn_workspace_bytes bytes (16-byte aligned; NULL when
  *              that is 0), for this call until it has run: calls that may
  *              overlap, captured ones among them, need workspaces of their own

@@ -195,7 +195,7 @@ qk::RowPrep to_prep(const qk_rope *r) {
 }
 
 constexpr int MAX_HEADS = 4096;
-constexpr int64_t MAX_ROW_HEADS = (int64_t)1 << 30;  // rows x heads of one launch
+constexpr int64_t MAX_ROW_HEADS = (int64_t)1 << 25;  // rows x heads of one launch (a grid of 2^32 threads)
 
 }  // namespace
 
@@ -454,7 +454,7 @@ int qk_kv_attn(const qk_kv_cache *cache, const qk_kv_seqs *seqs, int n_heads, co
                float scale, int window, void *workspace, int64_t workspace_bytes, void *stream) {
     int rc = check_attn(cache, seqs, n_heads);
     if (rc) return rc;
-    if (!isfinite(scale) || window < 0) return QK_EINVAL_SHAPE;
+    if (!(fabsf(scale) <= 0x1p64f) || window < 0) return QK_EINVAL_SHAPE;
     if (!q || !out) return QK_EINVAL_PTR;
     if (q->f16 != 1) return QK_EINVAL_TYPE;
     const int rows = seqs->rows, D = cache->head_dim;
@@ -492,7 +492,7 @@ const char *qk_strerror(int code) {
                "qk_gemv_chain_noalloc at most QK_CHAIN_NOALLOC_MAX_STEPS (4094) steps; the attention side needs "
                "head_dim 64, 128 or 256, page_size a power of two in 32..1024, rows a multiple of nseq without q_start, "
                "rot_dim even and at most head_dim, query heads a multiple of the KV heads, strides >= 0 and outputs "
-               "whose elements do not coincide, a finite scale, a window >= 0, a workspace of "
+               "whose elements do not coincide, at most 2^25 rows x heads, |scale| <= 2^64, a window >= 0, a workspace of "
                "qk_kv_attn_workspace_bytes";
     case QK_EINVAL_PTR:
         return "invalid pointer: NULL, or W/x not 16-byte aligned, or y/out/residual not 4-byte aligned (fp16 y: 2), "

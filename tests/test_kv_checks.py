@@ -113,6 +113,9 @@ def test_attn_arguments():
         assert b.qk_kv_attn_workspace_bytes(c, s, n) == -1
     assert b.qk_kv_attn(c, s, 4, q, o, float("inf"), 0, 20 * M, 1 << 40) == SHAPE
     assert b.qk_kv_attn(c, s, 4, q, o, float("nan"), 0, 20 * M, 1 << 40) == SHAPE
+    assert b.qk_kv_attn(c, s, 4, q, o, -2.0 ** 65, 0, 20 * M, 1 << 40) == SHAPE
+    big = seqs(rows=1 << 22, nseq=1, q_start=None)
+    assert b.qk_kv_attn(c, big, 16, heads(1, 2048, 128, 1, 1), heads(8, 2048, 128), 1.0, 0, 200 * M, 1 << 40) == SHAPE
     assert b.qk_kv_attn(c, s, 4, q, o, 1.0, -1, 20 * M, 1 << 40) == SHAPE
     # out over the queries, the pool, the tables
     for at in (1 * M + 4, 10 * M + 64, 11 * M, 12 * M + 4, 13 * M + 28):
