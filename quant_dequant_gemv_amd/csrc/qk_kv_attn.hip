@@ -331,7 +331,8 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
             }
         }
         // row norm N: scaled by 2^e to N in [2^9, 2^10), its largest element is
-        // in [2^5, 2^10); infinite, NaN or zero rows as they are
+        // in [2^5, 2^10) (2^3 less in rows below 2^-21); infinite, NaN or zero
+        // rows as they are
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < G; ++i)
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
         if (PAIR) ss += __shfl_xor(ss, 8);
         ss += __shfl_xor(ss, 16);
         ss += __shfl_xor(ss, 32);
-        const int e = ss > 0.f && ss < 1e30f ? 9 - (((int)(__float_as_uint(ss) >> 23) - 127) >> 1) : 0;
+        const int e = ss > 0.f && ss < 1e30f ? min(9 - (((int)(__float_as_uint(ss) >> 23) - 127) >> 1), 30) : 0;
         const float f = pow2(e);
         sc2[mt] = a.scale * 1.44269504088896340736f * pow2(-e);
         sc1[mt] = sc2[mt] * 2097152.f;  // 2^21, the codes' unit

@@ -300,12 +300,14 @@ def test_attn_lengths_past_the_table():
 
 
 @pytest.mark.parametrize("qs,vs,scale", [(1e-3, 1, 1.0), (300.0, 1, 1e-3), (1.0, 1e4, 0.01), (1.0, 1e-3, 0.06),
-                                         (1.0, 1.0, -0.06), (1.0, 1.0, 0.0), (6e4, 1.0, 1e-6), (1.0, 1.0, 3.0)])
+                                         (1.0, 1.0, -0.06), (1.0, 1.0, 0.0), (6e4, 1.0, 1e-6), (1.0, 1.0, 3.0),
+                                         (1e-6, 1.0, 1e5), (6e-8, 1.0, 1e6), (3e-5, 1.0, 3e3)])
 def test_attn_ranges(qs, vs, scale):
     rng = np.random.default_rng(4)
     c = kv_ref.Cache(rng, 1, 5, 1, 128, 64, scale=vs)
     q = np.clip(rng.standard_normal((2, 4, 128)) * qs, -65504, 65504).astype(np.float16)
     check_attn(c, q, [2], np.array([300], np.int32), scale / max(vs, 1), f32=True)
+    check_attn(c, np.tile(q, (1, 4, 1)), [2], np.array([300], np.int32), scale / max(vs, 1), f32=True)
 
 
 def test_attn_non_finite_queries_stay_in_their_rows():
