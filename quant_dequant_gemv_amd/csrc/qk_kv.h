@@ -28,24 +28,34 @@ template <int D> struct KvLayout {
 
 __device__ __forceinline__ int clamp_row(const KvSeqs &q, int v) { return min(max(v, 0), q.rows); }
 
+// How many of the first n indices hold, `holds` being true up to one of them
+// and false from there on: 64 places at a time, so one load deep up to 64 and
+// three up to 2^18.  One wave, every lane gets the same answer (in 0..n
+// whatever `holds` says).
+template <typename F> __device__ __forceinline__ int count_while(int n, int lane, F holds) {
+    int lo = 0;
+    while (n > 64) {
+        const int step = (n + 63) >> 6;
+        const int c = __popcll(__ballot(lane * step < n && holds(lo + min(lane * step, n - 1))));
+        if (!c) return lo;
+        lo += (c - 1) * step;
+        n = min(step, n - (c - 1) * step);
+    }
+    return lo + __popcll(__ballot(lane < n && holds(lo + min(lane, n - 1))));
+}
+
 // Sequence of row t (nseq where it belongs to none) and its first row and row
-// count; one wave, every lane gets the same answer.  The starts are compared
-// 64 at a time: the number of starts at or before t is the sequence's place.
+// count; one wave, uniform.
 struct RowSeq { int s, first, n; };
 __device__ __forceinline__ RowSeq row_seq(const KvSeqs &q, int t, int lane) {
     if (!q.q_start) {
         const int n = q.rows / q.nseq;
         return {t / n, t / n * n, n};
     }
-    int cnt = 0;
-    for (int b = 0; b <= q.nseq; b += 64) {
-        const int i = b + lane;
-        cnt += __popcll(__ballot(i <= q.nseq && q.q_start[min(i, q.nseq)] <= t));
-    }
-    const int s = cnt - 1;
-    if (s < 0 || s >= q.nseq) return {q.nseq, 0, 0};
+    const int s = __builtin_amdgcn_readfirstlane(count_while(q.nseq, lane, [&](int i) { return q.q_start[i] <= t; })) - 1;
+    if (s < 0) return {q.nseq, 0, 0};
     const int first = clamp_row(q, q.q_start[s]), end = clamp_row(q, q.q_start[s + 1]);
-    if (t < first || t >= end) return {q.nseq, 0, 0};  // only for starts that decrease
+    if (t < first || t >= end) return {q.nseq, 0, 0};  // behind the last sequence (or starts that decrease)
     return {s, first, end - first};
 }
 

@@ -100,9 +100,12 @@ template <typename T> __device__ __forceinline__ T scan(T v) {
 // r is token r / grp, head r % grp of the group, in tiles of RT rows.  A
 // tile's positions are cut into splits of about `chunk` tiles of 32, where
 // chunk shares the whole call's work out over the compute units -- from the
-// lengths themselves (at most one split more a tile), so neither a page table made for longer contexts nor a
-// batch of unlike lengths leaves units idle.  A work item is one (tile,
-// split); a sequence's items follow those of the sequences before it.
+// lengths themselves, so neither a page table made for longer contexts nor a
+// batch of unlike lengths leaves units idle (48 sequences of 1..16384
+// positions: 93 us with splits cut by the table's length, 48 with this).  A work item is one
+// (tile, split); a sequence's items follow those of the sequences before it,
+// which every workgroup sums up for itself.  Where tiles alone fill the card
+// (target 0) nothing is split and a tile's number says where it is.
 struct AttnArgs {
     KvCache c;
     KvSeqs sq;
@@ -127,6 +130,31 @@ struct Item {
 // otherwise the item number `want`.  false: there is none.
 template <int RT> __device__ __forceinline__ bool find_item(const AttnArgs &a, int want, bool by_row, int j, int lane,
                                                             Item &it) {
+    if (!a.target) {
+        // a sequence's tiles are numbered from first * grp / RT + min(s, first)
+        // on, a place of its own for each without a sum: the quotient and the
+        // 1 that a sequence with rows adds cover its tiles, and empty ones,
+        // however many, stay within rows * grp / RT + min(nseq, rows)
+        if (!a.sq.q_start) {
+            it.n = a.sq.rows / a.sq.nseq;
+            const int per = (it.n * a.grp + RT - 1) / RT;
+            it.s = __builtin_amdgcn_readfirstlane(want / per);
+            it.j = want - it.s * per;
+            it.first = it.s * it.n;
+        } else {
+            auto base_of = [&](int s, int first) { return (int)((int64_t)first * a.grp / RT) + min(s, first); };
+            auto base = [&](int s) { return base_of(s, clamp_row(a.sq, a.sq.q_start[s])); };
+            it.s = __builtin_amdgcn_readfirstlane(count_while(a.sq.nseq, lane, [&](int s) { return base(s) <= want; })) - 1;
+            if (it.s < 0) return false;
+            it.first = __builtin_amdgcn_readfirstlane(clamp_row(a.sq, a.sq.q_start[it.s]));
+            it.n = __builtin_amdgcn_readfirstlane(clamp_row(a.sq, a.sq.q_start[it.s + 1])) - it.first;
+            it.j = want - base_of(it.s, it.first);
+        }
+        it.len = __builtin_amdgcn_readfirstlane(a.sq.kv_len[it.s]);
+        it.split = it.id0 = 0;
+        it.ns = 1;
+        return it.n > 0 && it.j >= 0 && (int64_t)it.j * RT < (int64_t)it.n * a.grp;
+    }
     struct Seq { int first, n, len, tiles, span; };
     const int even = a.sq.q_start ? 0 : a.sq.rows / a.sq.nseq;
     auto seq = [&](int s0) {
@@ -156,7 +184,7 @@ template <int RT> __device__ __forceinline__ bool find_item(const AttnArgs &a, i
     }
     if (a.sq.nseq > 1) work = scan(work);
     work = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, work), a.sq.nseq > 1 ? 63 : 0));
-    const int chunk = a.target ? max(a.min_chunk, (int)fminf(work * a.per_target, 1e9f) + 1) : INT32_MAX;
+    const int chunk = max(a.min_chunk, (int)fminf(work * a.per_target, 1e9f) + 1);
     int before = 0;
     for (int s0 = 0; s0 < a.sq.nseq; s0 += 64) {
         const Seq v = s0 ? seq(s0) : head;
@@ -207,13 +235,11 @@ template <int MT, bool PAIR> struct Form {
 // Waves of a workgroup.
 constexpr int waves(int D, int rt) { return D == 256 && rt == 8 ? 8 : 4; }
 
-// Waves a SIMD has to have room for.
-constexpr int occupancy(int D, int rt) { return D == 256 ? 2 : D == 128 ? (rt == 32 ? 1 : 2) : 2; }
-
 // One workgroup: a tile of query rows, one KV head, one split of the
 // positions; its waves take tiles of 32 positions in turn and join at the end.
 template <int D, int MT, bool PAIR>
-__global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D, PAIR ? 8 : 16 * MT)) kv_attn_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(64 * waves(D, Form<MT, PAIR>::RT), 2)
+kv_attn_kernel(AttnArgs a) {
     using L = KvLayout<D>;
     constexpr int G = L::G, RT = Form<MT, PAIR>::RT, AW = waves(D, RT), NT = D / 16, OP = D + 4;
     constexpr int RC = PAIR ? 8 : 16;     // rows side by side in a wave's columns
@@ -228,6 +254,8 @@ __global__ void __launch_bounds__(64 * waves(D, PAIR ? 8 : 16 * MT), occupancy(D
     const int hk = blockIdx.x % a.c.hkv, bs = blockIdx.x / a.c.hkv;
     Item t;
     if (!find_item<RT>(a, bs, false, 0, lane, t)) return;
+    // scalar registers, also where both ways of finding an item meet (else 20 vector registers more)
+    for (int *f : {&t.s, &t.j, &t.split, &t.ns, &t.first, &t.n, &t.len, &t.id0}) *f = __builtin_amdgcn_readfirstlane(*f);
     const int R = t.n * a.grp;
     const int64_t cap = (int64_t)a.sq.max_pages << a.c.ps_log2;
     // positions of the tile's first and last row, and the split's tiles of 32
@@ -727,7 +755,15 @@ __global__ void __launch_bounds__(256) kv_attn_join_kernel(AttnArgs a) {
     }
 }
 
-// Launch shape: from sizes alone (the lengths are on the device).
+// Launch shape: from sizes alone (the lengths are on the device).  Rows of a
+// sequence by its heads of a KV head decide the tile: up to 8 the pair form;
+// beyond, 16 (a form of 32 shares the unpacking of more rows but leaves one
+// wave a SIMD at D = 128: 235 us against 195 at 509 rows x 4 heads, 8200
+// positions), and 32 only for D = 64 and many rows (108 us against 129 at
+// 2036, 56 against 52 at 512).  Workgroups of 8 waves where two waves fill a
+// SIMD's registers (D = 256, pairs), else 4: fewer splits to join, against
+// more of them to hide each other's start (48 sequences of 1..16384 positions,
+// D = 128: 50 us with 4, 93 with 8; 1 token over 32773, D = 256: 24 and 21).
 struct Shape {
     int rt, target, min_chunk, nitems;
 };
@@ -743,7 +779,12 @@ Shape attn_shape(const KvCache &c, const KvSeqs &sq, int hq) {
     const int64_t most = ((int64_t)sq.max_pages << c.ps_log2) / 32;  // tiles of 32 positions
     const int64_t slots = (int64_t)device_cus() * (c.D == 256 ? 8 : 12) / aw;  // workgroups that fit at once
     const int64_t share = slots * (sq.nseq > 1 ? 2 : 1) / c.hkv - tiles;
-    s.target = most > s.min_chunk && share > tiles ? (int)share : 0;
+    // Every workgroup sums over all sequences, 0.03..0.045 us each; a context
+    // in one piece takes 0.25 us a tile of 32 (D = 128, 8 KV heads; 1024
+    // sequences, most of them without rows, tables of 8192 positions: 38 us
+    // shared against 63 with one live sequence, 75 against 65 with 16; 8192
+    // sequences: 236 against 64; tables of 131072: 63 against 895)
+    s.target = most > s.min_chunk && share > tiles && sq.nseq <= 4 * most ? (int)share : 0;
     s.nitems = (int)(tiles + s.target);
     return s;
 }

@@ -365,6 +365,53 @@ def test_attn_many_sequences():
     check_attn(c, q, ns, kv_len, 0.125, window=40)
 
 
+def test_more_sequences_than_are_shared_out():
+    """A batch so wide that no context is split, ragged and even, with empty sequences: append and attention."""
+    rng = np.random.default_rng(51)
+    D, ps, hkv = 64, 32, 1
+    for even in (False, True):
+        nseq = 5000
+        ns = [1] * nseq if even else [int(x) for x in (rng.random(nseq) < 0.3) * rng.integers(1, 4, nseq)]
+        rows = sum(ns)
+        kv_len = np.array([n + int(rng.integers(0, 9)) for n in ns], np.int32)
+        table = np.zeros((nseq, 12), np.int32)
+        table[:, 0] = rng.permutation(nseq)
+        pool = torch.zeros(nseq, 2 * hkv * ps * 40, dtype=torch.uint8, device="cuda")
+        cache = binding.KVCache(nseq, hkv, D, ps, pool=pool)
+        q_start = None if even else dev(np.concatenate([[0], np.cumsum(ns)]).astype(np.int32))
+        k, v = (rng.standard_normal((rows, hkv, D)).astype(np.float32) for _ in range(2))
+        q = rng.standard_normal((rows, 2, D)).astype(np.float16)
+        binding.kv_append(cache, dev(k), dev(v), dev(table), dev(kv_len), q_start=q_start)
+        out = binding.kv_attn(cache, dev(q), dev(table), dev(kv_len), q_start=q_start, out=torch.empty(rows, 2, D, device="cuda"))
+        torch.cuda.synchronize()
+        where = rows_of(ns)
+        fk, fv = kv_ref.quantise(k), kv_ref.quantise(v)
+        first = np.concatenate([[0], np.cumsum(ns)])
+        for t in rng.choice(rows, 60, replace=False):
+            s, i, n = where[t]
+            old = int(kv_len[s]) - n  # positions that hold zeros, then this call's rows
+            c = kv_ref.Cache.__new__(kv_ref.Cache)
+            c.hkv, c.D, c.ps, c.mp, c.held = hkv, D, old + n, 1, np.ones((1, 1), bool)
+            c.f = [tuple(np.concatenate([np.zeros((old,) + x.shape[1:], x.dtype), x[first[s]:first[s] + n]])[None] for x in f)
+                   for f in (fk, fv)]
+            want, mass, amax = kv_ref.attention(c, q[t:t + 1], [(0, i, n)], [old + n], 0.125)
+            assert (np.abs(out[t].cpu().numpy() - want[0]) <= kv_ref.attention_bound(want, mass, amax, False)[0]).all()
+
+
+@pytest.mark.parametrize("nseq", [79, 80, 81, 130])
+def test_few_live_sequences_among_many(nseq):
+    """Contexts shared out over workgroups and, from a few sequences more on, one piece each; most sequences have no rows."""
+    rng = np.random.default_rng(52)
+    c = kv_ref.Cache(rng, nseq, 20, 1, 64, 32)
+    ns = [0] * nseq
+    ns[0], ns[nseq // 2], ns[nseq - 1] = 2, 1, 3
+    kv_len = np.where(np.array(ns) > 0, 640, rng.integers(0, 640, nseq)).astype(np.int32)
+    kv_len[nseq // 2] = 97
+    q = rng.standard_normal((6, 3, 64)).astype(np.float16)
+    for window in (0, 100):
+        check_attn(c, q, ns, kv_len, 0.125, window=window, f32=True)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attn_splits_with_windows_and_holes(D):
     """Contexts that are shared out over workgroups, by a table of the right length and by one 30 times as long."""
