@@ -510,6 +510,7 @@ int qk_kv_read(const qk_kv_cache *cache, const qk_kv_seqs *seqs, const qk_heads 
  *   out        rows x n_heads x D, fp16 or fp32, overlapping nothing the
  *              call reads; the x of the next GEMV is {x, 1, D*ncols, ncols, 1}
  *   scale      |scale| <= 2^64
+ *   min(rows, nseq) x n_kv_heads is at most 2^21
  *   window     >= 0; 0: none
  *   workspace  qk_kv_attn_workspace_bytes bytes (16-byte aligned; NULL when
  *              that is 0), for this call until it has run: calls that may

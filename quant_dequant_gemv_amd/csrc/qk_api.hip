@@ -195,7 +195,11 @@ qk::RowPrep to_prep(const qk_rope *r) {
 }
 
 constexpr int MAX_HEADS = 4096;
-constexpr int64_t MAX_ROW_HEADS = (int64_t)1 << 25;  // rows x heads of one launch (a grid of 2^32 threads)
+// Grids stay below 2^32 threads: rows of heads take a wave each at most; an
+// attention tile has 8 row-heads or more but for a sequence's last, and at most
+// 512 threads.
+constexpr int64_t MAX_ROW_HEADS = (int64_t)1 << 25;
+constexpr int64_t MAX_SEQ_HEADS = (int64_t)1 << 21;  // sequences with rows x KV heads (attention)
 
 }  // namespace
 
@@ -442,6 +446,8 @@ static int check_attn(const qk_kv_cache *cache, const qk_kv_seqs *seqs, int n_he
     if (rc) return rc;
     if (n_heads < 1 || n_heads > MAX_HEADS || n_heads % cache->n_kv_heads) return QK_EINVAL_SHAPE;
     if ((int64_t)seqs->rows * n_heads > MAX_ROW_HEADS) return QK_EINVAL_SHAPE;
+    if ((int64_t)(seqs->rows < seqs->nseq ? seqs->rows : seqs->nseq) * cache->n_kv_heads > MAX_SEQ_HEADS)
+        return QK_EINVAL_SHAPE;
     return QK_OK;
 }
 
@@ -492,7 +498,7 @@ const char *qk_strerror(int code) {
                "qk_gemv_chain_noalloc at most QK_CHAIN_NOALLOC_MAX_STEPS (4094) steps; the attention side needs "
                "head_dim 64, 128 or 256, page_size a power of two in 32..1024, rows a multiple of nseq without q_start, "
                "rot_dim even and at most head_dim, query heads a multiple of the KV heads, strides >= 0 and outputs "
-               "whose elements do not coincide, at most 2^25 rows x heads, |scale| <= 2^64, a window >= 0, a workspace of "
+               "whose elements do not coincide, at most 2^25 rows x heads and 2^21 sequences x KV heads, |scale| <= 2^64, a window >= 0, a workspace of "
                "qk_kv_attn_workspace_bytes";
     case QK_EINVAL_PTR:
         return "invalid pointer: NULL, or W/x not 16-byte aligned, or y/out/residual not 4-byte aligned (fp16 y: 2), "

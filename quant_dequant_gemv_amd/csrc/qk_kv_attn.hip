@@ -3,10 +3,10 @@
 // Mathematics.  With K_ji = d_jg c_ji + m_jg (g = i / 32), the score of a
 // query row is sum_g d_jg (sum_{i in g} q_i c_ji) + sum_g m_jg (sum_{i in g}
 // q_i).  A group's inner sum is one 16x16x32 matrix instruction of 16
-// positions by 16 query rows on exact operands: a nibble masked in place is
-// an fp16 subnormal, code * 2^-24 (or 16 times that for the odd nibbles,
-// whose queries carry 1/16), so unpacking is five bit operations for eight
-// codes and nothing is converted or rounded.  The step d is one fp32 fma per
+// positions by 16 query rows on exact operands: a nibble shifted and masked is
+// an fp16 subnormal, code * 2^-21 (or 16 times that for the odd nibbles,
+// whose queries carry 1/16), so a pair of codes costs a shift and a mask at
+// most and nothing is converted or rounded.  The step d is one fp32 fma per
 // result.  The minima's term is one more instruction for all groups, the
 // queries' group sums as two fp16 terms.
 // The values likewise: O_i = sum_j (p_j d_jg) c_ji + sum_j p_j m_jg, where
@@ -19,7 +19,19 @@
 // lane are the operand of the second product as they are (slot j of quad a
 // is position 16 (j / 4) + 4 a + j % 4 of a tile of 32), and the softmax
 // statistics are one scalar per lane.  The page layout is made for this:
-// every operand is whole 16-byte pieces of the page, nothing passes LDS.
+// the cache's bytes go from whole pieces in memory to operands in registers;
+// LDS holds the queries where registers do not (D = 256, tiles of 16 rows) and
+// joins the waves at the end.
+//
+// Bounds and figures (device time in a graph, of the floor that the bytes set
+// at 5.1 TB/s or the products at 1150 TFLOP/s):
+// - D = 256, 24 heads on 4, 1 token: 262139 positions 74 us, 336 MB, floor 66:
+//   memory.  32773 positions 21 us, floor 8: start, one round trip a tile and
+//   the joining launch (4 us).
+// - D = 128, 48 sequences of 1..16384 positions: 50 us, 135 MB, floor 26: the
+//   latency of 40 KB pages in any order (loads alone: 39..42 us).
+// - D = 64, 509 rows under a window: 59 us, 17 GFLOP, floor 15: vector
+//   instructions (two thirds of the issue slots).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -764,6 +776,11 @@ __global__ void __launch_bounds__(256) kv_attn_join_kernel(AttnArgs a) {
 // SIMD's registers (D = 256, pairs), else 4: fewer splits to join, against
 // more of them to hide each other's start (48 sequences of 1..16384 positions,
 // D = 128: 50 us with 4, 93 with 8; 1 token over 32773, D = 256: 24 and 21).
+// A split has two tiles of 32 positions a wave or more (1 token over 32773:
+// 21.7 us with one or two, 24.3 with four).  One sequence is cut into as many
+// splits as fit at once, several into twice that, which evens out their unlike
+// lengths (48 sequences: 49 us against 126; one sequence of 262139 and 32773
+// positions: 81 and 33 us with twice, 74 and 22 with once).
 struct Shape {
     int rt, target, min_chunk, nitems;
 };

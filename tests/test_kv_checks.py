@@ -117,6 +117,10 @@ def test_attn_arguments():
     big = seqs(rows=1 << 22, nseq=1, q_start=None)
     assert b.qk_kv_attn(c, big, 16, heads(1, 2048, 128, 1, 1), heads(8, 2048, 128), 1.0, 0, 200 * M, 1 << 40) == SHAPE
     assert b.qk_kv_attn(c, s, 4, q, o, 1.0, -1, 20 * M, 1 << 40) == SHAPE
+    # a row each for 65536 sequences: 2^21 sequences x KV heads pass, a KV head more does not
+    for hk, ok in ((32, True), (33, False), (512, False)):
+        wide = b.qk_kv_cache(c.pool, c.num_pages, hk, c.head_dim, c.page_size)
+        assert (b.qk_kv_attn_workspace_bytes(wide, seqs(rows=65536, nseq=65536, q_start=None), hk) >= 0) == ok
     # out over the queries, the pool, the tables
     for at in (1 * M + 4, 10 * M + 64, 11 * M, 12 * M + 4, 13 * M + 28):
         assert b.qk_kv_attn(c, s, 4, q, b.qk_heads(at, 512, 128, 1, 0), 1.0, 0, 20 * M, 1 << 40) == PTR
