@@ -25,10 +25,10 @@
 //
 // Bounds and figures (device time in a graph, of the floor that the bytes set
 // at 5.1 TB/s or the products at 1150 TFLOP/s):
-// - D = 256, 24 heads on 4, 1 token: 262139 positions 74 us, 336 MB, floor 66:
+// - D = 256, 24 heads on 4, 1 token: 262139 positions 73 us, 336 MB, floor 66:
 //   memory.  32773 positions 21 us, floor 8: start, one round trip a tile and
 //   the joining launch (4 us).
-// - D = 128, 48 sequences of 1..16384 positions: 50 us, 135 MB, floor 26: the
+// - D = 128, 48 sequences of 1..16384 positions: 46 us, 135 MB, floor 26: the
 //   latency of 40 KB pages in any order (loads alone: 39..42 us).
 // - D = 64, 509 rows under a window: 59 us, 17 GFLOP, floor 15: vector
 //   instructions (two thirds of the issue slots).
@@ -36,6 +36,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "qk_kv.h"
 
@@ -114,10 +115,12 @@ template <typename T> __device__ __forceinline__ T scan(T v) {
 // chunk shares the whole call's work out over the compute units -- from the
 // lengths themselves, so neither a page table made for longer contexts nor a
 // batch of unlike lengths leaves units idle (48 sequences of 1..16384
-// positions: 93 us with splits cut by the table's length, 48 with this).  A work item is one
+// positions: 93 us with splits cut by the table's length, 46 with this).  A work item is one
 // (tile, split); a sequence's items follow those of the sequences before it,
-// which every workgroup sums up for itself.  Where tiles alone fill the card
-// (target 0) nothing is split and a tile's number says where it is.
+// which every workgroup sums up for itself (SHARE).  Where tiles alone fill
+// the card (target 0) nothing is split and a tile's number says where it is
+// (4000 sequences of 300 positions, D = 128: 2900 us with sums, 520 without);
+// a kernel of its own, as the second way cost the first 5..7% in one.
 struct AttnArgs {
     KvCache c;
     KvSeqs sq;
@@ -140,9 +143,9 @@ struct Item {
 
 // One wave, uniform results.  by_row: the tile `j` of sequence `want`;
 // otherwise the item number `want`.  false: there is none.
-template <int RT> __device__ __forceinline__ bool find_item(const AttnArgs &a, int want, bool by_row, int j, int lane,
+template <int RT, bool SHARE> __device__ __forceinline__ bool find_item(const AttnArgs &a, int want, bool by_row, int j, int lane,
                                                             Item &it) {
-    if (!a.target) {
+    if constexpr (!SHARE) {
         // a sequence's tiles are numbered from first * grp / RT + min(s, first)
         // on, a place of its own for each without a sum: the quotient and the
         // 1 that a sequence with rows adds cover its tiles, and empty ones,
@@ -163,6 +166,8 @@ template <int RT> __device__ __forceinline__ bool find_item(const AttnArgs &a, i
             it.j = want - base_of(it.s, it.first);
         }
         it.len = __builtin_amdgcn_readfirstlane(a.sq.kv_len[it.s]);
+        // (kept in scalar registers: 20 vector registers fewer)
+        for (int *f : {&it.s, &it.j, &it.first, &it.n, &it.len}) *f = __builtin_amdgcn_readfirstlane(*f);
         it.split = it.id0 = 0;
         it.ns = 1;
         return it.n > 0 && it.j >= 0 && (int64_t)it.j * RT < (int64_t)it.n * a.grp;
@@ -249,7 +254,7 @@ constexpr int waves(int D, int rt) { return D == 256 && rt == 8 ? 8 : 4; }
 
 // One workgroup: a tile of query rows, one KV head, one split of the
 // positions; its waves take tiles of 32 positions in turn and join at the end.
-template <int D, int MT, bool PAIR>
+template <int D, int MT, bool PAIR, bool SHARE>
 __global__ void __launch_bounds__(64 * waves(D, Form<MT, PAIR>::RT), 2)
 kv_attn_kernel(AttnArgs a) {
     using L = KvLayout<D>;
@@ -265,9 +270,7 @@ kv_attn_kernel(AttnArgs a) {
     const int hc = PAIR ? col >> 3 : 0;   // half of the groups, by column
     const int hk = blockIdx.x % a.c.hkv, bs = blockIdx.x / a.c.hkv;
     Item t;
-    if (!find_item<RT>(a, bs, false, 0, lane, t)) return;
-    // scalar registers, also where both ways of finding an item meet (else 20 vector registers more)
-    for (int *f : {&t.s, &t.j, &t.split, &t.ns, &t.first, &t.n, &t.len, &t.id0}) *f = __builtin_amdgcn_readfirstlane(*f);
+    if (!find_item<RT, SHARE>(a, bs, false, 0, lane, t)) return;
     const int R = t.n * a.grp;
     const int64_t cap = (int64_t)a.sq.max_pages << a.c.ps_log2;
     // positions of the tile's first and last row, and the split's tiles of 32
@@ -718,7 +721,7 @@ __global__ void __launch_bounds__(256) kv_attn_join_kernel(AttnArgs a) {
     if (rs.s >= a.sq.nseq) return;
     const int hk = h / a.grp, r = (row - rs.first) * a.grp + h % a.grp;
     Item t;
-    if (!find_item<RT>(a, rs.s, true, r / RT, lane, t) || t.ns == 1) return;  // (one split: written already)
+    if (!find_item<RT, true>(a, rs.s, true, r / RT, lane, t) || t.ns == 1) return;  // (one split: written already)
     const int ns = t.ns;
     auto unit = [&](int s) { return ((int64_t)(t.id0 + s) * a.c.hkv + hk) * RT + r % RT; };
     const float2 v = tid < ns ? a.ml[unit(tid)] : make_float2(M_NONE, 0.f);
@@ -832,15 +835,19 @@ hipError_t launch_kv_attn(const KvCache &c, const KvSeqs &seqs, int hq, const He
         hipLaunchKernelGGL(join, dim3((unsigned)(seqs.rows * hq)), dim3(256), 0, st, a);
         return hipGetLastError();
     };
-    if (c.D == 256)
-        return s.rt == 8 ? go(kv_attn_kernel<256, 1, true>, kv_attn_join_kernel<256, 8>)
-                         : go(kv_attn_kernel<256, 1, false>, kv_attn_join_kernel<256, 16>);
-    if (c.D == 128)
-        return s.rt == 8 ? go(kv_attn_kernel<128, 1, true>, kv_attn_join_kernel<128, 8>)
-                         : go(kv_attn_kernel<128, 1, false>, kv_attn_join_kernel<128, 16>);
-    return s.rt == 8    ? go(kv_attn_kernel<64, 1, true>, kv_attn_join_kernel<64, 8>)
-           : s.rt == 16 ? go(kv_attn_kernel<64, 1, false>, kv_attn_join_kernel<64, 16>)
-                        : go(kv_attn_kernel<64, 2, false>, kv_attn_join_kernel<64, 32>);
+    auto form = [&](auto share) {
+        constexpr bool SHARE = decltype(share)::value;
+        if (c.D == 256)
+            return s.rt == 8 ? go(kv_attn_kernel<256, 1, true, SHARE>, kv_attn_join_kernel<256, 8>)
+                             : go(kv_attn_kernel<256, 1, false, SHARE>, kv_attn_join_kernel<256, 16>);
+        if (c.D == 128)
+            return s.rt == 8 ? go(kv_attn_kernel<128, 1, true, SHARE>, kv_attn_join_kernel<128, 8>)
+                             : go(kv_attn_kernel<128, 1, false, SHARE>, kv_attn_join_kernel<128, 16>);
+        return s.rt == 8    ? go(kv_attn_kernel<64, 1, true, SHARE>, kv_attn_join_kernel<64, 8>)
+               : s.rt == 16 ? go(kv_attn_kernel<64, 1, false, SHARE>, kv_attn_join_kernel<64, 16>)
+                            : go(kv_attn_kernel<64, 2, false, SHARE>, kv_attn_join_kernel<64, 32>);
+    };
+    return s.target ? form(std::true_type{}) : form(std::false_type{});
 }
 
 }  // namespace qk
