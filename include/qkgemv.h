@@ -516,11 +516,17 @@ int qk_kv_read(const qk_kv_cache *cache, const qk_kv_seqs *seqs, const qk_heads 
  *              that is 0), for this call until it has run: calls that may
  *              overlap, captured ones among them, need workspaces of their own
  * Scores, softmax statistics and sums are fp32, products of codes and queries
- * exact; a probability times a step enters the matrix instructions as a sum
- * of two fp16 values (2^-20 of it).  Non-finite queries give non-finite rows
- * and touch no other row.  Accuracy, for exact p_j and, of values and keys,
- * a_ji = d * code + |m|: within (2^-15 + 2^-17 * max_j |scale| sum_i |q_i|
- * a_ji) * sum_j p_j a'_ji, plus the rounding of the output type.
+ * exact.  A probability, and its product with a step, enter the matrix
+ * instructions as sums of two fp16 values: to 2^-20 of themselves, and not
+ * below 2^-38 of the row's largest probability P, times (for the product) up
+ * to 16 times the largest step S of the positions that the sequence's rows
+ * see.  So the tail of a softmax counts however long it is and whatever the
+ * values' scale.  Non-finite queries give non-finite rows and touch no other
+ * row.  Accuracy, for exact p_j, n positions and, of values and keys, a_ji =
+ * d * code + |m|: within
+ *   (2^-15 + 2^-38 n P + 2^-17 max_j |scale| sum_i |q_i| a_ji) sum_j p_j a'_ji
+ *   + n P (2^-28 max(S, 2^-15) + 2^-38 max |m|)  + (S >= 1: 2^-20 S),
+ * plus the rounding of the output type.
  */
 int64_t qk_kv_attn_workspace_bytes(const qk_kv_cache *cache, const qk_kv_seqs *seqs, int n_heads);
 int qk_kv_attn(const qk_kv_cache *cache, const qk_kv_seqs *seqs, int n_heads, const qk_heads *q, const qk_heads *out,

@@ -10,8 +10,18 @@
 // result.  The minima's term is one more instruction for all groups, the
 // queries' group sums as two fp16 terms.
 // The values likewise: O_i = sum_j (p_j d_jg) c_ji + sum_j p_j m_jg, where
-// p_j d_jg goes in as two fp16 terms (product, and its exact residual by fma
-// plus the residual of p), so a probability is never rounded to 11 bits.
+// p_j d_jg goes in as two fp16 terms (product, and its residual by fma plus the
+// residual of p), so a probability is not rounded to 11 bits.  Two terms end
+// where fp16 does, at 2^-24, whatever they stand for: probabilities are held
+// up to 2^15 (2^13 at the running maximum) and steps times a power of two that
+// has the largest one met so far in [1/16, 1), so that a position 16 nats below
+// the maximum still has 11 bits or more, values of any scale alike.  A long tail
+// under one high score is the ordinary state of a trained model; with 1 at the
+// maximum and steps as they are, 32768 positions 12 nats down with values of
+// 0.02 came out wrong by more than the output.  One step out of that range
+// costs the tile its scaling; finding none costs 1..2% of every case below
+// (one maximum and a branch a tile; scaling every tile: 8..10% at 509 rows
+// under a window and at 17 drafts over 8191 positions).
 //
 // Layout.  Scores are computed transposed (positions are the rows of the
 // result, query rows its columns) and so is the output (dimensions by query
@@ -58,7 +68,9 @@ constexpr float M_NONE = -3e38f; // running maximum before any visible position
 // place (code * 2^-24) it was 2^-18 of the largest product, toward zero; here
 // it is 2^-21 and less.
 constexpr uint32_t EVEN = 0x00780078u, ODD = 0x07800780u;
-constexpr float GROW = 2.f;      // a probability may reach 2^GROW before the maximum is moved
+constexpr float TOP = 13.f;      // a probability is held as 2^TOP at the running maximum ...
+constexpr float GROW = 15.f;     // ... and may reach 2^GROW (fp16 ends at 2^16) before the maximum is moved
+constexpr int NEAR = 3;          // largest steps in [2^-(NEAR + 1), 1) are near enough to 1 as they are
 
 __device__ __forceinline__ f4 mfma(u4 a, u4 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
@@ -71,6 +83,10 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 __device__ __forceinline__ h2 half_pair(float v) { return h2{(_Float16)v, (_Float16)v}; }
+// the larger of each half's values (NaN where one is); three operands are one instruction
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_maximum(__builtin_bit_cast(h2, a), __builtin_bit_cast(h2, b)));
+}
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
     return __builtin_amdgcn_fdot2(__builtin_bit_cast(h2, a), __builtin_bit_cast(h2, b), c, false);
 }
@@ -444,7 +460,8 @@ kv_attn_kernel(AttnArgs a) {
     const int64_t held = min((int64_t)t.len, cap);
 
     f4 o[MT][NT], om[MT];
-    float m[MT], grow[MT];  // the maximum so far; how far a score may pass it before it moves (M_NONE: no score yet)
+    float m[MT], grow[MT];  // the maximum so far less TOP; how far a score may pass it before it moves (M_NONE: no score yet)
+    int ve = 14;            // steps are taken times 2^ve, below 1 in every tile so far; wave-uniform
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -551,7 +568,7 @@ kv_attn_kernel(AttnArgs a) {
                 mx = fmaxf(mx, __shfl_xor(mx, 16));
                 mx = fmaxf(mx, __shfl_xor(mx, 32));
                 const bool fresh = grow[mt] == M_NONE, some = mx > M_NONE;
-                const float up = fresh ? (some ? mx : 0.f) : fmaxf(mx, 0.f);
+                const float up = fresh ? (some ? mx - TOP : 0.f) : fmaxf(mx - TOP, 0.f);
                 const float al = fresh ? 0.f : __builtin_amdgcn_exp2f(-up);
                 m[mt] += up;
                 if (some) grow[mt] = GROW;
@@ -575,19 +592,57 @@ kv_attn_kernel(AttnArgs a) {
         }
 
         // values; of places that hold nothing yet, whatever their bytes say,
-        // the step and the minimum are 0
-        if (!live || x * 32 + 32 > held) {
-            const int left = live ? (int)(held - x * 32) : 0;
+        // the step and the minimum are 0.  Steps are to be below 1, and not far
+        // below: those of a tile that holds a larger one are scaled, and the
+        // sums so far with them.
+        const bool edge = !live || x * 32 + 32 > held;
+        auto largest = [&] {  // step in either half of a lane's
+            uint32_t v = 0;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int k2 = 0; k2 < 2; ++k2) {
-                    const int p = 16 * u + 4 * quad + 2 * k2;
-                    const uint32_t mask = (p < left ? 0xffffu : 0u) | (p + 1 < left ? 0xffff0000u : 0u);
+                for (int i = 0; i < 2 * GL; ++i) v = max2(v, vd[u][i]);
+            return max(v & 0xffffu, v >> 16);
+        };
+        const uint32_t top = largest();
+        if (edge || ve != 0 || __any(top >= 0x3c00u)) {
+            if (edge) {
+                const int left = live ? (int)(held - x * 32) : 0;
 #pragma unroll
-                    for (int g = 0; g < GL; ++g) vd[u][2 * g + k2] &= mask;
-                    vm[u][k2] &= mask;
-                }
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int k2 = 0; k2 < 2; ++k2) {
+                        const int p = 16 * u + 4 * quad + 2 * k2;
+                        const uint32_t mask = (p < left ? 0xffffu : 0u) | (p + 1 < left ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int g = 0; g < GL; ++g) vd[u][2 * g + k2] &= mask;
+                        vm[u][k2] &= mask;
+                    }
+            }
+            const uint32_t most = largest();
+            if (__any(most >= (uint32_t)(15 - ve) << 10)) {
+                int field = 0;  // exponent of the wave's largest step (30 for what is not finite, as others may write)
+#pragma unroll
+                for (int bit = 16; bit; bit >>= 1)
+                    if (__any(most >= (uint32_t)(field | bit) << 10)) field |= bit;
+                int to = 14 - min(field, 30);
+                if (to >= 0 && to <= NEAR) to = 0;
+                to = min(to, ve);
+                const float down = pow2(to - ve);
+                ve = to;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) o[mt][i] *= down;
+            }
+            if (ve != 0) {
+                const h2 vs = half_pair(pow2(ve));
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2 * GL; ++i)
+                        vd[u][i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, vd[u][i]) * vs);
+            }
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -673,7 +728,7 @@ kv_attn_kernel(AttnArgs a) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const f4 v = o[mt][2 * g + k];
-                const float s = (k ? 131072.f : 2097152.f) * f;  // 2^17, 2^21: the codes' units
+                const float s = (k ? 131072.f : 2097152.f) * f * pow2(-ve);  // 2^17, 2^21: the codes' units
                 *reinterpret_cast<float4 *>(mine + 32 * g + 16 * k + 4 * quad) =
                     make_float4(fmaf(v.x, s, mg), fmaf(v.y, s, mg), fmaf(v.z, s, mg), fmaf(v.w, s, mg));
             }
