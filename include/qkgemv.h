@@ -504,6 +504,8 @@ int qk_kv_read(const qk_kv_cache *cache, const qk_kv_seqs *seqs, const qk_heads 
  *
  * over the positions j <= p (row t's own, p) that are held and, with
  * window > 0, have j > p - window.  A row that sees no position gives zeros.
+ * What the cache's bytes say in places that no row of a sequence sees (not yet
+ * appended, before the window) makes no difference.
  *
  *   n_heads    query heads, a multiple of n_kv_heads, at most 4096
  *   q          rows x n_heads x D, fp16 (QK_EINVAL_TYPE otherwise)

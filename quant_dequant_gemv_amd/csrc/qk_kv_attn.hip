@@ -457,7 +457,7 @@ kv_attn_kernel(AttnArgs a) {
     }
     // (wave-uniform) tiles that every row sees whole, and positions that hold something
     const int64_t all_lo = a.window ? max((int64_t)0, pmax - a.window + 1) : 0, all_hi = min(pmin, cap - 1);
-    const int64_t held = min((int64_t)t.len, cap);
+    const int held = (int)min((int64_t)t.len, cap), past = (int)min(begin, cap);  // (cap is at most 2^30)
 
     f4 o[MT][NT], om[MT];
     float m[MT], grow[MT];  // the maximum so far less TOP; how far a score may pass it before it moves (M_NONE: no score yet)
@@ -591,11 +591,12 @@ kv_attn_kernel(AttnArgs a) {
                 }
         }
 
-        // values; of places that hold nothing yet, whatever their bytes say,
-        // the step and the minimum are 0.  Steps are to be below 1, and not far
+        // values; of places that hold nothing yet or that no row's window
+        // reaches, whatever their bytes say, the step and the minimum are 0
+        // (a probability of 0 does not hide NaN).  Steps are to be below 1, and not far
         // below: those of a tile that holds a larger one are scaled, and the
         // sums so far with them.
-        const bool edge = !live || x * 32 + 32 > held;
+        const bool edge = !live || x * 32 + 32 > held || x * 32 < past;
         auto largest = [&] {  // step in either half of a lane's
             uint32_t v = 0;
 #pragma unroll
@@ -607,13 +608,13 @@ kv_attn_kernel(AttnArgs a) {
         const uint32_t top = largest();
         if (edge || ve != 0 || __any(top >= 0x3c00u)) {
             if (edge) {
-                const int left = live ? (int)(held - x * 32) : 0;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int k2 = 0; k2 < 2; ++k2) {
-                        const int p = 16 * u + 4 * quad + 2 * k2;
-                        const uint32_t mask = (p < left ? 0xffffu : 0u) | (p + 1 < left ? 0xffff0000u : 0u);
+                        const int p = x * 32 + 16 * u + 4 * quad + 2 * k2;
+                        const uint32_t mask = (live && p >= past && p < held ? 0xffffu : 0u) |
+                                              (live && p + 1 >= past && p + 1 < held ? 0xffff0000u : 0u);
 #pragma unroll
                         for (int g = 0; g < GL; ++g) vd[u][2 * g + k2] &= mask;
                         vm[u][k2] &= mask;

@@ -75,24 +75,30 @@ def attention(c, q, pos, seen, scale, window=0):
     return out, bound
 
 
-def check_attn(c, q, nseq, split, picks, window=0, length=None):
-    """q [rows, hq, D], the same number of rows for each of nseq sequences over the context c, into fp32; the rows
-    `picks` against fp64.  split: whether the call has to be one that cuts contexts into splits."""
+def check_attn(c, q, ns, split, picks, window=0, length=None):
+    """q [rows, hq, D], ns[s] rows for sequence s (or the number of sequences, of as many rows each), every sequence
+    over the context c, into fp32; the rows `picks` against fp64.  split: whether the call has to be one that cuts
+    contexts into splits."""
     import torch
     from quant_dequant_gemv_amd import binding
     rows, hq = q.shape[:2]
-    n, length, scale = rows // nseq, length or c.length, c.D ** -0.5
+    even = isinstance(ns, int)
+    ns = [rows // ns] * ns if even else ns
+    first = np.concatenate([[0], np.cumsum(ns)]).astype(np.int32)
+    length, scale = length or c.length, c.D ** -0.5
     out = torch.full((rows, hq, c.D), 77.0, device="cuda")
-    lens, pages = _dev(np.full(nseq, length, np.int32)), c.table(nseq)
-    need = binding.qk_kv_attn_workspace_bytes(c.cache._c, binding._seqs_arg(rows, pages, lens, None), hq)
+    lens, pages, q_start = _dev(np.full(len(ns), length, np.int32)), c.table(len(ns)), None if even else _dev(first)
+    need = binding.qk_kv_attn_workspace_bytes(c.cache._c, binding._seqs_arg(rows, pages, lens, q_start), hq)
     assert (need > 0) == split, "not the form that this case is for"
-    binding.kv_attn(c.cache, _dev(q), pages, lens, out=out, window=window)
+    binding.kv_attn(c.cache, _dev(q), pages, lens, q_start=q_start, out=out, window=window)
     torch.cuda.synchronize()
     got = out[list(picks)].cpu().numpy().astype(np.float64)
-    seen = slice(max(0, length - n - window + 1) if window else 0, length)
     worst = 0
     for t, y in zip(picks, got):
-        want, bound = attention(c, q[t], length - n + t % n, seen, scale, window)
+        s = int(np.searchsorted(first, t, "right")) - 1
+        n, i = ns[s], t - first[s]
+        seen = slice(max(0, length - n - window + 1) if window else 0, length)
+        want, bound = attention(c, q[t], length - n + i, seen, scale, window)
         err = np.abs(y - want)
         assert (err <= bound).all(), \
             f"row {t}: {np.max(err / bound):.3g} of the bound, {np.max(err) / np.max(np.abs(want)):.3g} of the output"
