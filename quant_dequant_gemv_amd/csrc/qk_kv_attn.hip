@@ -18,10 +18,11 @@
 // the maximum still has 11 bits or more, values of any scale alike.  A long tail
 // under one high score is the ordinary state of a trained model; with 1 at the
 // maximum and steps as they are, 32768 positions 12 nats down with values of
-// 0.02 came out wrong by more than the output.  One step out of that range
-// costs the tile its scaling; finding none costs 1..2% of every case below
-// (one maximum and a branch a tile; scaling every tile: 8..10% at 509 rows
-// under a window and at 17 drafts over 8191 positions).
+// 0.02 came out wrong by more than the output.  The power is chosen at a wave's
+// first tile and lowered where a later one has a larger step: a maximum and a
+// branch a tile, within the spread of the cases below but for 2% at 509 rows
+// under a window.  It is 1 where the first tile allows it (values of 0.02, which
+// are scaled: 2..4% more at 509 rows, 2% at 48 sequences and 17 drafts).
 //
 // Layout.  Scores are computed transposed (positions are the rows of the
 // result, query rows its columns) and so is the output (dimensions by query
@@ -461,7 +462,7 @@ kv_attn_kernel(AttnArgs a) {
 
     f4 o[MT][NT], om[MT];
     float m[MT], grow[MT];  // the maximum so far less TOP; how far a score may pass it before it moves (M_NONE: no score yet)
-    int ve = 14;            // steps are taken times 2^ve, below 1 in every tile so far; wave-uniform
+    int ve = 0;             // steps are taken times 2^ve, below 1 in every tile so far; wave-uniform
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -605,8 +606,8 @@ kv_attn_kernel(AttnArgs a) {
                 for (int i = 0; i < 2 * GL; ++i) v = max2(v, vd[u][i]);
             return max(v & 0xffffu, v >> 16);
         };
-        const uint32_t top = largest();
-        if (edge || ve != 0 || __any(top >= 0x3c00u)) {
+        uint32_t top = largest();
+        if (edge || ve != 0 || __any(top >= 0x3c00u) || (k == 1 && !__any(top >= (uint32_t)(14 - NEAR) << 10))) {
             if (edge) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
@@ -619,16 +620,16 @@ kv_attn_kernel(AttnArgs a) {
                         for (int g = 0; g < GL; ++g) vd[u][2 * g + k2] &= mask;
                         vm[u][k2] &= mask;
                     }
+                top = largest();
             }
-            const uint32_t most = largest();
-            if (__any(most >= (uint32_t)(15 - ve) << 10)) {
+            if (k == 1 || __any(top >= (uint32_t)(15 - ve) << 10)) {
                 int field = 0;  // exponent of the wave's largest step (30 for what is not finite, as others may write)
 #pragma unroll
                 for (int bit = 16; bit; bit >>= 1)
-                    if (__any(most >= (uint32_t)(field | bit) << 10)) field |= bit;
+                    if (__any(top >= (uint32_t)(field | bit) << 10)) field |= bit;
                 int to = 14 - min(field, 30);
                 if (to >= 0 && to <= NEAR) to = 0;
-                to = min(to, ve);
+                if (k > 1) to = min(to, ve);
                 const float down = pow2(to - ve);
                 ve = to;
 #pragma unroll
