@@ -401,8 +401,9 @@ typedef struct qk_rope {
  *   (u, v) of pair j -> (u cos a - v sin a, u sin a + v cos a),
  *   a = position * inv_freq[j];  dimensions >= rot_dim keep n
  *
- * in fp64 (positions far from 0 keep their angle), rounded once to the output
- * type (fp16: beyond the range +-inf).
+ * in fp64 (positions far from 0 keep their angle), rounded to fp32 and, for
+ * fp16 outputs, from there to fp16 (beyond its range +-inf): off by at most
+ * half a step of the output type, for fp16 and 2^-24 of the value.
  *
  *   head_dim    D: 64, 128 or 256
  *   q, q_out    rows x n_heads x D, or both NULL (n_heads is then ignored)

@@ -134,7 +134,12 @@ struct RowsArgs {
     int per, chunks;           // groups of HPW heads a wave takes, waves of a row
 };
 
-// Norm, rotation and grouping in registers.  The pair of a rotated dimension
+// Norm, rotation and grouping in registers, in fp64 up to the fp32 value that is
+// grouped or stored; an fp16 output is rounded from that value, so it is off by
+// half a step and 2^-24 at most.  (The fp64 value cut to 21 bits with a sticky
+// last one would be rounded once: two instructions an element, 17.95 against
+// 17.1 us at 2048 rows, D = 128, for one value in 2^14 one step nearer by less
+// than 2^-24.)  The pair of a rotated dimension
 // is in the same lane (interleaved) or, the normed value depending on its own
 // element alone, loaded a second time from where it lies (an L1 hit): nothing
 // but the row's sines and cosines passes LDS, once for all heads of the wave.
@@ -142,9 +147,10 @@ struct RowsArgs {
 // VEC: every view's heads are whole pieces of 4 elements, the weights whole
 // 16 bytes, and so are the rotated part and the way to a pair (2048 rows of 32
 // + 8 heads, D = 128: 17.4 us with it, 19.3 without).
-// 2048 rows, D = 128: 17 us, 42 MB, floor 8: fp64 norm and rotation (67% of the
-// vector issue slots; fp32 would not hold the angles of far positions, and its
-// sums would round before the one rounding of the result).  4096 rows, D = 64,
+// 2048 rows, D = 128: 17 us, 42 MB, floor 8: vector instructions, those of every
+// element (a head's element and its pair are both normed, and types and form of
+// rotation told apart as the kernel runs), not the angles, which are found once
+// a row.  4096 rows, D = 64,
 // into the cache: 20 us.  One token: 3.5 us, a launch.
 template <int D, bool VEC>
 __global__ void __launch_bounds__(64 * WAVES) kv_rows_kernel(RowsArgs a) {

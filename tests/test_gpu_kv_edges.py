@@ -33,3 +33,30 @@ def test_positions_before_the_window_may_hold_anything(D, grp, n):
     got = binding.kv_attn(cache, dev(q), dev(c.pages), dev(kv_len), window=window, out=torch.empty(n, grp, D, device="cuda"))
     torch.cuda.synchronize()
     assert (np.abs(got.cpu().numpy() - want) <= kv_ref.attention_bound(want, mass, amax, False)).all()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+def test_fp16_rows_are_rounded_by_way_of_fp32(norm, interleaved):
+    """The fp64 value to fp32 and from there to fp16: never further off than those two roundings."""
+    rng = np.random.default_rng(7)
+    rows, hq, hk, D = 400, 8, 2, 128
+    f = (1e4 ** (-np.arange(64) / 64)).astype(np.float32)
+    w = (1 + 0.3 * rng.standard_normal(D)).astype(np.float32) if norm else None
+    pos = rng.integers(0, 100000, rows).astype(np.int32)
+    q, k = (rng.standard_normal((rows, h, D)).astype(np.float32) for h in (hq, hk))
+    q[0] *= np.float32(1e-6)  # subnormal results
+    rope = binding.Rope(dev(f), interleaved, *([dev(w)] * 2 if norm else []), eps=1e-5)
+    outs = binding.norm_rope(rope, dev(pos), dev(q), dev(k))
+    strided = torch.empty(hq, D, rows, dtype=torch.float16, device="cuda").permute(2, 0, 1)
+    binding.norm_rope(rope, dev(pos), dev(q), q_out=strided)
+    cache = binding.KVCache(7, hk, D, 64)
+    args = dev(np.arange(7, dtype=np.int32)[None]), dev(np.array([rows], np.int32))
+    appended = binding.kv_append(cache, dev(k), dev(k), *args, q=dev(q), rope=rope, positions=dev(pos))
+    torch.cuda.synchronize()
+    for x, got in ((q, outs[0]), (k, outs[1]), (q, strided), (q, appended)):
+        ref = kv_ref.norm_rope(x, pos, f, interleaved, w, 1e-5)
+        err = np.abs(got.cpu().numpy().astype(np.float64) - ref)
+        best = np.abs(ref.astype(np.float32).astype(np.float16).astype(np.float64) - ref)
+        # fp64's own roundings: a few 2^-53 of the pair's size
+        assert (err <= best + 2.0 ** -45 * np.abs(ref).max(-1, keepdims=True)).all(), (err > best + 2.0 ** -45).sum()
