@@ -532,11 +532,16 @@ def _int32_arg(t, name, shape):
     return t.data_ptr()
 
 
+_INT_MAX = 0x7fffffff  # ctypes takes an int's low 32 bits for a C int without a word
+
+
 def _seqs_arg(rows, pages, kv_len, q_start):
     i32 = _torch.int32
     try:
         nseq, = kv_len.shape
         n, mp = pages.shape
+        if rows > _INT_MAX or mp > _INT_MAX:
+            raise QKError(QK_EINVAL_SHAPE, "qk_kv_seqs")
         if kv_len.dtype is i32 and pages.dtype is i32 and n == nseq and kv_len.is_contiguous() and \
                 pages.is_contiguous():
             if q_start is None:
@@ -621,8 +626,9 @@ class KVCache:
 
     def __init__(self, num_pages: int, n_kv_heads: int, head_dim: int, page_size: int = 64, device="cuda", pool=None):
         torch = _start()
-        pb = qk_kv_page_bytes(head_dim, n_kv_heads, page_size)
-        if pb < 0 or not 1 <= num_pages < 1 << 31:
+        small = all(abs(n) <= _INT_MAX for n in (head_dim, n_kv_heads, page_size))
+        pb = qk_kv_page_bytes(head_dim, n_kv_heads, page_size) if small else -1
+        if pb < 0 or not 1 <= num_pages <= _INT_MAX:
             raise QKError(QK_EINVAL_SHAPE, "KVCache")
         if pool is None:
             pool = torch.empty((num_pages, pb), dtype=torch.uint8, device=device)
@@ -752,6 +758,7 @@ def kv_attn(cache: KVCache, q, pages, kv_len, q_start=None, scale: float | None 
     else:
         _need(workspace, "workspace", torch.uint8)
         ws, need = workspace, workspace.numel()
+    window = max(-1, min(window, _INT_MAX))  # (no context is longer)
     rc = _lib.qk_kv_attn(c, seqs, heads, qa, oa, D ** -0.5 if scale is None else scale, window,
                     None if ws is None else ws.data_ptr(), max(need, 0), _current(dev))
     if rc != QK_OK:

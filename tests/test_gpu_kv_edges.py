@@ -60,3 +60,17 @@ def test_fp16_rows_are_rounded_by_way_of_fp32(norm, interleaved):
         best = np.abs(ref.astype(np.float32).astype(np.float16).astype(np.float64) - ref)
         # fp64's own roundings: a few 2^-53 of the pair's size
         assert (err <= best + 2.0 ** -45 * np.abs(ref).max(-1, keepdims=True)).all(), (err > best + 2.0 ** -45).sum()
+
+
+def test_windows_past_32_bits():
+    """A window longer than any context hides nothing, also past the C type; a negative one is refused."""
+    rng = np.random.default_rng(3)
+    c = kv_ref.Cache(rng, 1, 4, 1, 64, 32)
+    cache = binding.KVCache(c.num_pages, 1, 64, 32, pool=dev(c.pool))
+    args = cache, dev(rng.standard_normal((2, 4, 64)).astype(np.float16)), dev(c.pages), dev(np.array([100], np.int32))
+    every = binding.kv_attn(*args)
+    for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63 - 1):
+        assert torch.equal(binding.kv_attn(*args, window=window), every)
+    for window in (-1, -2 ** 31, -2 ** 32, -2 ** 32 + 5):
+        with pytest.raises(binding.QKError):
+            binding.kv_attn(*args, window=window)

@@ -210,6 +210,20 @@ def test_helpers_refuse():
             call()
 
 
+def test_helpers_refuse_sizes_past_32_bits():
+    """Not their low 32 bits."""
+    pool = z(4 * 2 * 2 * 32 * 80, dtype=torch.uint8)
+    for sizes in ((4, 2 + 2 ** 32, 128, 32), (4, 2, 128 + 2 ** 32, 32), (4, 2, 128, 32 + 2 ** 32), (4 + 2 ** 32, 2, 128, 32)):
+        with pytest.raises(b.QKError):
+            b.KVCache(*sizes, pool=pool)
+    c = b.KVCache(4, 2, 128, 32, pool=pool)
+    pages, kv_len = z(1, 3, dtype=torch.int32), z(1, dtype=torch.int32)
+    with pytest.raises(b.QKError):
+        b.kv_read(c, 2 ** 32 + 1, pages, kv_len)
+    with pytest.raises(b.QKError):
+        b.kv_read(c, 1, z(1, 1, dtype=torch.int32).expand(1, 2 ** 32 + 3), kv_len)
+
+
 def test_struct_layouts():
     assert ctypes.sizeof(b.qk_heads) == 40 and ctypes.sizeof(b.qk_rope) == 48
     assert ctypes.sizeof(b.qk_kv_cache) == 32 and ctypes.sizeof(b.qk_kv_seqs) == 40
