@@ -487,6 +487,13 @@ def attention_stream(torch, tensors, entries, groups, fused, context):
     return out
 
 
+def attention_launches(stream):
+    """Launches of the attention layers' own work in an attention_stream: the
+    append, the attention and, where its contexts are cut into splits (it then
+    needs a workspace, the last of its arguments), their join."""
+    return sum(2 + (a[1][-1] > 0) for kind, a in stream if kind == "heads")
+
+
 def run_stream(torch, launcher, warm=2, only=None, tokens=1, context=32768):
     """448 GEMVs of one decode token, all weights resident, back to back on
     one stream: one launch per GEMV; one qk_gemv_batch launch per group of
@@ -681,7 +688,7 @@ def run_stream(torch, launcher, warm=2, only=None, tokens=1, context=32768):
         fn = fns[only[:-6] if graph else only]
         launches = len(entries) if fn is one_token else 2 if only.startswith("chain") else len(groups)
         if fn is one_token_attention:
-            launches += 3 * sum(kind == "heads" for kind, _ in attention)
+            launches += attention_launches(attention)
         if graph:
             s2 = torch.cuda.Stream()
             gr = torch.cuda.CUDAGraph()
