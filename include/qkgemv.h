@@ -527,9 +527,10 @@ int qk_kv_read(const qk_kv_cache *cache, const qk_kv_seqs *seqs, const qk_heads 
  * values' scale.  Non-finite queries give non-finite rows and touch no other
  * row.  Accuracy, for exact p_j, n positions and, of values and keys, a_ji =
  * d * code + |m|: within
- *   (2^-15 + 2^-38 n P + 2^-17 max_j |scale| sum_i |q_i| a_ji) sum_j p_j a'_ji
+ *   (2^-15 + 2^-38 n P + 2^-17 max_j z_j) sum_j p_j a'_ji
  *   + n P (2^-28 max(S, 2^-15) + 2^-38 max |m|)  + (S >= 1: 2^-20 S),
- * plus the rounding of the output type.
+ * z_j = |scale| sum_i (|q_i| + 2^-14 |q|) a_ji with the row's norm |q| (a query's
+ * elements are held to 2^-33 of it), plus the rounding of the output type.
  */
 int64_t qk_kv_attn_workspace_bytes(const qk_kv_cache *cache, const qk_kv_seqs *seqs, int n_heads);
 int qk_kv_attn(const qk_kv_cache *cache, const qk_kv_seqs *seqs, int n_heads, const qk_heads *q, const qk_heads *out,

@@ -390,9 +390,10 @@ kv_attn_kernel(AttnArgs a) {
                 load_v(max(page, 0), x);
             }
         }
-        // row norm N: scaled by 2^e to N in [2^9, 2^10), its largest element is
-        // in [2^5, 2^10) (2^3 less in rows below 2^-21); infinite, NaN or zero
-        // rows as they are
+        // row norm N: scaled by 2^e to N in [2^12, 2^13), as high as a group's
+        // sum (below 2^5/2 N) stays in fp16; the smallest elements' sixteenths
+        // are then held to 2^-33 N.  Rows below 2^-18 by 2^30, which is exact;
+        // infinite, NaN or zero rows as they are.
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < G; ++i)
@@ -401,7 +402,7 @@ kv_attn_kernel(AttnArgs a) {
         if (PAIR) ss += __shfl_xor(ss, 8);
         ss += __shfl_xor(ss, 16);
         ss += __shfl_xor(ss, 32);
-        const int e = ss > 0.f && ss < 1e30f ? min(9 - (((int)(__float_as_uint(ss) >> 23) - 127) >> 1), 30) : 0;
+        const int e = ss > 0.f && ss < 1e30f ? min(12 - (((int)(__float_as_uint(ss) >> 23) - 127) >> 1), 30) : 0;
         const float f = pow2(e);
         sc2[mt] = a.scale * 1.44269504088896340736f * pow2(-e);
         sc1[mt] = sc2[mt] * 2097152.f;  // 2^21, the codes' unit

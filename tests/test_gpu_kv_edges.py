@@ -74,3 +74,29 @@ def test_windows_past_32_bits():
     for window in (-1, -2 ** 31, -2 ** 32, -2 ** 32 + 5):
         with pytest.raises(binding.QKError):
             binding.kv_attn(*args, window=window)
+
+
+@pytest.mark.parametrize("D,grp", [(64, 4), (128, 6), (256, 6), (64, 16), (128, 16), (256, 16)])
+def test_small_elements_beside_a_large_one(D, grp):
+    """A query's elements are held to 2^-33 of its norm: multiples of it are exact.  The keys are 0 at the large one,
+    so the small ones alone make the score."""
+    length, big, small = 2, 2, np.float16(2.0 ** -18)
+    k, v = np.zeros((2, length, 1, D), np.float32)
+    k[0, 0, 33::2], k[1, 0, 33::2] = 20000, -20000  # (0 between them: codes, not the minimum alone)
+    v[0], v[1] = 1, -1
+    q = np.zeros((1, grp, D), np.float16)
+    q[:, 0::2, 33::2] = small  # the odd dimensions' codes are read 16 times as large
+    q[:, 1::2, 33::2] = -small
+    q[..., big] = 8192
+    c = kv_ref.Cache.__new__(kv_ref.Cache)
+    c.hkv, c.D, c.ps, c.mp, c.held = 1, D, length, 1, np.ones((1, 1), bool)
+    c.f = [tuple(t[None] for t in kv_ref.quantise(x)) for x in (k, v)]
+    assert (c.kv()[0][0, :, 0, big] == 0).all()
+    want, mass, amax = kv_ref.attention(c, q, [(0, 1, 2)], [length], D ** -0.5)
+    assert (np.abs(want) > 0.05).all()
+    cache = binding.KVCache(1, 1, D, 64)
+    pages, lens = dev(np.zeros((1, 1), np.int32)), dev(np.array([length], np.int32))
+    binding.kv_append(cache, dev(k), dev(v), pages, lens)
+    got = binding.kv_attn(cache, dev(q), pages, lens, out=torch.empty(1, grp, D, device="cuda"))
+    torch.cuda.synchronize()
+    assert (np.abs(got.cpu().numpy() - want) <= kv_ref.attention_bound(want, mass, amax, False)).all()
