@@ -455,7 +455,8 @@ def attention_stream(torch, tensors, entries, groups, fused, context):
     """The fused stream's launches with ("heads", (qk_kv_append arguments,
     qk_kv_attn arguments)) behind every attention layer's q/k/v group.  The
     token stands at position context - 1 of a filled cache: 24 query and 4 KV
-    heads of 256, 64 of them rotated, pages of 64 positions."""
+    heads of 256, 64 of them rotated, pages of 64 positions.  The gates beside
+    the query heads are not applied."""
     from quant_dequant_gemv_amd import binding
     hq, hkv, D, ps = 24, 4, 256, 64
     n = -(-context // ps)

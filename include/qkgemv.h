@@ -419,8 +419,8 @@ int qk_norm_rope(const qk_rope *rope, int rows, int head_dim, int n_heads, const
 /*
  * One layer's cache: a pool of num_pages pages, each page_size positions of
  * every KV head.  A row of D values is held as D/32 groups of 32 consecutive
- * dimensions, 5 bits a value: a 4-bit code each, an fp16 step d and an fp16
- * minimum m per group, value = d * code + m.  Of an fp32 row (NaN taken as 0,
+ * dimensions, 5 bits a value: a 4-bit code each, an fp16 step d >= 0 and an
+ * fp16 minimum m per group, value = d * code + m.  Of an fp32 row (NaN taken as 0,
  * values beyond +-65504 as +-65504, so a cache never holds a non-finite
  * value), in fp32: m = fp16(min), d = fp16((max - m) / 15),
  * code = rint((x - m) / d) kept in 0..15 (0 where d <= 0), so each value is

@@ -674,7 +674,8 @@ def kv_append(cache: KVCache, k, v, pages, kv_len, q_start=None, q=None, rope: R
     qk_kv_seqs: pages int32 [nseq, max_pages], kv_len int32 [nseq], q_start
     int32 [nseq + 1] or None), keys -- and the queries q [rows, heads, D] --
     normed and rotated by ``rope``; returns q_out (float16 unless given; None
-    without q)."""
+    without q).  Rows of no sequence are left as they were: undefined in a
+    q_out that is allocated here."""
     torch = _torch
     D, hk = cache.head_dim, cache.n_kv_heads
     ka = _heads_arg(k, "k", None, hk, D)
@@ -711,7 +712,8 @@ def kv_append(cache: KVCache, k, v, pages, kv_len, q_start=None, q=None, rope: R
 
 def kv_read(cache: KVCache, rows: int, pages, kv_len, q_start=None, k_out=None, v_out=None, stream=None):
     """What the cache holds at the rows' positions: (k, v), float32
-    [rows, kv heads, D] unless given."""
+    [rows, kv heads, D] unless given.  Rows of no sequence are left as they
+    were."""
     torch = _torch
     seqs = _seqs_arg(rows, pages, kv_len, q_start)
     shape = (rows, cache.n_kv_heads, cache.head_dim)
@@ -735,7 +737,9 @@ def kv_attn(cache: KVCache, q, pages, kv_len, q_start=None, scale: float | None 
     """Attention of q (float16 [rows, heads, D]) over the rows' sequences;
     scale None: D ** -0.5; window 0: none.  Returns out, float16 contiguous
     unless given.  workspace: uint8 device tensor of at least
-    qk_kv_attn_workspace_bytes bytes (None: allocated for the call)."""
+    qk_kv_attn_workspace_bytes bytes (None: allocated for the call).  Rows of
+    no sequence are left as they were: undefined in an out that is allocated
+    here."""
     torch = _torch
     D = cache.head_dim
     qa = _heads_arg(q, "q", None, None, D)

@@ -37,12 +37,12 @@
 // Bounds and figures (device time in a graph, of the floor that the bytes set
 // at 5.1 TB/s or the products at 1150 TFLOP/s):
 // - D = 256, 24 heads on 4, 1 token: 262139 positions 73 us, 336 MB, floor 66:
-//   memory.  32773 positions 21 us, floor 8: start, one round trip a tile and
+//   memory.  32773 positions 20 us, floor 8: start, one round trip a tile and
 //   the joining launch (4 us).
 // - D = 128, 48 sequences of 1..16384 positions: 46 us, 135 MB, floor 26: the
-//   latency of 40 KB pages in any order (loads alone: 39..42 us).
+//   latency of 40 KB pages in any order (a copy that only loads: 39..42 us).
 // - D = 64, 509 rows under a window: 59 us, 17 GFLOP, floor 15: vector
-//   instructions (two thirds of the issue slots).
+//   instructions (63% of the issue slots; the matrix cores are busy 25%).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -841,7 +841,9 @@ __global__ void __launch_bounds__(256) kv_attn_join_kernel(AttnArgs a) {
 // 21.7 us with one or two, 24.3 with four).  One sequence is cut into as many
 // splits as fit at once, several into twice that, which evens out their unlike
 // lengths (48 sequences: 49 us against 126; one sequence of 262139 and 32773
-// positions: 81 and 33 us with twice, 74 and 22 with once).
+// positions: 81 and 33 us with twice, 74 and 22 with once).  (Both sides of
+// each comparison are of one build; its split kernels were 2..7% slower than
+// these.)
 struct Shape {
     int rt, target, min_chunk, nitems;
 };
@@ -861,7 +863,11 @@ Shape attn_shape(const KvCache &c, const KvSeqs &sq, int hq) {
     // in one piece takes 0.25 us a tile of 32 (D = 128, 8 KV heads; 1024
     // sequences, most of them without rows, tables of 8192 positions: 38 us
     // shared against 63 with one live sequence, 75 against 65 with 16; 8192
-    // sequences: 236 against 64; tables of 131072: 63 against 895)
+    // sequences: 236 against 64; tables of 131072: 63 against 895).
+    // Nor are contexts shared where tiles alone are half of the workgroups that
+    // fit: right for lengths alike (8000 positions, one of 16384: 209 us at 95
+    // sequences, shared, 220 at 96), wrong for one of 131072 among others of
+    // 300 (51 us at 95, 992 at 96), which the lengths alone would tell.
     s.target = most > s.min_chunk && share > tiles && sq.nseq <= 4 * most ? (int)share : 0;
     s.nitems = (int)(tiles + s.target);
     return s;
