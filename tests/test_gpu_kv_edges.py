@@ -100,3 +100,34 @@ def test_small_elements_beside_a_large_one(D, grp):
     got = binding.kv_attn(cache, dev(q), pages, lens, out=torch.empty(1, grp, D, device="cuda"))
     torch.cuda.synchronize()
     assert (np.abs(got.cpu().numpy() - want) <= kv_ref.attention_bound(want, mass, amax, False)).all()
+
+
+@pytest.mark.parametrize("D,grp,n", [(64, 4, 1), (128, 6, 1), (256, 6, 1), (64, 4, 9), (128, 4, 9), (256, 4, 9), (64, 4, 260)])
+@pytest.mark.parametrize("pages", [5, 90], ids=["one piece", "split"])
+def test_queries_and_outputs_of_any_layout(D, grp, n, pages):
+    """The same bits for queries and outputs as a GEMV leaves and reads them, inside wider rows, at odd places, and for
+    one query row seen as many; what lies around an output stays."""
+    rng = np.random.default_rng(D + n)
+    hkv, length = 2, 32 * pages - 3
+    cache = binding.KVCache(pages, hkv, D, 32)
+    table, lens = dev(rng.permutation(pages)[None].astype(np.int32)), dev(np.array([max(length, n)], np.int32))
+    binding.kv_append(cache, *(torch.randn(length, hkv, D, device="cuda") for _ in range(2)), table, dev(np.array([length], np.int32)))
+    hq = hkv * grp
+    q = torch.randn(n, hq, D, device="cuda").half()
+    want = binding.kv_attn(cache, q, table, lens)
+    wide = torch.zeros(n, hq + 3, D + 5, device="cuda").half()
+    wide[:, 2:-1, 1:D + 1] = q
+    gated = torch.full((hq, 2, D, n), 7.0, device="cuda").half()
+    gated[:, 0] = q.permute(1, 2, 0)
+    far = torch.zeros(n, 2, hq, D, device="cuda").half()
+    far[:, 1] = q
+    for view in (wide[:, 2:-1, 1:D + 1], gated[:, 0].permute(2, 0, 1), far[:, 1], q.permute(1, 2, 0).contiguous().permute(2, 0, 1)):
+        assert torch.equal(binding.kv_attn(cache, view, table, lens), want)
+        for dtype in (torch.float16, torch.float32):
+            around = torch.full((hq + 1, D, n + 3), 77.0, dtype=dtype, device="cuda")
+            out = around[:hq, :, 1:n + 1].permute(2, 0, 1)
+            binding.kv_attn(cache, view, table, lens, out=out)
+            assert torch.equal(out.half(), want)
+            assert (around[hq:] == 77).all() and (around[:, :, 0] == 77).all() and (around[:, :, n + 1:] == 77).all()
+    one = q[:1].expand(n, hq, D)
+    assert torch.equal(binding.kv_attn(cache, one, table, lens), binding.kv_attn(cache, one.contiguous(), table, lens))
