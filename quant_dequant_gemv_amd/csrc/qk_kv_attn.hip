@@ -391,8 +391,8 @@ kv_attn_kernel(AttnArgs a) {
             }
         }
         // row norm N: scaled by 2^e to N in [2^12, 2^13), as high as a group's
-        // sum (below 2^5/2 N) stays in fp16; the smallest elements' sixteenths
-        // are then held to 2^-33 N.  Rows below 2^-18 by 2^30, which is exact;
+        // sum (at most sqrt(32) N) stays in fp16; the smallest elements'
+        // sixteenths are then held to 2^-33 N.  Rows below 2^-18 by 2^30, which is exact;
         // infinite, NaN or zero rows as they are.
         float ss = 0.f;
 #pragma unroll
@@ -595,9 +595,9 @@ kv_attn_kernel(AttnArgs a) {
 
         // values; of places that hold nothing yet or that no row's window
         // reaches, whatever their bytes say, the step and the minimum are 0
-        // (a probability of 0 does not hide NaN).  Steps are to be below 1, and not far
-        // below: those of a tile that holds a larger one are scaled, and the
-        // sums so far with them.
+        // (a probability of 0 does not hide NaN).  Steps are to be below 1, and
+        // not far below: those of a tile that holds a larger one are scaled,
+        // and the sums so far with them.
         const bool edge = !live || x * 32 + 32 > held || x * 32 < past;
         auto largest = [&] {  // step in either half of a lane's
             uint32_t v = 0;
