@@ -536,6 +536,193 @@ int64_t qk_kv_attn_workspace_bytes(const qk_kv_cache *cache, const qk_kv_seqs *s
 int qk_kv_attn(const qk_kv_cache *cache, const qk_kv_seqs *seqs, int n_heads, const qk_heads *q, const qk_heads *out,
                float scale, int window, void *workspace, int64_t workspace_bytes, void *stream);
 
+/*
+ * The rest of a token: norms, gates and residuals between the GEMVs, the
+ * recurrent layers' convolution and recurrence, and what is read off the
+ * logits.  Views are qk_heads; an input's strides may be 0 (one row of gates
+ * for all rows, say).
+ */
+
+/* The gate's function. */
+enum { QK_ACT_NONE = 0, QK_ACT_SILU = 1, QK_ACT_SIGMOID = 2 };
+
+typedef struct qk_block {
+    const float *post_norm;   /* dim weights of the norm behind the block, or NULL (no norm)  */
+    const float *pre_norm;    /* dim weights of the next block's norm, or NULL                */
+    float eps;                /* >= 0, under the norms' root                                  */
+    float scale;              /* of what is added to the residual; finite                     */
+    int act;                  /* QK_ACT_*: of the gate                                        */
+} qk_block;
+
+/*
+ * qk_block_norm -- from one block of a model to the next, in one pass: the
+ * norm of the block's output, its gate, the scaled sum with the residual, and
+ * the norm that the next block's GEMVs read:
+ *
+ *   n = y / sqrt(mean(y^2) + eps) * post_norm     (n = y without weights)
+ *   h = residual + scale * n * act(gate)          (residual 0, act(gate) 1 where absent)
+ *   x = h / sqrt(mean(h^2) + eps) * pre_norm      (x = h without weights)
+ *
+ * with means over the dim values of a row's group: groups 1 and dim the hidden
+ * size for a block, groups the heads and dim theirs for a norm of heads.  As
+ * the x of the next GEMV, x_out is {x, 1, 0, ncols, 1}, dim x ncols fp16.
+ *
+ *   rows      0 .. 2^22     groups  1 .. 4096     dim  1 .. 32768
+ *   y         rows x groups x dim, as is each of the others
+ *   gate, residual   may be NULL
+ *   h_out, x_out     either may be NULL
+ * An output may be an input (the same view and type: residual += in place);
+ * any other overlap of an output with what the call reads or writes is
+ * QK_EINVAL_PTR, judged by the address ranges that the views span.
+ *
+ * Sums of squares are fp64, and a quotient is rounded once to fp32; the rest
+ * is fp32.  x is made of the fp32 h, whatever the type of h_out.  For exact n,
+ * h and x of the row: n within 2^-22 |n|; h within 2^-21 |scale n act| + 2^-23
+ * |h|, its e; x within 2^-22 |x| + |pre_norm| e / sqrt(mean(h^2) + eps) + 2^-20
+ * |x| max_i(e_i) / sqrt(mean(h^2) + eps); each then rounded to its type.
+ */
+int qk_block_norm(const qk_block *block, int rows, int groups, int dim, const qk_heads *y, const qk_heads *gate,
+                  const qk_heads *residual, const qk_heads *h_out, const qk_heads *x_out, void *stream);
+
+/*
+ * The rows of one call and the sequences they continue, for layers that carry
+ * a state of fixed size: sequence s owns rows q_start[s] .. q_start[s+1] - 1 (n
+ * of them).  Its state is read from slot slots[s] of the layer's pool and left,
+ * as it is after the first commit[s] rows, in slot slots_out[s]: drafts are
+ * verified with the state of the accepted ones kept, or with the old one still
+ * there.
+ *
+ * What the arrays hold is read on the device and bounded there: rows outside
+ * every sequence are left as they were; a slot outside 0..num_slots-1 is read
+ * as zeros and not written.  q_start must not decrease (rows of a q_start
+ * that does are undefined, but in bounds).  A slot that a call writes must not
+ * be another sequence's in the same call (its state is undefined then, and
+ * that sequence's rows).
+ */
+typedef struct qk_state_seqs {
+    int rows;                 /* 0 .. 2^22                                                */
+    int nseq;                 /* 1 .. 65536                                               */
+    const int32_t *q_start;   /* device, nseq + 1 values, or NULL: rows / nseq each
+                                 (rows must then be a multiple of nseq)                   */
+    const int32_t *slots;     /* device, nseq values                                      */
+    const int32_t *slots_out; /* device, nseq values, or NULL: slots                      */
+    const int32_t *kv_len;    /* device, nseq values, or NULL: positions of the sequence, these rows
+                                 included (as in qk_kv_seqs); one whose rows are its first (kv_len
+                                 <= n) starts from zeros.  NULL: every sequence goes on   */
+    const int32_t *commit;    /* device, nseq values, taken into 0..n, or NULL: all rows.
+                                 0: nothing is written                                    */
+} qk_state_seqs;
+
+/* The short causal convolution of a recurrent layer, and its state: the last
+ * taps - 1 rows of its input. */
+typedef struct qk_conv {
+    float *pool;              /* fp32 [num_slots][taps - 1][channels], oldest row first; 16-byte
+                                 aligned                                                  */
+    int64_t num_slots;        /* 1 .. 2^31 - 1                                            */
+    int channels;             /* 1 .. 65536                                               */
+    int taps;                 /* 2 .. 8                                                   */
+    const float *weight;      /* [channels][taps], the current row's last                 */
+    const float *bias;        /* [channels] or NULL                                       */
+} qk_conv;
+
+/*
+ * qk_conv_silu -- y[t][c] = act(bias[c] + sum_j weight[c][j] x[t - taps + 1 + j][c]),
+ * rows before a sequence's first from its state.
+ *
+ *   act    QK_ACT_SILU or QK_ACT_NONE (QK_EINVAL_FLAGS otherwise)
+ *   x      rows x 1 x channels (head says nothing)
+ *   y      the same, or NULL: the state alone
+ * fp32 sums in the order of the taps, rounded once to the type of y: within
+ * 2^-20 (|bias| + sum_j |weight x|) + 2^-22 |y| and that rounding.  y overlaps nothing
+ * that the call reads or writes.
+ */
+int qk_conv_silu(const qk_conv *conv, const qk_state_seqs *seqs, int act, const qk_heads *x, const qk_heads *y,
+                 void *stream);
+
+/* The state of a gated delta recurrence: a matrix a value head. */
+typedef struct qk_delta {
+    float *pool;              /* fp32 [num_slots][v_heads][value_dim][key_dim], 16-byte aligned */
+    int64_t num_slots;        /* 1 .. 2^31 - 1                                            */
+    int k_heads, v_heads;     /* 1 .. 4096, v_heads a multiple of k_heads                 */
+    int key_dim;              /* 64 or 128                                                */
+    int value_dim;            /* a multiple of 32, 32 .. 512                              */
+} qk_delta;
+
+/* What the rows of a call bring; every p a device pointer. */
+typedef struct qk_delta_rows {
+    qk_heads q, k;            /* rows x k_heads x key_dim                                 */
+    qk_heads v;               /* rows x v_heads x value_dim                               */
+    qk_heads alpha, beta;     /* rows x v_heads (elem says nothing)                       */
+    const float *A;           /* v_heads values <= 0, or NULL: alpha is the log decay, beta the step */
+    const float *dt_bias;     /* v_heads values, or NULL: 0 (NULL without A)              */
+    float eps;                /* >= 0, of the rows' norm                                  */
+    float scale;              /* of the outputs; finite                                   */
+    int norm;                 /* 1: q / sqrt(sum(q^2) + eps), and k so; 0: as they are    */
+} qk_delta_rows;
+
+/*
+ * qk_delta_rule -- the gated delta recurrence of a DeltaNet layer over the rows
+ * of each sequence, for every value head h (its key head h / (v_heads / k_heads)):
+ *
+ *   a_t = exp(g_t),  g_t = A log(1 + e^(alpha_t + dt_bias)),  b_t = 1 / (1 + e^-beta_t)
+ *   u_t = b_t (v_t - a_t S_{t-1} k_t),  S_t = a_t S_{t-1} + u_t k_t^T,  out_t = scale S_t q_t
+ *
+ * (the recurrence and its state [48,128,128] of the dossier's design-doc prompt,
+ * "SSM / GATED DELTANET LAYERS").  A g above 0 counts as 0.
+ *
+ *   out    rows x v_heads x value_dim, overlapping nothing that the call reads or
+ *          writes; or NULL: the state alone
+ *   nseq x v_heads x value_dim is at most 2^27
+ *   workspace  qk_delta_workspace_bytes bytes (16-byte aligned; NULL when that is
+ *          0), for this call until it has run: calls that may overlap, captured
+ *          ones among them, need workspaces of their own
+ * States, sums and decays are fp32.  Sums of squares of rows of q and k must be
+ * below 2^126.  A non-finite value of a row makes that head's later rows of its
+ * sequence and its state undefined, and touches no other sequence or head.
+ */
+int64_t qk_delta_workspace_bytes(const qk_delta *delta, const qk_state_seqs *seqs);
+int qk_delta_rule(const qk_delta *delta, const qk_state_seqs *seqs, const qk_delta_rows *in, const qk_heads *out,
+                  void *workspace, int64_t workspace_bytes, void *stream);
+
+/* What qk_logprobs finds for each row; every pointer a device pointer. */
+typedef struct qk_probs {
+    const int32_t *tokens;    /* [rows][ntok] given tokens, or NULL (ntok 0)              */
+    float *token_lp;          /* [rows][ntok] their log probabilities                     */
+    float *lse;               /* [rows] log sum_v exp(scale z_v), or NULL                 */
+    float *entropy;           /* [rows] -sum_v p_v log p_v, or NULL                       */
+    int32_t *top_ids;         /* [rows][top] the largest logits' tokens, the largest first */
+    float *top_lp;            /* [rows][top] their log probabilities                      */
+    int ntok;                 /* 0 .. 1024                                                */
+    int top;                  /* 0 .. 64                                                  */
+} qk_probs;
+
+/*
+ * qk_logprobs -- p = softmax(scale * z) over the vocabulary for each row of
+ * logits: log probabilities of given tokens (drafts to verify, a text to
+ * score), the entropy, and the `top` most probable tokens.
+ *
+ *   logits    rows x 1 x vocab, fp32 or fp16: y of the head's GEMV is
+ *             {y, 1, 0, ncols, 0} (head says nothing)
+ *   rows      0 .. 2^22     vocab  1 .. 2^30
+ *   scale     0 < scale <= 2^64 (1 / temperature)
+ *   workspace as for qk_kv_attn, qk_logprobs_workspace_bytes bytes
+ * At least one of the outputs is asked for.  Outputs overlap nothing that the
+ * call reads or writes.
+ *
+ * A logit of -inf is a masked token: its log probability is -inf, and it is no
+ * alternative; where fewer than `top` are left, ids are -1 with -inf.  Equal
+ * logits (-0 and 0 are) go by the lower index.  A token outside 0..vocab-1 is
+ * none: 0.  A row with no token left: lse -inf, entropy 0.  A NaN or +inf in
+ * a row makes its lse, entropy and log probabilities NaN (NaN is no
+ * alternative).  Sums are fp32 over terms 2^x of the distance to the row's
+ * largest logit m: log probabilities within 2^-20 (1 + scale |z - m|), the
+ * entropy within 2^-18 (1 + log vocab), lse within 2^-20 + 2^-23 scale |m|
+ * of the exact values for logits below 2^125 / scale.
+ */
+int64_t qk_logprobs_workspace_bytes(const qk_heads *logits, int rows, int64_t vocab, int top);
+int qk_logprobs(const qk_heads *logits, int rows, int64_t vocab, float scale, const qk_probs *probs, void *workspace,
+                int64_t workspace_bytes, void *stream);
+
 /* Bytes per 256-weight superblock: 144 / 176 / 210, or -1 for a bad type. */
 int qk_block_bytes(int type);
 

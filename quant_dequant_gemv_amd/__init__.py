@@ -17,6 +17,7 @@ _BINDING_NAMES = {
     "qk_gemv", "qk_dequant", "qk_block_bytes", "qk_row_bytes", "qk_strerror", "qk_version",
     "gemv", "dequant", "load_library", "QKError", "LIB_PATH",
     "Rope", "KVCache", "norm_rope", "kv_append", "kv_read", "kv_attn",
+    "ConvState", "DeltaState", "LogProbs", "block_norm", "conv_silu", "delta_rule", "logprobs",
 }
 
 

@@ -8,6 +8,7 @@ raises -- there is no fallback.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -26,7 +27,10 @@ EXPORTS = ("qk_gemv", "qk_gemv_ex", "qk_gemv_swiglu", "qk_gemv_batch", "qk_dequa
            "qk_chain_plan_bytes", "qk_chain_plan", "qk_chain_workspace_bytes", "qk_gemv_chain",
            "qk_gemv_chain_noalloc",
            "qk_norm_rope", "qk_kv_page_bytes", "qk_kv_append", "qk_kv_read", "qk_kv_attn_workspace_bytes",
-           "qk_kv_attn")
+           "qk_kv_attn",
+           "qk_block_norm", "qk_conv_silu", "qk_delta_workspace_bytes", "qk_delta_rule",
+           "qk_logprobs_workspace_bytes", "qk_logprobs")
+ACT_NONE, ACT_SILU, ACT_SIGMOID = 0, 1, 2  # QK_ACT_*
 CHAIN_TIMEOUT = 0x1  # QK_CHAIN_TIMEOUT: bit of the chain workspace's first word
 CHAIN_NOALLOC_MAX_STEPS = 4094  # QK_CHAIN_NOALLOC_MAX_STEPS
 
@@ -67,6 +71,44 @@ class qk_kv_seqs(ctypes.Structure):
     """struct qk_kv_seqs of include/qkgemv.h."""
     _fields_ = [("rows", ctypes.c_int), ("nseq", ctypes.c_int), ("max_pages", ctypes.c_int),
                 ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p)]
+
+
+class qk_block(ctypes.Structure):
+    """struct qk_block of include/qkgemv.h."""
+    _fields_ = [("post_norm", ctypes.c_void_p), ("pre_norm", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("act", ctypes.c_int)]
+
+
+class qk_state_seqs(ctypes.Structure):
+    """struct qk_state_seqs of include/qkgemv.h."""
+    _fields_ = [("rows", ctypes.c_int), ("nseq", ctypes.c_int), ("q_start", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("slots_out", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("commit", ctypes.c_void_p)]
+
+
+class qk_conv(ctypes.Structure):
+    """struct qk_conv of include/qkgemv.h."""
+    _fields_ = [("pool", ctypes.c_void_p), ("num_slots", ctypes.c_int64), ("channels", ctypes.c_int), ("taps", ctypes.c_int),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class qk_delta(ctypes.Structure):
+    """struct qk_delta of include/qkgemv.h."""
+    _fields_ = [("pool", ctypes.c_void_p), ("num_slots", ctypes.c_int64), ("k_heads", ctypes.c_int), ("v_heads", ctypes.c_int),
+                ("key_dim", ctypes.c_int), ("value_dim", ctypes.c_int)]
+
+
+class qk_delta_rows(ctypes.Structure):
+    """struct qk_delta_rows of include/qkgemv.h."""
+    _fields_ = [("q", qk_heads), ("k", qk_heads), ("v", qk_heads), ("alpha", qk_heads), ("beta", qk_heads),
+                ("A", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("norm", ctypes.c_int)]
+
+
+class qk_probs(ctypes.Structure):
+    """struct qk_probs of include/qkgemv.h."""
+    _fields_ = [("tokens", ctypes.c_void_p), ("token_lp", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("entropy", ctypes.c_void_p), ("top_ids", ctypes.c_void_p), ("top_lp", ctypes.c_void_p),
+                ("ntok", ctypes.c_int), ("top", ctypes.c_int)]
 
 
 class QKError(RuntimeError):
@@ -132,6 +174,19 @@ def load_library(path: str = LIB_PATH):
     lib.qk_kv_attn_workspace_bytes.restype = i64
     lib.qk_kv_attn.argtypes = [C, S, c_int, H, H, ctypes.c_float, c_int, P, i64, P]
     lib.qk_kv_attn.restype = c_int
+    B, T, V, D, I, O = (ctypes.POINTER(t) for t in (qk_block, qk_state_seqs, qk_conv, qk_delta, qk_delta_rows, qk_probs))
+    lib.qk_block_norm.argtypes = [B, c_int, c_int, c_int, H, H, H, H, H, P]
+    lib.qk_block_norm.restype = c_int
+    lib.qk_conv_silu.argtypes = [V, T, c_int, H, H, P]
+    lib.qk_conv_silu.restype = c_int
+    lib.qk_delta_workspace_bytes.argtypes = [D, T]
+    lib.qk_delta_workspace_bytes.restype = i64
+    lib.qk_delta_rule.argtypes = [D, T, I, H, P, i64, P]
+    lib.qk_delta_rule.restype = c_int
+    lib.qk_logprobs_workspace_bytes.argtypes = [H, c_int, i64, c_int]
+    lib.qk_logprobs_workspace_bytes.restype = i64
+    lib.qk_logprobs.argtypes = [H, c_int, i64, ctypes.c_float, O, P, i64, P]
+    lib.qk_logprobs.restype = c_int
     _lib = lib
     return lib
 
@@ -239,6 +294,35 @@ def qk_kv_attn_workspace_bytes(cache, seqs, n_heads: int) -> int:
 def qk_kv_attn(cache, seqs, n_heads: int, q, out, scale: float, window: int, workspace, workspace_bytes: int,
                stream: int = 0) -> int:
     return load_library().qk_kv_attn(cache, seqs, n_heads, q, out, scale, window, workspace, workspace_bytes, stream)
+
+
+def qk_block_norm(block, rows: int, groups: int, dim: int, y, gate, residual, h_out, x_out, stream: int = 0) -> int:
+    """block: a qk_block; y, gate, residual, h_out, x_out: qk_heads (all but y may be None)."""
+    return load_library().qk_block_norm(block, rows, groups, dim, y, gate, residual, h_out, x_out, stream)
+
+
+def qk_conv_silu(conv, seqs, act: int, x, y, stream: int = 0) -> int:
+    """conv: qk_conv; seqs: qk_state_seqs; x, y: qk_heads (y or None)."""
+    return load_library().qk_conv_silu(conv, seqs, act, x, y, stream)
+
+
+def qk_delta_workspace_bytes(delta, seqs) -> int:
+    return load_library().qk_delta_workspace_bytes(delta, seqs)
+
+
+def qk_delta_rule(delta, seqs, rows, out, workspace, workspace_bytes: int, stream: int = 0) -> int:
+    """delta: qk_delta; seqs: qk_state_seqs; rows: qk_delta_rows; out: qk_heads or None."""
+    return load_library().qk_delta_rule(delta, seqs, rows, out, workspace, workspace_bytes, stream)
+
+
+def qk_logprobs_workspace_bytes(logits, rows: int, vocab: int, top: int) -> int:
+    return load_library().qk_logprobs_workspace_bytes(logits, rows, vocab, top)
+
+
+def qk_logprobs(logits, rows: int, vocab: int, scale: float, probs, workspace, workspace_bytes: int,
+                stream: int = 0) -> int:
+    """logits: qk_heads; probs: qk_probs."""
+    return load_library().qk_logprobs(logits, rows, vocab, scale, probs, workspace, workspace_bytes, stream)
 
 
 # ---------------------------------------------------------------- torch helpers
@@ -489,7 +573,7 @@ class Chain:
 # microseconds on the device, so what is right is found right in a few steps
 # here, and put into words only where it is not.
 
-_torch = _f16 = None  # set by the first KVCache or Rope, which every call here takes: torch, {float16: 1, float32: 0}
+_torch = _f16 = None  # set by the first KVCache, Rope or state, or by a call that takes none: torch, {float16: 1, float32: 0}
 
 
 def _start():
@@ -768,3 +852,241 @@ def kv_attn(cache: KVCache, q, pages, kv_len, q_start=None, scale: float | None 
     if rc != QK_OK:
         raise QKError(rc, "qk_kv_attn")
     return out
+
+
+# ------------------------------------------------ the rest of a token (torch)
+
+_ACTS = {"none": ACT_NONE, "silu": ACT_SILU, "sigmoid": ACT_SIGMOID}
+
+
+def _act_arg(act, allowed):
+    if act not in allowed:
+        raise ValueError(f"act must be one of {', '.join(map(repr, allowed))}, got {act!r}")
+    return _ACTS[act]
+
+
+def _float_arg(t, name, shape):
+    """The address of a contiguous float32 tensor of this shape, or None for None."""
+    if t is None:
+        return None
+    _need(t, name, _torch.float32)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _matrix_arg(t, name, rows=None, n=None, by_head=False):
+    """The qk_heads of a tensor [rows, n] of any strides: n elements of one head, or (by_head) one element of n heads."""
+    try:
+        f16 = _f16[t.dtype]
+        r, m = t.shape
+        if (rows is None or r == rows) and (n is None or m == n):
+            s, e = t.stride()
+            return qk_heads(t.data_ptr(), s, e, 0, f16) if by_head else qk_heads(t.data_ptr(), s, 0, e, f16)
+    except (AttributeError, KeyError, ValueError):
+        pass
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in _f16:
+        raise TypeError(f"{name} must be torch.float16 or torch.float32, got {t.dtype}")
+    raise ValueError(f"{name} must have shape [{'rows' if rows is None else rows}, {'n' if n is None else n}], "
+                     f"got {tuple(t.shape)}")
+
+
+def _state_seqs_arg(rows, slots, slots_out, q_start, kv_len, commit):
+    """The qk_state_seqs of a call."""
+    if rows > _INT_MAX:
+        raise QKError(QK_EINVAL_SHAPE, "qk_state_seqs")
+    p = _int32_arg(slots, "slots", (None,))
+    nseq = slots.shape[0]
+    return qk_state_seqs(rows, nseq, None if q_start is None else _int32_arg(q_start, "q_start", (nseq + 1,)), p,
+                         *(None if t is None else _int32_arg(t, name, (nseq,))
+                           for t, name in ((slots_out, "slots_out"), (kv_len, "kv_len"), (commit, "commit"))))
+
+
+def _workspace(workspace, need, device):
+    """The tensor (or None) and its bytes: the caller's, or one allocated here."""
+    if workspace is None:
+        return (_torch.empty(need, dtype=_torch.uint8, device=device) if need > 0 else None), max(need, 0)
+    _need(workspace, "workspace", _torch.uint8)
+    return workspace, workspace.numel()
+
+
+def block_norm(y, post_norm=None, gate=None, act: str = "silu", scale: float = 1.0, residual=None, pre_norm=None,
+               eps: float = 1e-6, h_out=None, x_out=None, stream=None):
+    """From one block to the next (qk_block_norm), y [rows, groups, dim]:
+
+        h = residual + scale * norm(y, post_norm) * act(gate),  x = norm(h, pre_norm)
+
+    post_norm, pre_norm: float32 [dim] or None (no norm); gate, residual: as y
+    or None; act of the gate: "silu", "sigmoid" or "none".  h is stored where
+    h_out is given (it may be residual).  Returns (h_out, x_out): x float16
+    contiguous unless given, None where h_out is given and neither pre_norm
+    nor x_out."""
+    torch = _start()
+    ya = _heads_arg(y, "y")
+    shape = rows, groups, dim = y.shape
+    block = qk_block(_float_arg(post_norm, "post_norm", (dim,)), _float_arg(pre_norm, "pre_norm", (dim,)), eps, scale,
+                     _act_arg(act, _ACTS))
+    dev = _one_device(y, post_norm, gate, residual, pre_norm, h_out, x_out,
+                      names="y post_norm gate residual pre_norm h_out x_out")
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return block_norm(y, post_norm, gate, act, scale, residual, pre_norm, eps, h_out, x_out)
+    if max(shape) > _INT_MAX:
+        raise QKError(QK_EINVAL_SHAPE, "qk_block_norm")
+    if x_out is None and (h_out is None or pre_norm is not None):
+        x_out = torch.empty(shape, dtype=torch.float16, device=y.device)
+    rc = _lib.qk_block_norm(block, rows, groups, dim, ya, *(None if t is None else _heads_arg(t, name, *shape) for t, name in
+                                                           ((gate, "gate"), (residual, "residual"), (h_out, "h_out"),
+                                                            (x_out, "x_out"))), _current(dev))
+    if rc != QK_OK:
+        raise QKError(rc, "qk_block_norm")
+    return h_out, x_out
+
+
+class ConvState:
+    """The short causal convolution of a recurrent layer (qk_conv) and its
+    state: weight float32 [channels, taps] (the current row's last), bias
+    float32 [channels] or None.  pool: float32 device tensor [num_slots,
+    taps - 1, channels], oldest row first (None: allocated here, zeros)."""
+
+    def __init__(self, num_slots: int, weight, bias=None, pool=None):
+        torch = _start()
+        _need(weight, "weight", torch.float32)
+        if weight.dim() != 2:
+            raise ValueError(f"weight must have shape [channels, taps], got {tuple(weight.shape)}")
+        C, taps = weight.shape
+        if not (1 <= num_slots <= _INT_MAX and 1 <= C <= 65536 and 2 <= taps <= 8):
+            raise QKError(QK_EINVAL_SHAPE, "ConvState")
+        if pool is None:
+            pool = torch.zeros((num_slots, taps - 1, C), dtype=torch.float32, device=weight.device)
+        _float_arg(pool, "pool", (num_slots, taps - 1, C))
+        self.pool, self.weight, self.bias = pool, weight, bias
+        self.num_slots, self.channels, self.taps = num_slots, C, taps
+        self._c = qk_conv(pool.data_ptr(), num_slots, C, taps, weight.data_ptr(), _float_arg(bias, "bias", (C,)))
+
+
+class DeltaState:
+    """The state of a gated delta recurrence (qk_delta): pool, a float32 device
+    tensor [num_slots, v_heads, value_dim, key_dim] (None: allocated here,
+    zeros)."""
+
+    def __init__(self, num_slots: int, k_heads: int, v_heads: int, key_dim: int = 128, value_dim: int = 128, device="cuda",
+                 pool=None):
+        torch = _start()
+        shape = (num_slots, v_heads, value_dim, key_dim)
+        if not all(1 <= n <= _INT_MAX for n in (*shape, k_heads)):
+            raise QKError(QK_EINVAL_SHAPE, "DeltaState")
+        self._c = qk_delta(None, num_slots, k_heads, v_heads, key_dim, value_dim)
+        if qk_delta_workspace_bytes(self._c, qk_state_seqs(0, 1)) < 0:
+            raise QKError(QK_EINVAL_SHAPE, "DeltaState")
+        if pool is None:
+            pool = torch.zeros(shape, dtype=torch.float32, device=device)
+        self._c.pool = _float_arg(pool, "pool", shape)
+        self.pool = pool
+        self.num_slots, self.k_heads, self.v_heads, self.key_dim, self.value_dim = num_slots, k_heads, v_heads, key_dim, value_dim
+
+
+def conv_silu(conv: ConvState, x, slots, slots_out=None, q_start=None, kv_len=None, commit=None, act: str = "silu",
+              out=None, state_only: bool = False, stream=None):
+    """The convolution of new rows x [rows, channels] behind their sequences'
+    states (see qk_state_seqs: slots, slots_out, kv_len, commit int32 [nseq],
+    q_start int32 [nseq + 1]; all but slots may be None), then SiLU (act
+    "none": without).  Returns out, [rows, channels] of the type of x unless
+    given, None with state_only.  Rows of no sequence are left as they were:
+    undefined in an out that is allocated here."""
+    torch = _torch
+    xa = _matrix_arg(x, "x", None, conv.channels)
+    rows = x.shape[0]
+    a = _act_arg(act, ("silu", "none"))
+    seqs = _state_seqs_arg(rows, slots, slots_out, q_start, kv_len, commit)
+    dev = _one_device(x, slots, slots_out, q_start, kv_len, commit, out, conv.pool, conv.weight, conv.bias,
+                      names="x slots slots_out q_start kv_len commit out pool weight bias")
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return conv_silu(conv, x, slots, slots_out, q_start, kv_len, commit, act, out, state_only)
+    if state_only and out is not None:
+        raise ValueError("an out with state_only")
+    if out is None and not state_only:
+        out = torch.empty_like(x)
+    rc = _lib.qk_conv_silu(conv._c, seqs, a, xa, None if out is None else _matrix_arg(out, "out", rows, conv.channels),
+                           _current(dev))
+    if rc != QK_OK:
+        raise QKError(rc, "qk_conv_silu")
+    return out
+
+
+def delta_rule(state: DeltaState, q, k, v, alpha, beta, slots, slots_out=None, q_start=None, kv_len=None, commit=None,
+               A=None, dt_bias=None, norm: bool = True, eps: float = 1e-6, scale: float | None = None, out=None,
+               state_only: bool = False, workspace=None, stream=None):
+    """The gated delta recurrence (qk_delta_rule) of new rows: q, k [rows, k
+    heads, key_dim], v [rows, v heads, value_dim], alpha, beta [rows, v heads]
+    -- raw gates with A (and dt_bias, float32 [v heads]), log decay and step
+    without.  norm: q and k are brought to length 1 first; scale of the
+    outputs, None: key_dim ** -0.5.  Sequences as in conv_silu.  Returns out,
+    float32 [rows, v heads, value_dim] unless given, None with state_only.
+    workspace: uint8 device tensor of at least qk_delta_workspace_bytes bytes
+    (None: allocated for the call).  Rows of no sequence are left as they were:
+    undefined in an out that is allocated here."""
+    torch = _torch
+    hk, hv, dk, dv = state.k_heads, state.v_heads, state.key_dim, state.value_dim
+    qa = _heads_arg(q, "q", None, hk, dk)
+    rows = q.shape[0]
+    ins = qk_delta_rows(qa, _heads_arg(k, "k", rows, hk, dk), _heads_arg(v, "v", rows, hv, dv),
+                        _matrix_arg(alpha, "alpha", rows, hv, True), _matrix_arg(beta, "beta", rows, hv, True),
+                        _float_arg(A, "A", (hv,)), _float_arg(dt_bias, "dt_bias", (hv,)), eps,
+                        dk ** -0.5 if scale is None else scale, int(norm))
+    if dt_bias is not None and A is None:
+        raise ValueError("dt_bias without A")
+    seqs = _state_seqs_arg(rows, slots, slots_out, q_start, kv_len, commit)
+    dev = _one_device(q, k, v, alpha, beta, slots, slots_out, q_start, kv_len, commit, A, dt_bias, out, state.pool, workspace,
+                      names="q k v alpha beta slots slots_out q_start kv_len commit A dt_bias out pool workspace")
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return delta_rule(state, q, k, v, alpha, beta, slots, slots_out, q_start, kv_len, commit, A, dt_bias, norm, eps,
+                              scale, out, state_only, workspace)
+    if state_only and out is not None:
+        raise ValueError("an out with state_only")
+    if out is None and not state_only:
+        out = torch.empty((rows, hv, dv), dtype=torch.float32, device=q.device)
+    ws, need = _workspace(workspace, _lib.qk_delta_workspace_bytes(state._c, seqs), q.device)
+    rc = _lib.qk_delta_rule(state._c, seqs, ins, None if out is None else _heads_arg(out, "out", rows, hv, dv),
+                            None if ws is None else ws.data_ptr(), need, _current(dev))
+    if rc != QK_OK:
+        raise QKError(rc, "qk_delta_rule")
+    return out
+
+
+LogProbs = collections.namedtuple("LogProbs", "token_lp lse entropy top_ids top_lp")
+
+
+def logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, workspace=None, stream=None):
+    """Log probabilities under softmax(scale * logits), logits [rows, vocab]
+    (qk_logprobs): LogProbs of token_lp float32 as tokens (int32 [rows, n] or
+    None), lse and entropy float32 [rows], and of the `top` most probable
+    tokens top_ids int32 and top_lp float32 [rows, top] (None for top 0).
+    workspace: uint8 device tensor of at least qk_logprobs_workspace_bytes
+    bytes (None: allocated for the call)."""
+    torch = _start()
+    za = _matrix_arg(logits, "logits")
+    rows, vocab = logits.shape
+    tp = None if tokens is None else _int32_arg(tokens, "tokens", (rows, None))
+    ntok = 0 if tokens is None else tokens.shape[1]
+    if max(rows, ntok) > _INT_MAX or not 0 <= top <= 64:
+        raise QKError(QK_EINVAL_SHAPE, "qk_logprobs")
+    dev = _one_device(logits, tokens, workspace, names="logits tokens workspace")
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return logprobs(logits, tokens, top, scale, workspace)
+    f32 = dict(dtype=torch.float32, device=logits.device)
+    r = LogProbs(None if tokens is None else torch.empty((rows, ntok), **f32), torch.empty(rows, **f32),
+                 torch.empty(rows, **f32), torch.empty((rows, top), dtype=torch.int32, device=logits.device) if top else None,
+                 torch.empty((rows, top), **f32) if top else None)
+    ws, need = _workspace(workspace, _lib.qk_logprobs_workspace_bytes(za, rows, vocab, top), logits.device)
+    out = qk_probs(tp if ntok else None, r.token_lp.data_ptr() if ntok else None, r.lse.data_ptr(), r.entropy.data_ptr(),
+                   r.top_ids.data_ptr() if top else None, r.top_lp.data_ptr() if top else None, ntok, top)
+    rc = _lib.qk_logprobs(za, rows, vocab, scale, out, None if ws is None else ws.data_ptr(), need, _current(dev))
+    if rc != QK_OK:
+        raise QKError(rc, "qk_logprobs")
+    return r

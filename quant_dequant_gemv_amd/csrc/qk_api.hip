@@ -201,6 +201,76 @@ constexpr int MAX_HEADS = 4096;
 constexpr int64_t MAX_ROW_HEADS = (int64_t)1 << 25;
 constexpr int64_t MAX_SEQ_HEADS = (int64_t)1 << 21;  // sequences with rows x KV heads (attention)
 
+// ---- the rest of a token
+
+// An output's span against the inputs' (an input of the same view and type is
+// its own: in place).
+struct View {
+    const qk_heads *x;
+    Span s;
+};
+bool meets_another(const View &out, const View *in, int nin) {
+    for (int i = 0; i < nin; ++i)
+        if (!(in[i].x && same_view(out.x, in[i].x)) && spans_meet(out.s, in[i].s)) return true;
+    return false;
+}
+
+// Sequences of a layer with a state (host values), then their pointers.
+int check_state_seqs(const qk_state_seqs *q, int64_t num_slots) {
+    if (q->rows < 0 || q->rows > 1 << 22 || q->nseq < 1 || q->nseq > 65536) return QK_EINVAL_SHAPE;
+    if (!q->q_start && q->rows % q->nseq) return QK_EINVAL_SHAPE;
+    if (num_slots < 1 || num_slots > INT32_MAX) return QK_EINVAL_SHAPE;
+    return QK_OK;
+}
+int check_state_ptrs(const qk_state_seqs *q, Span *in, int *nin) {
+    if (!q->slots) return QK_EINVAL_PTR;
+    const int64_t n = 4 * (int64_t)q->nseq;
+    const Span s[5] = {{q->q_start, n + 4}, {q->slots, n}, {q->slots_out, n}, {q->kv_len, n}, {q->commit, n}};
+    for (const Span &x : s) {
+        if (!aligned(x.p, 4)) return QK_EINVAL_PTR;
+        in[(*nin)++] = x;
+    }
+    return QK_OK;
+}
+qk::StateSeqs to_state_seqs(const qk_state_seqs *q, int64_t num_slots) {
+    return qk::StateSeqs{q->rows, q->nseq, q->q_start, q->slots, q->slots_out, q->kv_len, q->commit, num_slots};
+}
+
+int check_delta(const qk_delta *d, const qk_state_seqs *q) {
+    if (!d || !q) return QK_EINVAL_PTR;
+    if (d->k_heads < 1 || d->v_heads < 1 || d->k_heads > MAX_HEADS || d->v_heads > MAX_HEADS || d->v_heads % d->k_heads)
+        return QK_EINVAL_SHAPE;
+    if ((d->key_dim != 64 && d->key_dim != 128) || d->value_dim < 32 || d->value_dim > 512 || d->value_dim % 32)
+        return QK_EINVAL_SHAPE;
+    const int rc = check_state_seqs(q, d->num_slots);
+    if (rc) return rc;
+    // (16 lanes a column of a state: a grid stays below 2^32 threads)
+    if ((int64_t)q->nseq * d->v_heads * d->value_dim > (int64_t)1 << 27) return QK_EINVAL_SHAPE;
+    return (int64_t)q->rows * d->v_heads > MAX_ROW_HEADS ? QK_EINVAL_SHAPE : QK_OK;
+}
+qk::DeltaState to_delta(const qk_delta *d) {
+    return qk::DeltaState{d->pool, d->k_heads, d->v_heads, d->key_dim, d->value_dim};
+}
+
+int check_probs(const qk_heads *z, int rows, int64_t vocab, int top) {
+    if (!z) return QK_EINVAL_PTR;
+    if (rows < 0 || rows > 1 << 22 || vocab < 1 || vocab > (int64_t)1 << 30 || top < 0 || top > 64) return QK_EINVAL_SHAPE;
+    return QK_OK;
+}
+qk::Probs to_probs(const qk_heads *z, int rows, int64_t vocab, float scale, const qk_probs *o, int top) {
+    qk::Probs p{to_heads(z, rows, 1), rows, (int)vocab, 0, top, scale, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+    if (o) {
+        p.ntok = o->ntok;
+        p.tokens = o->tokens;
+        p.token_lp = o->token_lp;
+        p.lse = o->lse;
+        p.entropy = o->entropy;
+        p.top_lp = o->top_lp;
+        p.top_ids = o->top_ids;
+    }
+    return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -484,6 +554,138 @@ int qk_kv_attn(const qk_kv_cache *cache, const qk_kv_seqs *seqs, int n_heads, co
                                        (hipStream_t)stream));
 }
 
+int qk_block_norm(const qk_block *b, int rows, int groups, int dim, const qk_heads *y, const qk_heads *gate,
+                  const qk_heads *residual, const qk_heads *h_out, const qk_heads *x_out, void *stream) {
+    if (!b || !y || (!h_out && !x_out)) return QK_EINVAL_PTR;
+    if (rows < 0 || rows > 1 << 22 || groups < 1 || groups > MAX_HEADS || dim < 1 || dim > 32768) return QK_EINVAL_SHAPE;
+    if ((int64_t)rows * groups > MAX_ROW_HEADS) return QK_EINVAL_SHAPE;
+    if (!(b->eps >= 0.f) || !isfinite(b->eps) || !isfinite(b->scale)) return QK_EINVAL_SHAPE;
+    if (b->act != QK_ACT_NONE && b->act != QK_ACT_SILU && b->act != QK_ACT_SIGMOID) return QK_EINVAL_FLAGS;
+    if (rows == 0) return QK_OK;
+    if (!aligned(b->post_norm, 4) || !aligned(b->pre_norm, 4)) return QK_EINVAL_PTR;
+    View in[5] = {{nullptr, {b->post_norm, 4 * (int64_t)dim}}, {nullptr, {b->pre_norm, 4 * (int64_t)dim}}}, h{}, x{};
+    int nin = 2, rc;
+    for (const qk_heads *v : {y, gate, residual}) {
+        if (!v) continue;
+        in[nin].x = v;
+        if ((rc = check_heads(v, rows, groups, dim, false, &in[nin++].s))) return rc;
+    }
+    h.x = h_out;
+    x.x = x_out;
+    if (h_out && (rc = check_heads(h_out, rows, groups, dim, true, &h.s))) return rc;
+    if (x_out && (rc = check_heads(x_out, rows, groups, dim, true, &x.s))) return rc;
+    if ((h_out && meets_another(h, in, nin)) || (x_out && meets_another(x, in, nin)) || spans_meet(h.s, x.s))
+        return QK_EINVAL_PTR;
+    const qk::BlockNorm bn{b->post_norm, b->pre_norm, b->eps, b->scale, b->act};
+    return launched(qk::launch_block_norm(bn, rows, groups, dim, to_heads(y, rows, groups), to_heads(gate, rows, groups),
+                                          to_heads(residual, rows, groups), to_heads(h_out, rows, groups),
+                                          to_heads(x_out, rows, groups), (hipStream_t)stream));
+}
+
+int qk_conv_silu(const qk_conv *c, const qk_state_seqs *seqs, int act, const qk_heads *x, const qk_heads *y,
+                 void *stream) {
+    if (!c || !seqs || !x) return QK_EINVAL_PTR;
+    if (c->channels < 1 || c->channels > 65536 || c->taps < 2 || c->taps > 8) return QK_EINVAL_SHAPE;
+    int rc = check_state_seqs(seqs, c->num_slots);
+    if (rc) return rc;
+    if (act != QK_ACT_NONE && act != QK_ACT_SILU) return QK_EINVAL_FLAGS;
+    const int rows = seqs->rows;
+    if (rows == 0) return QK_OK;
+    Span in[8], pool, sy{};
+    int nin = 0;
+    if (!c->pool || !aligned(c->pool, 16) || !c->weight || !aligned(c->weight, 4) || !aligned(c->bias, 4)) return QK_EINVAL_PTR;
+    pool = Span{c->pool, c->num_slots * (c->taps - 1) * c->channels * 4};
+    in[nin++] = Span{c->weight, 4 * (int64_t)c->channels * c->taps};
+    in[nin++] = Span{c->bias, 4 * (int64_t)c->channels};
+    if ((rc = check_state_ptrs(seqs, in, &nin))) return rc;
+    if ((rc = check_heads(x, rows, 1, c->channels, false, &in[nin++]))) return rc;
+    if (y && (rc = check_heads(y, rows, 1, c->channels, true, &sy))) return rc;
+    for (int i = 0; i < nin; ++i)
+        if (spans_meet(pool, in[i]) || spans_meet(sy, in[i])) return QK_EINVAL_PTR;
+    if (spans_meet(pool, sy)) return QK_EINVAL_PTR;
+    const qk::ConvState cs{c->pool, c->channels, c->taps, c->weight, c->bias};
+    return launched(qk::launch_conv(to_state_seqs(seqs, c->num_slots), cs, act == QK_ACT_SILU, to_heads(x, rows, 1),
+                                    to_heads(y, rows, 1), (hipStream_t)stream));
+}
+
+int64_t qk_delta_workspace_bytes(const qk_delta *delta, const qk_state_seqs *seqs) {
+    if (check_delta(delta, seqs)) return -1;
+    return seqs->rows ? qk::delta_workspace(to_state_seqs(seqs, delta->num_slots), to_delta(delta)) : 0;
+}
+
+int qk_delta_rule(const qk_delta *d, const qk_state_seqs *seqs, const qk_delta_rows *r, const qk_heads *out,
+                  void *workspace, int64_t workspace_bytes, void *stream) {
+    int rc = check_delta(d, seqs);
+    if (rc) return rc;
+    if (!r) return QK_EINVAL_PTR;
+    if (!(r->eps >= 0.f) || !isfinite(r->eps) || !isfinite(r->scale)) return QK_EINVAL_SHAPE;
+    if (r->norm != 0 && r->norm != 1) return QK_EINVAL_FLAGS;
+    const int rows = seqs->rows, hk = d->k_heads, hv = d->v_heads;
+    if (rows == 0) return QK_OK;
+    if (!d->pool || !aligned(d->pool, 16) || !aligned(r->A, 4) || !aligned(r->dt_bias, 4) || (r->dt_bias && !r->A))
+        return QK_EINVAL_PTR;
+    const Span pool{d->pool, d->num_slots * hv * d->value_dim * d->key_dim * 4};
+    Span in[12], so{};
+    int nin = 0;
+    in[nin++] = Span{r->A, 4 * (int64_t)hv};
+    in[nin++] = Span{r->dt_bias, 4 * (int64_t)hv};
+    if ((rc = check_state_ptrs(seqs, in, &nin))) return rc;
+    if ((rc = check_heads(&r->q, rows, hk, d->key_dim, false, &in[nin++])) ||
+        (rc = check_heads(&r->k, rows, hk, d->key_dim, false, &in[nin++])) ||
+        (rc = check_heads(&r->v, rows, hv, d->value_dim, false, &in[nin++])) ||
+        (rc = check_heads(&r->alpha, rows, hv, 1, false, &in[nin++])) ||
+        (rc = check_heads(&r->beta, rows, hv, 1, false, &in[nin++])))
+        return rc;
+    if (out && (rc = check_heads(out, rows, hv, d->value_dim, true, &so))) return rc;
+    const qk::StateSeqs sq = to_state_seqs(seqs, d->num_slots);
+    const int64_t need = qk::delta_workspace(sq, to_delta(d));
+    if (workspace_bytes < need) return QK_EINVAL_SHAPE;
+    if (need && (!workspace || !aligned(workspace, 16))) return QK_EINVAL_PTR;
+    const Span ws{need ? workspace : nullptr, need};
+    for (int i = 0; i < nin; ++i)
+        if (spans_meet(pool, in[i]) || spans_meet(so, in[i]) || spans_meet(ws, in[i])) return QK_EINVAL_PTR;
+    if (spans_meet(pool, so) || spans_meet(pool, ws) || spans_meet(so, ws)) return QK_EINVAL_PTR;
+    const qk::DeltaIn di{to_heads(&r->q, rows, hk), to_heads(&r->k, rows, hk), to_heads(&r->v, rows, hv),
+                         to_heads(&r->alpha, rows, hv), to_heads(&r->beta, rows, hv), r->A, r->dt_bias, r->norm, r->eps,
+                         r->scale};
+    return launched(qk::launch_delta(sq, to_delta(d), di, to_heads(out, rows, hv), workspace, (hipStream_t)stream));
+}
+
+int64_t qk_logprobs_workspace_bytes(const qk_heads *logits, int rows, int64_t vocab, int top) {
+    if (check_probs(logits, rows, vocab, top)) return -1;
+    return rows ? qk::probs_workspace(to_probs(logits, rows, vocab, 1.f, nullptr, top)) : 0;
+}
+
+int qk_logprobs(const qk_heads *logits, int rows, int64_t vocab, float scale, const qk_probs *o, void *workspace,
+                int64_t workspace_bytes, void *stream) {
+    if (!o) return QK_EINVAL_PTR;
+    int rc = check_probs(logits, rows, vocab, o->top);
+    if (rc) return rc;
+    if (!(scale > 0.f && scale <= 0x1p64f) || o->ntok < 0 || o->ntok > 1024) return QK_EINVAL_SHAPE;
+    if (!o->ntok != !o->tokens || !o->ntok != !o->token_lp || !o->top != !o->top_ids || !o->top != !o->top_lp)
+        return QK_EINVAL_PTR;
+    if (!o->ntok && !o->top && !o->lse && !o->entropy) return QK_EINVAL_PTR;
+    if (rows == 0) return QK_OK;
+    Span in[2] = {{o->tokens, 4 * (int64_t)rows * o->ntok}, {}};
+    if ((rc = check_heads(logits, rows, 1, vocab, false, &in[1]))) return rc;
+    const qk::Probs p = to_probs(logits, rows, vocab, scale, o, o->top);
+    const int64_t need = qk::probs_workspace(p);
+    if (workspace_bytes < need) return QK_EINVAL_SHAPE;
+    if (need && (!workspace || !aligned(workspace, 16))) return QK_EINVAL_PTR;
+    const Span out[6] = {{o->token_lp, 4 * (int64_t)rows * o->ntok}, {o->lse, 4 * (int64_t)rows}, {o->entropy, 4 * (int64_t)rows},
+                         {o->top_ids, 4 * (int64_t)rows * o->top}, {o->top_lp, 4 * (int64_t)rows * o->top},
+                         {need ? workspace : nullptr, need}};
+    if (!aligned(o->tokens, 4)) return QK_EINVAL_PTR;
+    for (int i = 0; i < 6; ++i) {
+        if (!aligned(out[i].p, 4)) return QK_EINVAL_PTR;
+        for (const Span &x : in)
+            if (spans_meet(out[i], x)) return QK_EINVAL_PTR;
+        for (int j = 0; j < i; ++j)
+            if (spans_meet(out[i], out[j])) return QK_EINVAL_PTR;
+    }
+    return launched(qk::launch_probs(p, workspace, (hipStream_t)stream));
+}
+
 const char *qk_strerror(int code) {
     switch (code) {
     case QK_OK: return "ok";
@@ -499,13 +701,18 @@ const char *qk_strerror(int code) {
                "head_dim 64, 128 or 256, page_size a power of two in 32..1024, rows a multiple of nseq without q_start, "
                "rot_dim even and at most head_dim, query heads a multiple of the KV heads, strides >= 0 and outputs "
                "whose elements do not coincide, at most 2^25 rows x heads and 2^21 sequences x KV heads, |scale| <= 2^64, a window >= 0, a workspace of "
-               "qk_kv_attn_workspace_bytes";
+               "qk_kv_attn_workspace_bytes; qk_block_norm 1..4096 groups of 1..32768 and a finite scale; recurrent layers "
+               "1..65536 channels, 2..8 taps, key_dim 64 or 128, value_dim a multiple of 32 in 32..512, value heads a "
+               "multiple of the key heads, at most 2^27 sequences x value heads x value_dim, a workspace of "
+               "qk_delta_workspace_bytes; qk_logprobs a vocabulary of 1..2^30, 0..1024 tokens, the top 0..64, "
+               "0 < scale <= 2^64, a workspace of qk_logprobs_workspace_bytes";
     case QK_EINVAL_PTR:
         return "invalid pointer: NULL, or W/x not 16-byte aligned, or y/out/residual not 4-byte aligned (fp16 y: 2), "
                "or an output that overlaps an input (y with W or x, out with W, a batch entry's y with any entry's "
                "W, x or y, Wp with W), or a residual that overlaps y without being y (fp32 y); heads not aligned to their type, the pool or the "
                "workspace not to 16 bytes, int32 arrays not to 4";
-    case QK_EINVAL_FLAGS: return "invalid flags: the only epilogue flag is QK_Y_F16 (0x1); interleaved is 0 or 1";
+    case QK_EINVAL_FLAGS: return "invalid flags: the only epilogue flag is QK_Y_F16 (0x1); interleaved is 0 or 1, as is "
+                                 "norm of qk_delta_rule; act is a QK_ACT_* (SILU or NONE for qk_conv_silu)";
     case QK_ELAUNCH: return g_launch_msg;
     default: return "unknown error code";
     }

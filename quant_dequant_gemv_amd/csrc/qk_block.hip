@@ -1,0 +1,235 @@
+// qk_block.hip -- the norms before and after a block with its gate and
+// residual, in one pass over the row.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "qk_launch.h"
+
+namespace qk {
+namespace block {
+
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+
+struct Args {
+    BlockNorm b;
+    int64_t units;  // rows x groups
+    int groups, dim;
+    Heads y, gate, res, h, x;
+};
+
+// Row t, group g of a view.
+__device__ __forceinline__ char *at(const Heads &v, int64_t t, int64_t g) {
+    return reinterpret_cast<char *>(v.p) + ((t * v.row + g * v.head) << (v.f16 ? 1 : 2));
+}
+
+// E elements of a group of `dim` at p, TPG threads: pieces of 4 side by side
+// (VEC), or single ones `elem` apart.  Zeros past the end.  All loads of a
+// thread are under way before the first is converted.
+template <int TPG, int E, bool VEC>
+__device__ __forceinline__ void load(const char *p, int64_t elem, bool f16, int tid, int dim, float *x) {
+    if constexpr (VEC) {
+        if (f16) {
+            h4 h[E / 4];
+#pragma unroll
+            for (int j = 0; j < E / 4; ++j) {
+                const int i = 4 * (tid + TPG * j);
+                h[j] = i < dim ? *reinterpret_cast<const h4 *>(p + 2 * i) : h4{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = (float)h[e / 4][e % 4];
+        } else {
+#pragma unroll
+            for (int j = 0; j < E / 4; ++j) {
+                const int i = 4 * (tid + TPG * j);
+                const float4 f = i < dim ? *reinterpret_cast<const float4 *>(p + 4 * i) : make_float4(0, 0, 0, 0);
+                x[4 * j] = f.x; x[4 * j + 1] = f.y; x[4 * j + 2] = f.z; x[4 * j + 3] = f.w;
+            }
+        }
+    } else if (f16) {
+        _Float16 h[E];
+        p += tid * elem * 2;
+#pragma unroll
+        for (int j = 0; j < E; ++j, p += TPG * elem * 2) h[j] = tid + TPG * j < dim ? *reinterpret_cast<const _Float16 *>(p) : (_Float16)0;
+#pragma unroll
+        for (int j = 0; j < E; ++j) x[j] = (float)h[j];
+    } else {
+        p += tid * elem * 4;
+#pragma unroll
+        for (int j = 0; j < E; ++j, p += TPG * elem * 4) x[j] = tid + TPG * j < dim ? *reinterpret_cast<const float *>(p) : 0.f;
+    }
+}
+template <int TPG, int E, bool VEC>
+__device__ __forceinline__ void store(char *p, int64_t elem, bool f16, int tid, int dim, const float *x) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int j = 0; j < E / 4; ++j) {
+            const int i = 4 * (tid + TPG * j);
+            if (i >= dim) continue;
+            const float *f = x + 4 * j;
+            if (f16) *reinterpret_cast<h4 *>(p + 2 * i) = h4{(_Float16)f[0], (_Float16)f[1], (_Float16)f[2], (_Float16)f[3]};
+            else *reinterpret_cast<float4 *>(p + 4 * i) = make_float4(f[0], f[1], f[2], f[3]);
+        }
+    } else {
+        p += (tid * elem) << (f16 ? 1 : 2);
+        const int64_t step = (TPG * elem) << (f16 ? 1 : 2);
+#pragma unroll
+        for (int j = 0; j < E; ++j, p += step) {
+            if (tid + TPG * j >= dim) continue;
+            if (f16) *reinterpret_cast<_Float16 *>(p) = (_Float16)x[j];
+            else *reinterpret_cast<float *>(p) = x[j];
+        }
+    }
+}
+
+// Sum over the TPG threads of a group: every one gets it.  Fixed order.
+template <int TPG, int THREADS> __device__ __forceinline__ double group_sum(double v, double *part, int tid) {
+#pragma unroll
+    for (int m = 1; m < (TPG < 64 ? TPG : 64); m *= 2) v += __shfl_xor(v, m);
+    if constexpr (TPG > 64) {
+        static_assert(TPG == THREADS, "one group a block above a wave");
+        __syncthreads();
+        if ((tid & 63) == 0) part[tid >> 6] = v;
+        __syncthreads();
+        v = 0;
+#pragma unroll
+        for (int w = 0; w < TPG / 64; ++w) v += part[w];
+    }
+    return v;
+}
+
+__device__ __forceinline__ float gate_of(float z, int act) {
+    return act == 0 ? z : (act == 1 ? z : 1.f) / (1.f + expf(-z));
+}
+// (fp64: no row overflows or vanishes under its root)
+__device__ __forceinline__ double root(double ss, int dim, float eps) { return 1.0 / sqrt(ss / dim + (double)eps); }
+
+// x <- x / sqrt(mean x^2 + eps) * w.  The sum of squares and the product with
+// its root are fp64: no row overflows or vanishes, and the row's elements are
+// rounded twice in all (the quotient, its weight).
+template <int TPG, int THREADS, int E, bool VEC>
+__device__ __forceinline__ void norm(float *x, const float *w, float eps, int dim, int tid, double *part) {
+    float wv[E];
+    load<TPG, E, VEC>(reinterpret_cast<const char *>(w), 1, false, tid, dim, wv);
+    double ss = 0;
+#pragma unroll
+    for (int j = 0; j < E; ++j) ss = fma((double)x[j], (double)x[j], ss);
+    const double r = root(group_sum<TPG, THREADS>(ss, part, tid), dim, eps);
+#pragma unroll
+    for (int j = 0; j < E; ++j) x[j] = (float)((double)x[j] * r) * wv[j];
+}
+
+// TPG threads a group of `dim` values, E of them each, in registers from the
+// loads to the stores: every input is read once.
+template <int TPG, int THREADS, int E, bool VEC> __global__ void __launch_bounds__(THREADS) block_norm_kernel(Args a) {
+    __shared__ double part[THREADS / 64];
+    const int tid = threadIdx.x % TPG;
+    constexpr int PER = THREADS / TPG;
+    for (int64_t u0 = (int64_t)blockIdx.x * PER; u0 < a.units; u0 += (int64_t)gridDim.x * PER) {
+        // (units past the end work on the last one and store nothing: all threads meet at the sums)
+        const int64_t u = u0 + threadIdx.x / TPG, uc = u < a.units ? u : a.units - 1;
+        const int64_t t = uc / a.groups, g = uc % a.groups;
+        float y[E], z[E], r[E];
+        load<TPG, E, VEC>(at(a.y, t, g), a.y.elem, a.y.f16, tid, a.dim, y);
+        if (a.gate.p) load<TPG, E, VEC>(at(a.gate, t, g), a.gate.elem, a.gate.f16, tid, a.dim, z);
+        if (a.res.p) load<TPG, E, VEC>(at(a.res, t, g), a.res.elem, a.res.f16, tid, a.dim, r);
+        if (a.b.post) norm<TPG, THREADS, E, VEC>(y, a.b.post, a.b.eps, a.dim, tid, part);
+        if (a.gate.p) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) y[j] *= gate_of(z[j], a.b.act);
+        }
+#pragma unroll
+        for (int j = 0; j < E; ++j) y[j] = a.res.p ? fmaf(a.b.scale, y[j], r[j]) : a.b.scale * y[j];
+        if (a.h.p && u < a.units) store<TPG, E, VEC>(at(a.h, t, g), a.h.elem, a.h.f16, tid, a.dim, y);
+        if (a.x.p) {
+            if (a.b.pre) norm<TPG, THREADS, E, VEC>(y, a.b.pre, a.b.eps, a.dim, tid, part);
+            if (u < a.units) store<TPG, E, VEC>(at(a.x, t, g), a.x.elem, a.x.f16, tid, a.dim, y);
+        }
+    }
+}
+
+// Groups too long for registers: the row's values wait in LDS between the
+// sums, one group a block.
+template <bool VEC> __global__ void __launch_bounds__(1024) block_norm_wide_kernel(Args a) {
+    constexpr int T = 1024, E = VEC ? 4 : 1;
+    extern __shared__ float row[];
+    __shared__ double part[T / 64];
+    const int tid = threadIdx.x;
+    for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
+        const int64_t t = u / a.groups, g = u % a.groups;
+        double ss = 0, r = 1;
+        // element i of a view, and E from it on
+        auto from = [&](const Heads &v, int i) { return at(v, t, g) + ((i * v.elem) << (v.f16 ? 1 : 2)); };
+        for (int i = E * tid; i < a.dim; i += E * T) {
+            float y[E];
+            load<T, E, VEC>(from(a.y, i), 1, a.y.f16, 0, E, y);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                row[i + e] = y[e];
+                ss = fma((double)y[e], (double)y[e], ss);
+            }
+        }
+        if (a.b.post) r = root(group_sum<T, T>(ss, part, tid), a.dim, a.b.eps);
+        ss = 0;
+        for (int i = E * tid; i < a.dim; i += E * T) {
+            float z[E], s[E];
+            if (a.gate.p) load<T, E, VEC>(from(a.gate, i), 1, a.gate.f16, 0, E, z);
+            if (a.res.p) load<T, E, VEC>(from(a.res, i), 1, a.res.f16, 0, E, s);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                float y = row[i + e];
+                if (a.b.post) y = (float)((double)y * r) * a.b.post[i + e];
+                if (a.gate.p) y *= gate_of(z[e], a.b.act);
+                row[i + e] = z[e] = a.res.p ? fmaf(a.b.scale, y, s[e]) : a.b.scale * y;
+                ss = fma((double)z[e], (double)z[e], ss);
+            }
+            if (a.h.p) store<T, E, VEC>(from(a.h, i), 1, a.h.f16, 0, E, z);
+        }
+        if (!a.x.p) continue;
+        if (a.b.pre) r = root(group_sum<T, T>(ss, part, tid), a.dim, a.b.eps);
+        for (int i = E * tid; i < a.dim; i += E * T) {
+            float y[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[e] = a.b.pre ? (float)((double)row[i + e] * r) * a.b.pre[i + e] : row[i + e];
+            store<T, E, VEC>(from(a.x, i), 1, a.x.f16, 0, E, y);
+        }
+    }
+}
+
+bool whole4(const Heads &v) {
+    return !v.p || (v.elem == 1 && v.row % 4 == 0 && v.head % 4 == 0 && ((uintptr_t)v.p & (v.f16 ? 7 : 15)) == 0);
+}
+
+template <int TPG, int THREADS, int E> hipError_t go(const Args &a, bool vec, hipStream_t st) {
+    constexpr int PER = THREADS / TPG;
+    const int64_t blocks = std::min<int64_t>((a.units + PER - 1) / PER, 1 << 20);  // (a grid stays below 2^32 threads)
+    if (vec) hipLaunchKernelGGL((block_norm_kernel<TPG, THREADS, E, true>), dim3((unsigned)blocks), dim3(THREADS), 0, st, a);
+    else hipLaunchKernelGGL((block_norm_kernel<TPG, THREADS, E, false>), dim3((unsigned)blocks), dim3(THREADS), 0, st, a);
+    return hipGetLastError();
+}
+
+}  // namespace block
+
+hipError_t launch_block_norm(const BlockNorm &b, int rows, int groups, int dim, const Heads &y, const Heads &gate,
+                             const Heads &res, const Heads &h, const Heads &x, hipStream_t st) {
+    using namespace block;
+    const Args a{b, (int64_t)rows * groups, groups, dim, y, gate, res, h, x};
+    const bool vec = dim % 4 == 0 && whole4(y) && whole4(gate) && whole4(res) && whole4(h) && whole4(x) &&
+                     (((uintptr_t)b.post | (uintptr_t)b.pre) & 15) == 0;
+    if (dim <= 64) return go<16, 256, 4>(a, vec, st);
+    if (dim <= 128) return go<32, 256, 4>(a, vec, st);
+    if (dim <= 512) return go<64, 256, 8>(a, vec, st);
+    if (dim <= 2048) return go<256, 256, 8>(a, vec, st);
+    if (dim <= 8192) return go<1024, 1024, 8>(a, vec, st);
+    const unsigned blocks = (unsigned)std::min<int64_t>(a.units, 1 << 20);
+    auto wide = [&](auto kern, hipError_t e) {
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(kern, dim3(blocks), dim3(1024), 4 * dim, st, a);
+        return hipGetLastError();
+    };
+    return vec ? wide(block_norm_wide_kernel<true>, lds_opt_in<block_norm_wide_kernel<true>>(4 * 32768))
+               : wide(block_norm_wide_kernel<false>, lds_opt_in<block_norm_wide_kernel<false>>(4 * 32768));
+}
+
+}  // namespace qk

@@ -1,0 +1,79 @@
+// qk_delta.h -- device side shared by the kernels of the gated delta
+// recurrence: arguments, elements of rows, gates.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qk_state.h"
+
+namespace qk {
+namespace delta {
+
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+
+struct Args {
+    StateSeqs q;
+    float *pool;              // [slots][hv][dv][DK]
+    int hv, rep, dv;          // rep: value heads a key head
+    int norm, kv_vec;         // kv_vec: rows of queries and keys are whole pieces of 4 elements
+    float eps, scale;
+    Heads qh, kh, vh, alpha, beta, out;
+    const float *A, *dt;
+};
+
+inline bool whole4(const Heads &v) {
+    return v.elem == 1 && v.row % 4 == 0 && v.head % 4 == 0 && ((uintptr_t)v.p & (v.f16 ? 7 : 15)) == 0;
+}
+
+inline Args make_args(const StateSeqs &q, const DeltaState &d, const DeltaIn &in, const Heads &out) {
+    return Args{q, d.pool, d.hv, d.hv / d.hk, d.dv, in.norm, whole4(in.q) && whole4(in.k), in.eps, in.scale,
+                in.q, in.k, in.v, in.alpha, in.beta, out, in.A, in.dt};
+}
+
+__device__ __forceinline__ float load1(const Heads &x, int64_t t, int h, int i) {
+    const int64_t o = t * x.row + h * x.head + i * x.elem;
+    return x.f16 ? (float)reinterpret_cast<const _Float16 *>(x.p)[o] : reinterpret_cast<const float *>(x.p)[o];
+}
+__device__ __forceinline__ void store1(const Heads &x, int64_t t, int h, int i, float v) {
+    const int64_t o = t * x.row + h * x.head + i * x.elem;
+    if (x.f16) reinterpret_cast<_Float16 *>(x.p)[o] = (_Float16)v;
+    else reinterpret_cast<float *>(x.p)[o] = v;
+}
+// Dimensions 64 p + 4 l .. + 3 of a row's head.
+template <int P>
+__device__ __forceinline__ void load_row(bool vec, const Heads &x, int64_t t, int h, int l, float (*r)[4]) {
+    const int64_t o = t * x.row + h * x.head;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int i = 64 * p + 4 * l;
+        if (vec && x.f16) {
+            const h4 v = *reinterpret_cast<const h4 *>(reinterpret_cast<const _Float16 *>(x.p) + o + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[p][e] = (float)v[e];
+        } else if (vec) {
+            const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(x.p) + o + i);
+            r[p][0] = v.x; r[p][1] = v.y; r[p][2] = v.z; r[p][3] = v.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[p][e] = load1(x, t, h, i + e);
+        }
+    }
+}
+
+// Log decay (never above 0) and step of a row's head.  Raw gates: g = A log(1 +
+// e^(alpha + dt)), without overflow on either side; beta through the logistic
+// function.
+struct Gate { float g, b; };
+__device__ __forceinline__ Gate gates(const Args &a, int h, float al, float be) {
+    float g = al, b = be;
+    if (a.A) {
+        const float w = al + (a.dt ? a.dt[h] : 0.f);
+        g = a.A[h] * (fmaxf(w, 0.f) + log1pf(expf(-fabsf(w))));
+        b = 1.f / (1.f + expf(-be));
+    }
+    return {g > 0.f ? 0.f : g, b};  // (NaN stays)
+}
+
+}  // namespace delta
+}  // namespace qk

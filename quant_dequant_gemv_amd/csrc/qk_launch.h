@@ -140,4 +140,55 @@ int64_t kv_attn_workspace(const KvCache &cache, const KvSeqs &seqs, int hq);
 hipError_t launch_kv_attn(const KvCache &cache, const KvSeqs &seqs, int hq, const Heads &q, const Heads &out,
                           float scale, int window, void *workspace, hipStream_t stream);
 
+// ---- the rest of a token: block norms, recurrent layers, log probabilities
+struct BlockNorm {
+    const float *post, *pre;  // weights of the norms (NULL: none)
+    float eps, scale;
+    int act;                  // of the gate: 0 none, 1 SiLU, 2 logistic
+};
+// h = res + scale * post-norm(y) * act(gate); x = pre-norm(h).  gate, res, h, x: p may be NULL.
+hipError_t launch_block_norm(const BlockNorm &b, int rows, int groups, int dim, const Heads &y, const Heads &gate,
+                             const Heads &res, const Heads &h, const Heads &x, hipStream_t stream);
+
+// Rows of sequences that carry a state (qk_state_seqs of the C ABI).
+struct StateSeqs {
+    int rows, nseq;
+    const int32_t *q_start, *slots, *slots_out, *kv_len, *commit;
+    int64_t num_slots;
+};
+struct ConvState {
+    float *pool;              // [slots][taps - 1][channels]
+    int channels, taps;
+    const float *weight, *bias;  // [channels][taps], [channels] or NULL
+};
+// y.p may be NULL (the state alone).
+hipError_t launch_conv(const StateSeqs &q, const ConvState &c, int act, const Heads &x, const Heads &y, hipStream_t stream);
+
+struct DeltaState {
+    float *pool;              // [slots][hv][dv][dk]
+    int hk, hv, dk, dv;
+};
+struct DeltaIn {
+    Heads q, k, v, alpha, beta;
+    const float *A, *dt;      // NULL: alpha is the log decay, beta the step
+    int norm;
+    float eps, scale;
+};
+int64_t delta_workspace(const StateSeqs &q, const DeltaState &d);
+// out.p may be NULL (the state alone).
+hipError_t launch_delta(const StateSeqs &q, const DeltaState &d, const DeltaIn &in, const Heads &out, void *workspace,
+                        hipStream_t stream);
+
+// Element (t, v) of the logits at p[t * row + v * elem].
+struct Probs {
+    Heads z;
+    int rows, vocab, ntok, top;
+    float scale;
+    const int32_t *tokens;    // [rows][ntok]
+    float *token_lp, *lse, *entropy, *top_lp;
+    int32_t *top_ids;
+};
+int64_t probs_workspace(const Probs &p);
+hipError_t launch_probs(const Probs &p, void *workspace, hipStream_t stream);
+
 }  // namespace qk
