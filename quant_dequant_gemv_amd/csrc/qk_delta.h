@@ -16,7 +16,7 @@ struct Args {
     StateSeqs q;
     float *pool;              // [slots][hv][dv][DK]
     int hv, rep, dv;          // rep: value heads a key head
-    int norm, kv_vec;         // kv_vec: rows of queries and keys are whole pieces of 4 elements
+    int norm, q_vec, k_vec;   // _vec: rows of heads are whole pieces of 4 elements
     float eps, scale;
     Heads qh, kh, vh, alpha, beta, out;
     const float *A, *dt;
@@ -27,8 +27,21 @@ inline bool whole4(const Heads &v) {
 }
 
 inline Args make_args(const StateSeqs &q, const DeltaState &d, const DeltaIn &in, const Heads &out) {
-    return Args{q, d.pool, d.hv, d.hv / d.hk, d.dv, in.norm, whole4(in.q) && whole4(in.k), in.eps, in.scale,
+    return Args{q, d.pool, d.hv, d.hv / d.hk, d.dv, in.norm, whole4(in.q), whole4(in.k), in.eps, in.scale,
                 in.q, in.k, in.v, in.alpha, in.beta, out, in.A, in.dt};
+}
+
+// v of the lane `CTRL` away inside a row of 16 lanes
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// Sum over 16 lanes: each gets it.
+__device__ __forceinline__ float sum16(float v) {
+    v += dpp<0xB1>(v);   // quad_perm [1,0,3,2]
+    v += dpp<0x4E>(v);   // quad_perm [2,3,0,1]
+    v += dpp<0x141>(v);  // half row mirrored
+    v += dpp<0x140>(v);  // row mirrored
+    return v;
 }
 
 __device__ __forceinline__ float load1(const Heads &x, int64_t t, int h, int i) {

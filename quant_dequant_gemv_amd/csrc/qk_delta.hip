@@ -10,91 +10,132 @@ namespace qk {
 namespace delta {
 
 constexpr int WAVES = 4;
-constexpr int COLS = 4;  // columns of the state a wave has: 16 lanes each
+constexpr int THREADS = 64 * WAVES;
+constexpr int R = 16;  // rows made ready at once: 16 lanes each
 
-// v of the lane `CTRL` away inside a row of 16 lanes
-template <int CTRL> __device__ __forceinline__ float dpp(float v) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
-}
-__device__ __forceinline__ float sum16(float v) {
-    v += dpp<0xB1>(v);   // quad_perm [1,0,3,2]
-    v += dpp<0x4E>(v);   // quad_perm [2,3,0,1]
-    v += dpp<0x141>(v);  // half row mirrored
-    v += dpp<0x140>(v);  // row mirrored
-    return v;
-}
-
-// The state of a head is held as S[Dv][Dk]: a column j (one value dimension)
-// is 16 lanes with DK / 16 values each.  With the old state S, a row is
-//   d = S k, e = S q (together),  u = beta (v - a d),  o = scale (a e + u (k.q)),  S <- a S + u k
-// so that only one sum over lanes lies between a state and the next one.
-template <int DK> __global__ void __launch_bounds__(64 * WAVES) delta_rows_kernel(Args a) {
-    constexpr int P = DK / 64;  // pieces of 4 dimensions a lane has
-    const int lane = threadIdx.x & 63, l = lane & 15;
-    const int per_head = a.dv / (COLS * WAVES);
+// The state of a head is held as S[Dv][Dk]: a column (one value dimension) is
+// 16 lanes with DK / 16 values each, a lane has CPL columns.  With the old
+// state S, a row is
+//   d = S k, e = S q (together),  u = beta (v - a d),  o = a e + u (k.q),  S <- a S + u k
+// so that only one sum over lanes lies between a state and the next one.  What
+// does not depend on the state -- normed queries and keys, k.q, gates -- is
+// made ready for R rows at once, a row to 16 lanes, and waits in LDS.
+template <int DK, int CPL> __global__ void __launch_bounds__(THREADS) delta_rows_kernel(Args a) {
+    constexpr int P = DK / 64;                 // pieces of 4 dimensions a lane has
+    constexpr int COLS = 4 * WAVES * CPL;      // columns of a block
+    __shared__ float4 q_s[R][P][16], k_s[R][P][16];
+    __shared__ float v_s[R][COLS], o_s[R][COLS];
+    __shared__ float4 g_s[R];                  // decay, step, k.q
+    const int tid = threadIdx.x, lane = tid & 63, l = lane & 15;
+    const int per_head = a.dv / COLS;
     const int64_t b = blockIdx.x;
     const int s = (int)(b / ((int64_t)per_head * a.hv)), hb = (int)(b % ((int64_t)per_head * a.hv));
-    const int h = hb / per_head, hk = h / a.rep;
-    const int col = (hb % per_head) * (COLS * WAVES) + (threadIdx.x >> 6) * COLS + (lane >> 4);
+    const int h = hb / per_head, hk = h / a.rep, c0 = (hb % per_head) * COLS;
+    const int col = (tid >> 6) * 4 * CPL + (lane >> 4);  // of the block; the lane's others are 4 apart
     const SeqState sq = seq_state(a.q, s);
     const int n = a.out.p ? sq.n : sq.commit;
     if (n == 0) return;
-    const int64_t cell = ((int64_t)h * a.dv + col) * DK, slot = (int64_t)a.hv * a.dv * DK;
-    float S[P][4];
+    const int64_t cell = ((int64_t)h * a.dv + c0 + col) * DK + 4 * l, slot = (int64_t)a.hv * a.dv * DK;
+    float S[CPL][P][4];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        float4 f = make_float4(0, 0, 0, 0);
-        if (sq.src >= 0) f = *reinterpret_cast<const float4 *>(a.pool + sq.src * slot + cell + 64 * p + 4 * l);
-        S[p][0] = f.x; S[p][1] = f.y; S[p][2] = f.z; S[p][3] = f.w;
-    }
-    struct Row { float q[P][4], k[P][4], v, al, be; };
-    auto fetch = [&](int t, Row &r) {
-        load_row<P>(a.kv_vec, a.qh, t, hk, l, r.q);
-        load_row<P>(a.kv_vec, a.kh, t, hk, l, r.k);
-        r.v = load1(a.vh, t, h, col);
-        r.al = load1(a.alpha, t, h, 0);
-        r.be = load1(a.beta, t, h, 0);
-    };
-    Row cur, nxt;
-    fetch(sq.first, cur);
-    for (int i = 0; i < n; ++i) {
-        const int t = sq.first + i;
-        if (i + 1 < n) fetch(t + 1, nxt);
-        float qq = 0, kk = 0, kq = 0, d = 0, e = 0;
+    for (int c = 0; c < CPL; ++c)
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                qq = fmaf(cur.q[p][x], cur.q[p][x], qq);
-                kk = fmaf(cur.k[p][x], cur.k[p][x], kk);
-                kq = fmaf(cur.k[p][x], cur.q[p][x], kq);
-                d = fmaf(cur.k[p][x], S[p][x], d);
-                e = fmaf(cur.q[p][x], S[p][x], e);
-            }
-        qq = sum16(qq); kk = sum16(kk); kq = sum16(kq); d = sum16(d); e = sum16(e);
-        float rq = a.scale, rk = 1.f;
-        if (a.norm) {
-            rq *= rsqrtf(qq + a.eps);
-            rk = rsqrtf(kk + a.eps);
+        for (int p = 0; p < P; ++p) {
+            float4 f = make_float4(0, 0, 0, 0);
+            if (sq.src >= 0) f = *reinterpret_cast<const float4 *>(a.pool + sq.src * slot + cell + 4 * c * DK + 64 * p);
+            S[c][p][0] = f.x; S[c][p][1] = f.y; S[c][p][2] = f.z; S[c][p][3] = f.w;
         }
-        const Gate g = gates(a, h, cur.al, cur.be);
-        const float decay = expf(g.g);
-        const float u = g.b * (cur.v - decay * (d * rk));
-        const float o = rq * fmaf(u * rk, kq, decay * e);
-        const float uk = u * rk;
+    const int r = tid >> 4;  // the row that this thread's 16 lanes make ready
+    for (int i0 = 0; i0 < n; i0 += R) {
+        const int m = min(R, n - i0);
+        if (r < m) {
+            const int t = sq.first + i0 + r;
+            float q[P][4], k[P][4], v[COLS / 16];
+            load_row<P>(a.q_vec, a.qh, t, hk, l, q);
+            load_row<P>(a.k_vec, a.kh, t, hk, l, k);
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) S[p][x] = fmaf(cur.k[p][x], uk, decay * S[p][x]);
-        if (a.out.p && l == 0) store1(a.out, t, h, col, o);
-        if (i + 1 == sq.commit) {
+            for (int c = 0; c < COLS / 16; ++c) v[c] = load1(a.vh, t, h, c0 + l + 16 * c);
+            const float al = load1(a.alpha, t, h, 0), be = load1(a.beta, t, h, 0);
+            float qq = 0, kk = 0, kq = 0;
 #pragma unroll
             for (int p = 0; p < P; ++p)
-                *reinterpret_cast<float4 *>(a.pool + sq.dst * slot + cell + 64 * p + 4 * l) =
-                    make_float4(S[p][0], S[p][1], S[p][2], S[p][3]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    qq = fmaf(q[p][x], q[p][x], qq);
+                    kk = fmaf(k[p][x], k[p][x], kk);
+                    kq = fmaf(k[p][x], q[p][x], kq);
+                }
+            qq = sum16(qq); kk = sum16(kk); kq = sum16(kq);
+            const float rq = a.norm ? a.scale * rsqrtf(qq + a.eps) : a.scale, rk = a.norm ? rsqrtf(kk + a.eps) : 1.f;
+            const Gate g = gates(a, h, al, be);
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                q_s[r][p][l] = make_float4(q[p][0] * rq, q[p][1] * rq, q[p][2] * rq, q[p][3] * rq);
+                k_s[r][p][l] = make_float4(k[p][0] * rk, k[p][1] * rk, k[p][2] * rk, k[p][3] * rk);
+            }
+#pragma unroll
+            for (int c = 0; c < COLS / 16; ++c) v_s[r][l + 16 * c] = v[c];
+            if (l == 0) g_s[r] = make_float4(expf(g.g), g.b, kq * rq * rk, 0);
         }
-        cur = nxt;
+        __syncthreads();
+        for (int i = 0; i < m; ++i) {
+            const float4 g = g_s[i];
+            float4 q[P], k[P];
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                q[p] = q_s[i][p][l];
+                k[p] = k_s[i][p][l];
+            }
+            float d[CPL], e[CPL];
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                d[c] = e[c] = 0;
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    d[c] = fmaf(k[p].x, S[c][p][0], d[c]); e[c] = fmaf(q[p].x, S[c][p][0], e[c]);
+                    d[c] = fmaf(k[p].y, S[c][p][1], d[c]); e[c] = fmaf(q[p].y, S[c][p][1], e[c]);
+                    d[c] = fmaf(k[p].z, S[c][p][2], d[c]); e[c] = fmaf(q[p].z, S[c][p][2], e[c]);
+                    d[c] = fmaf(k[p].w, S[c][p][3], d[c]); e[c] = fmaf(q[p].w, S[c][p][3], e[c]);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                d[c] = sum16(d[c]);
+                e[c] = sum16(e[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                const float u = g.y * fmaf(-g.x, d[c], v_s[i][col + 4 * c]);
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    S[c][p][0] = fmaf(k[p].x, u, g.x * S[c][p][0]);
+                    S[c][p][1] = fmaf(k[p].y, u, g.x * S[c][p][1]);
+                    S[c][p][2] = fmaf(k[p].z, u, g.x * S[c][p][2]);
+                    S[c][p][3] = fmaf(k[p].w, u, g.x * S[c][p][3]);
+                }
+                if (l == 0) o_s[i][col + 4 * c] = fmaf(u, g.z, g.x * e[c]);
+            }
+            if (i0 + i + 1 == sq.commit) {
+#pragma unroll
+                for (int c = 0; c < CPL; ++c)
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        *reinterpret_cast<float4 *>(a.pool + sq.dst * slot + cell + 4 * c * DK + 64 * p) =
+                            make_float4(S[c][p][0], S[c][p][1], S[c][p][2], S[c][p][3]);
+            }
+        }
+        __syncthreads();
+        if (a.out.p && r < m) {
+#pragma unroll
+            for (int c = 0; c < COLS / 16; ++c) store1(a.out, sq.first + i0 + r, h, c0 + l + 16 * c, o_s[r][l + 16 * c]);
+        }
     }
+}
+
+template <int DK, int CPL> hipError_t go(const Args &a, int nseq, hipStream_t st) {
+    const int64_t blocks = (int64_t)nseq * a.hv * (a.dv / (4 * WAVES * CPL));
+    hipLaunchKernelGGL((delta_rows_kernel<DK, CPL>), dim3((unsigned)blocks), dim3(THREADS), 0, st, a);
+    return hipGetLastError();
 }
 
 }  // namespace delta
@@ -105,10 +146,11 @@ hipError_t launch_delta(const StateSeqs &q, const DeltaState &d, const DeltaIn &
                         hipStream_t st) {
     using namespace delta;
     const Args a = make_args(q, d, in, out);
-    const int64_t blocks = (int64_t)q.nseq * d.hv * (d.dv / (COLS * WAVES));
-    if (d.dk == 64) hipLaunchKernelGGL(delta_rows_kernel<64>, dim3((unsigned)blocks), dim3(64 * WAVES), 0, st, a);
-    else hipLaunchKernelGGL(delta_rows_kernel<128>, dim3((unsigned)blocks), dim3(64 * WAVES), 0, st, a);
-    return hipGetLastError();
+    // a lane's columns: few where latency counts, more where rows are made ready for many
+    const int64_t columns = (int64_t)q.nseq * d.hv * d.dv;
+    const int cpl = d.dv % 64 == 0 && columns >= 64 * 8 * device_cus() ? 4 : columns >= 32 * 8 * device_cus() ? 2 : 1;
+    if (d.dk == 64) return cpl == 4 ? go<64, 4>(a, q.nseq, st) : cpl == 2 ? go<64, 2>(a, q.nseq, st) : go<64, 1>(a, q.nseq, st);
+    return cpl == 4 ? go<128, 4>(a, q.nseq, st) : cpl == 2 ? go<128, 2>(a, q.nseq, st) : go<128, 1>(a, q.nseq, st);
 }
 
 }  // namespace qk
