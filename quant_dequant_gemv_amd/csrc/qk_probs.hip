@@ -11,10 +11,11 @@
 namespace qk {
 namespace probs {
 
-constexpr int WAVES = 4;
-constexpr int THREADS = 64 * WAVES;
-constexpr int FEW = 32;    // rows that lie side by side (elem > 1) a tile has at most
-constexpr int TILE = 256;  // tokens of such a tile
+constexpr int ROW_WAVES = 4;       // waves of a block where a row's tokens lie side by side
+constexpr int WAVES = 16;          // where rows do, and where parts are joined
+constexpr int LANE = 16;           // tokens a lane has at a time
+constexpr int STEP = 64 * LANE;    // and a wave
+constexpr int FEW = 32;            // rows that lie side by side (elem > 1) a block has at most
 constexpr float LN2 = 0.693147180559945f;
 constexpr float LOW = -1e4f;  // 2^LOW is 0: terms below say nothing, and never as inf * 0
 
@@ -34,14 +35,20 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 // the maximum, sum 2^t, sum t 2^t.
 struct Stats { float m, s, w; };
 
-__device__ __forceinline__ float step(float z, float m, float scale) {
-    const float t = (z - (m == -INFINITY ? 0.f : m)) * scale;
-    return t < LOW ? LOW : t;  // (NaN stays)
+// LDS between the lanes of one wave: its accesses stay in program order, the
+// compiler is told not to move them.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
+
+// (a term below LOW is 0, and 0 * LOW is too; NaN stays in 2^t)
+__device__ __forceinline__ float step(float z, float m, float scale) { return (z - (m == -INFINITY ? 0.f : m)) * scale; }
 // The sums as they are with maximum m >= a.m.
 __device__ __forceinline__ void raise(Stats &a, float m, float scale) {
     const float d = step(a.m, m, scale), f = __builtin_amdgcn_exp2f(d);
-    a.w = f * fmaf(d, a.s, a.w);
+    a.w = f * fmaf(fmaxf(d, LOW), a.s, a.w);
     a.s *= f;
     a.m = m;
 }
@@ -52,22 +59,40 @@ __device__ __forceinline__ void join(Stats &a, Stats b, float scale) {
     a.s += b.s;
     a.w += b.w;
 }
-template <int N> __device__ __forceinline__ void add(Stats &a, const float *z, float scale) {
-    float m = a.m;
-#pragma unroll
-    for (int e = 0; e < N; ++e) m = fmaxf(m, z[e]);
-    raise(a, m, scale);
+// N terms more, the largest of them `top`.
+template <int N> __device__ __forceinline__ void add(Stats &a, const float *z, float top, float scale) {
+    raise(a, fmaxf(a.m, top), scale);
+    const float m = a.m == -INFINITY ? 0.f : a.m;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-        const float t = step(z[e], m, scale), p = __builtin_amdgcn_exp2f(t);
+        const float t = (z[e] - m) * scale, p = __builtin_amdgcn_exp2f(t);
         a.s += p;
-        a.w = fmaf(p, t, a.w);
+        a.w = fmaf(p, fmaxf(t, LOW), a.w);
     }
 }
+// Over the 64 lanes, by DPP inside rows of 16 (no LDS): every lane gets it.
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float lane_of(float v, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+template <typename F> __device__ __forceinline__ float over_lanes(float v, F f) {
+    v = f(v, dpp<0xB1>(v));   // quad_perm [1,0,3,2]
+    v = f(v, dpp<0x4E>(v));   // quad_perm [2,3,0,1]
+    v = f(v, dpp<0x141>(v));  // half row mirrored
+    v = f(v, dpp<0x140>(v));  // row mirrored
+    return f(f(lane_of(v, 0), lane_of(v, 16)), f(lane_of(v, 32), lane_of(v, 48)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    return over_lanes(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    return over_lanes(v, [](float a, float b) { return a + b; });
+}
 __device__ __forceinline__ Stats over_wave(Stats a, float scale) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) join(a, Stats{__shfl_xor(a.m, d), __shfl_xor(a.s, d), __shfl_xor(a.w, d)}, scale);
-    return a;
+    raise(a, wave_max(a.m), scale);
+    return Stats{a.m, wave_sum(a.s), wave_sum(a.w)};
 }
 
 __device__ __forceinline__ uint64_t lane_key(uint64_t k, int lane) {
@@ -75,33 +100,79 @@ __device__ __forceinline__ uint64_t lane_key(uint64_t k, int lane) {
            (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, lane);
 }
 
-// The largest keys that a wave has seen, sorted: lane i has the i-th.  Keys
-// come in batches of a lane each; thr, the last one of the `top` kept, rejects
-// nearly all after the first few.
+// The largest keys that a wave has seen, sorted: lane i has the i-th.  What
+// does not pass the last one of the `top` kept is rejected 64 at a time, so
+// after the first batch few are looked at one by one.
 struct Best {
     uint64_t key, thr;
-    __device__ __forceinline__ void clear() { key = 0; thr = 0; }
-    __device__ __forceinline__ void insert(uint64_t c, int top, int lane) {  // c uniform, > thr
-        const int at = __popcll(__ballot(key > c));
-        const uint64_t up = (uint64_t)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)(key >> 32), 0x138, 0xf, 0xf, false) << 32 |
-                            (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)key, 0x138, 0xf, 0xf, false);  // lane - 1
-        key = lane < at ? key : lane == at ? c : up;
+    float low;  // value of thr: a later token (of a higher index) has to be above it
+    __device__ __forceinline__ void clear() { key = thr = 0; low = -INFINITY; }
+    __device__ __forceinline__ void limit(int top) {
         thr = lane_key(key, top - 1);
+        low = thr ? key_value(thr) : -INFINITY;
     }
     __device__ __forceinline__ void offer(uint64_t c, int top, int lane) {
         uint64_t m;
         while ((m = __ballot(c > thr))) {
             const int l = __ffsll((unsigned long long)m) - 1;
-            insert(lane_key(c, l), top, lane);
+            const uint64_t k = lane_key(c, l);
+            const int at = __popcll(__ballot(key > k));
+            const uint64_t up = (uint64_t)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)(key >> 32), 0x138, 0xf, 0xf, false) << 32 |
+                                (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)key, 0x138, 0xf, 0xf, false);  // lane - 1
+            key = lane < at ? key : lane == at ? k : up;
+            thr = lane_key(key, top - 1);
             if (lane == l) c = 0;
         }
+    }
+    // The first batch: N tokens a lane, value(e) of the e-th one (-inf: none),
+    // key(e) its key, `most` the lane's largest value.  At least `top` tokens
+    // are at or above the top-th largest `most`, and few more: those go to LDS
+    // and are sorted by counting.
+    template <int N, typename V, typename K>
+    __device__ __forceinline__ void first(V value, K keyed, float most, int top, int lane, uint64_t *lds) {
+        int above = 0;
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+            above += lane_of(most, j) >= most;
+        // the largest of what at least `top` lanes reach (-inf: every token)
+        float floor = above >= top ? most : -INFINITY;
+        floor = wave_max(floor);
+        int n = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float z = value(e);
+            const bool in = z >= floor && z > -INFINITY;
+            const uint64_t m = __ballot(in);
+            const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+            if (in && at < 64) lds[at] = keyed(e);
+            n += __popcll(m);
+        }
+        wave_sync();
+        if (n <= 64) {
+            const uint64_t mine = lane < n ? lds[lane] : 0;
+            int rank = 0;
+            for (int j = 0; j < n; j += 4) {  // (lanes from n on hold 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) rank += lane_key(mine, j + i) > mine;
+            }
+            wave_sync();
+            if (lane < n) lds[rank] = mine;
+            wave_sync();
+            key = lane < n ? lds[lane] : 0;
+        } else {  // (many equals, or many asked for)
+            clear();
+#pragma unroll
+            for (int e = 0; e < N; ++e) offer(value(e) >= floor && value(e) > -INFINITY ? keyed(e) : 0, top, lane);
+        }
+        limit(top);
+        wave_sync();
     }
 };
 
 struct Args {
     Probs p;
     float scale;       // in units of log 2
-    int splits, span;  // parts of a row, tokens of one
+    int splits, span, subs;  // parts of a row, tokens of a block, parts of a row of one
     float *stats;      // [rows][splits][3]
     uint64_t *keys;    // [rows][splits][top]
 };
@@ -132,35 +203,84 @@ __device__ __forceinline__ void finish(const Args &a, int row, const Stats &st, 
     }
 }
 
-template <int N> __device__ __forceinline__ void take(const float *z, int v0, int stride, bool on, Stats &st, Best &best, float scale,
-                                                      int top, int lane) {
-    add<N>(st, z, scale);
-    if (!top) return;
+// N tokens a lane more (-inf: none), at(e) the e-th one's number; those of a
+// wave come in rising batches.  fresh: the first batch.
+template <int N, typename F>
+__device__ __forceinline__ void take(const float *z, F at, bool fresh, Stats &st, Best &best, float scale, int top, int lane, uint64_t *lds) {
+    float most = z[0];
 #pragma unroll
-    for (int e = 0; e < N; ++e) best.offer(on && z[e] > -INFINITY ? key_of(z[e], v0 + e * stride) : 0, top, lane);
+    for (int e = 1; e < N; ++e) most = fmaxf(most, z[e]);
+    add<N>(st, z, most, scale);
+    if (!top) return;
+    if (fresh) {
+        best.first<N>([&](int e) { return z[e]; }, [&](int e) { return key_of(z[e], at(e)); }, most, top, lane, lds);
+    } else if (__ballot(most > best.low)) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (__ballot(z[e] > best.low)) {
+                best.offer(z[e] > best.low ? key_of(z[e], at(e)) : 0, top, lane);
+                best.low = best.thr ? key_value(best.thr) : -INFINITY;
+            }
+    }
 }
 
-// The parts of a block's waves, joined by the first one.
-__device__ __forceinline__ bool join_waves(Stats &st, Best &best, const Args &a, int lane, int wave) {
-    __shared__ Stats part[WAVES];
-    __shared__ uint64_t keys[WAVES][64];
+// The largest of `count` keys from p on, for one wave.
+template <typename P> __device__ __forceinline__ void gather(P p, int count, Best &best, int top, int lane, uint64_t *lds) {
+    constexpr int N = 8;
+    for (int i = 0; i < count; i += 64 * N) {
+        uint64_t k[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) k[e] = i + 64 * e + lane < count ? p[i + 64 * e + lane] : 0;
+        if (i == 0) {
+            auto value = [&](int e) { return k[e] ? key_value(k[e]) : -INFINITY; };
+            float most = value(0);
+#pragma unroll
+            for (int e = 1; e < N; ++e) most = fmaxf(most, value(e));
+            best.first<N>(value, [&](int e) { return k[e]; }, most, top, lane, lds);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) best.offer(k[e], top, lane);
+        }
+    }
+}
+
+// What the waves of a block share.
+template <int W> struct Shared {
+    Stats part[W];
+    uint64_t keys[W * 64], sort[W][64];
+};
+
+// The parts of a block's waves, joined by the first one (true).
+template <int W>
+__device__ __forceinline__ bool join_waves(Stats &st, Best &best, const Args &a, Shared<W> &sh, int lane, int wave) {
+    const int top = a.p.top;
     st = over_wave(st, a.scale);
-    if (lane == 0) part[wave] = st;
-    keys[wave][lane] = best.key;
+    if (lane == 0) sh.part[wave] = st;
+    if (lane < top) sh.keys[wave * top + lane] = best.key;
     __syncthreads();
     if (wave) return false;
-    for (int w = 1; w < WAVES; ++w) {
-        join(st, part[w], a.scale);
-        if (a.p.top) best.offer(lane < a.p.top ? keys[w][lane] : 0, a.p.top, lane);
-    }
+    st = over_wave(lane < W ? sh.part[lane] : Stats{-INFINITY, 0, 0}, a.scale);
+    if (top) gather(sh.keys, W * top, best, top, lane, sh.sort[0]);
     return true;
 }
 
-// Rows whose tokens lie side by side: a block for a part of a row.
-template <bool F16> __global__ void __launch_bounds__(THREADS) probs_row_kernel(Args a) {
+__device__ __forceinline__ void leave(const Args &a, int row, int part, const Stats &st, uint64_t key, int lane) {
+    if (a.splits == 1) return finish(a, row, st, key, lane);
+    const int64_t cell = (int64_t)row * a.splits + part;
+    if (lane == 0) {
+        float *o = a.stats + cell * 3;
+        o[0] = st.m; o[1] = st.s; o[2] = st.w;
+    }
+    if (lane < a.p.top) a.keys[cell * a.p.top + lane] = key;
+}
+
+// Rows whose tokens lie side by side: a block for a part of a row, STEP tokens
+// of it to a wave at a time.
+template <bool F16> __global__ void __launch_bounds__(64 * ROW_WAVES) probs_row_kernel(Args a) {
     using T = std::conditional_t<F16, _Float16, float>;
-    constexpr int N = 16 / sizeof(T);
+    constexpr int THREADS = 64 * ROW_WAVES, N = 16 / sizeof(T), J = LANE / N;  // tokens of a piece, pieces of a lane
     typedef T Vec __attribute__((ext_vector_type(N)));
+    __shared__ Shared<ROW_WAVES> sh;
     const Probs &p = a.p;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (int64_t u = blockIdx.x; u < (int64_t)p.rows * a.splits; u += gridDim.x) {
@@ -170,131 +290,141 @@ template <bool F16> __global__ void __launch_bounds__(THREADS) probs_row_kernel(
         Stats st{-INFINITY, 0, 0};
         Best best;
         best.clear();
-        // up to the first whole piece of 16 bytes, then pieces, then the rest
+        // whole pieces of 16 bytes, and what is left before and behind them (wave 0 and the last one, at the end)
         const int head = min(v1, v0 + (int)((16 - ((uintptr_t)(z + v0) & 15)) % 16 / sizeof(T)));
-        const int pieces = max(0, (v1 - head) / N);
-        if (wave == 0 && head > v0) {
-            const bool on = v0 + lane < head;
-            const float x = on ? (float)z[v0 + lane] : -INFINITY;
-            take<1>(&x, v0 + lane, 0, on, st, best, a.scale, p.top, lane);
-        }
-        for (int i = wave * 64; i < pieces; i += THREADS) {
-            const bool on = i + lane < pieces;
-            const int v = head + (i + lane) * N;
-            float x[N];
-            Vec q;
-            if (on) q = *reinterpret_cast<const Vec *>(z + v);
+        const int pieces = max(0, (v1 - head) / N), tail = head + pieces * N;
+        bool fresh = true;
+        auto load = [&](int i, Vec *q) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) x[e] = on ? (float)q[e] : -INFINITY;
-            take<N>(x, v, 1, on, st, best, a.scale, p.top, lane);
-        }
-        const int tail = head + pieces * N;
-        if (wave == WAVES - 1 && tail < v1) {
-            const bool on = tail + lane < v1;
-            const float x = on ? (float)z[tail + lane] : -INFINITY;
-            take<1>(&x, tail + lane, 0, on, st, best, a.scale, p.top, lane);
-        }
-        if (join_waves(st, best, a, lane, wave)) {
-            if (a.splits == 1) {
-                finish(a, row, st, best.key, lane);
-            } else {
-                if (lane == 0) {
-                    float *o = a.stats + u * 3;
-                    o[0] = st.m; o[1] = st.s; o[2] = st.w;
-                }
-                if (lane < p.top) a.keys[u * p.top + lane] = best.key;
+            for (int j = 0; j < J; ++j)
+                if (i + 64 * j + lane < pieces) q[j] = *reinterpret_cast<const Vec *>(z + head + (i + 64 * j + lane) * N);
+        };
+        Vec q[J], nx[J];
+        load(wave * 64 * J, q);
+        for (int i = wave * 64 * J; i < pieces; i += THREADS * J) {
+            load(i + THREADS * J, nx);
+            float x[LANE];
+#pragma unroll
+            for (int e = 0; e < LANE; ++e) x[e] = (float)q[e / N][e % N];
+            if (i + 64 * J > pieces) {
+#pragma unroll
+                for (int e = 0; e < LANE; ++e) x[e] = i + 64 * (e / N) + lane < pieces ? x[e] : -INFINITY;
             }
+            take<LANE>(x, [&](int e) { return head + (i + 64 * (e / N) + lane) * N + e % N; }, fresh, st, best, a.scale, p.top, lane,
+                       sh.sort[wave]);
+            fresh = false;
+#pragma unroll
+            for (int j = 0; j < J; ++j) q[j] = nx[j];
         }
+        auto rest = [&](int from, int to) {
+            if (from >= to) return;
+            const float x = from + lane < to ? (float)z[from + lane] : -INFINITY;
+            add<1>(st, &x, x, a.scale);
+            if (p.top) best.offer(x > -INFINITY ? key_of(x, from + lane) : 0, p.top, lane);
+        };
+        if (wave == 0) rest(v0, head);
+        if (wave == ROW_WAVES - 1) rest(tail, v1);
+        if (join_waves(st, best, a, sh, lane, wave)) leave(a, row, part, st, best.key, lane);
         __syncthreads();
     }
 }
 
-// Rows side by side (any strides): a block for a part of up to FEW rows, TILE
-// tokens at a time through LDS, from where a wave has a row's.
-__global__ void __launch_bounds__(THREADS) probs_few_kernel(Args a) {
-    __shared__ float z[FEW][TILE + 1];
+// Rows side by side (any strides): a block for a part of up to FEW rows, a tile
+// of tokens at a time through LDS.  Where there are fewer rows than waves, a
+// row's tile is shared by `subs` of them, and each leaves a part of its own.
+__global__ void __launch_bounds__(64 * WAVES) probs_few_kernel(Args a) {
+    constexpr int THREADS = 64 * WAVES, AHEAD = 8;
+    extern __shared__ float z[];  // [rows][tile + 1]
+    __shared__ uint64_t sort[WAVES][64];
     const Probs &p = a.p;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int groups = (p.rows + FEW - 1) / FEW;
-    for (int64_t u = blockIdx.x; u < (int64_t)groups * a.splits; u += gridDim.x) {
-        const int r0 = (int)(u / a.splits) * FEW, nr = min(FEW, p.rows - r0), part = (int)(u % a.splits);
+    const int groups = (p.rows + FEW - 1) / FEW, blocks_row = a.splits / a.subs, tile = STEP * a.subs, pitch = tile + 1;
+    constexpr int UNITS = FEW / WAVES;
+    for (int64_t u = blockIdx.x; u < (int64_t)groups * blocks_row; u += gridDim.x) {
+        const int r0 = (int)(u / blocks_row) * FEW, nr = min(FEW, p.rows - r0), part = (int)(u % blocks_row);
         const int v0 = part * a.span, v1 = min(v0 + a.span, p.vocab);
-        Stats st[FEW / WAVES];
-        Best best[FEW / WAVES];
+        Stats st[UNITS];
+        Best best[UNITS];
 #pragma unroll
-        for (int k = 0; k < FEW / WAVES; ++k) {
+        for (int k = 0; k < UNITS; ++k) {
             st[k] = Stats{-INFINITY, 0, 0};
             best[k].clear();
         }
-        const int per = THREADS / nr, r = threadIdx.x % nr, first = threadIdx.x / nr;
-        for (int v = v0; v < v1; v += TILE) {
-            const int n = min(TILE, v1 - v);
-            if (first < per)
-                for (int i = first; i < n; i += per) {
-                    const int64_t o = (int64_t)(r0 + r) * p.z.row + (int64_t)(v + i) * p.z.elem;
-                    z[r][i] = p.z.f16 ? (float)reinterpret_cast<const _Float16 *>(p.z.p)[o] : reinterpret_cast<const float *>(p.z.p)[o];
+        for (int v = v0; v < v1; v += tile) {
+            const int n = min(tile, v1 - v), total = n * nr;
+            // element e of the tile: token e / nr, row e % nr
+            int i = threadIdx.x / nr, r = threadIdx.x % nr;
+            const int di = THREADS / nr, dr = THREADS % nr;
+            auto each = [&](auto get) {
+                for (int e = threadIdx.x; e < total; e += THREADS * AHEAD) {
+                    float x[AHEAD];
+                    int to[AHEAD];
+#pragma unroll
+                    for (int k = 0; k < AHEAD; ++k) {
+                        to[k] = r * pitch + i;
+                        if (e + THREADS * k < total) x[k] = get((int64_t)(r0 + r) * p.z.row + (int64_t)(v + i) * p.z.elem);
+                        i += di;
+                        r += dr;
+                        if (r >= nr) { r -= nr; ++i; }
+                    }
+#pragma unroll
+                    for (int k = 0; k < AHEAD; ++k)
+                        if (e + THREADS * k < total) z[to[k]] = x[k];
                 }
+            };
+            if (p.z.f16) each([&](int64_t o) { return (float)reinterpret_cast<const _Float16 *>(p.z.p)[o]; });
+            else each([&](int64_t o) { return reinterpret_cast<const float *>(p.z.p)[o]; });
             __syncthreads();
 #pragma unroll
-            for (int k = 0; k < FEW / WAVES; ++k) {
-                const int rr = k * WAVES + wave;
-                if (rr >= nr) continue;
-                for (int i = 0; i < n; i += 64) {
-                    const bool on = i + lane < n;
-                    const float x = on ? z[rr][i + lane] : -INFINITY;
-                    take<1>(&x, v + i + lane, 0, on, st[k], best[k], a.scale, p.top, lane);
-                }
+            for (int k = 0; k < UNITS; ++k) {
+                const int unit = k * WAVES + wave;
+                if (unit >= nr * a.subs) continue;
+                const int t0 = unit / nr * STEP;
+                const float *row = z + unit % nr * pitch;
+                float x[LANE];
+#pragma unroll
+                for (int e = 0; e < LANE; ++e) x[e] = t0 + 64 * e + lane < n ? row[t0 + 64 * e + lane] : -INFINITY;
+                take<LANE>(x, [&](int e) { return v + t0 + 64 * e + lane; }, v == v0, st[k], best[k], a.scale, p.top, lane, sort[wave]);
             }
             __syncthreads();
         }
 #pragma unroll
-        for (int k = 0; k < FEW / WAVES; ++k) {
-            const int rr = k * WAVES + wave;
-            if (rr >= nr) continue;
-            const Stats s = over_wave(st[k], a.scale);
-            const int64_t cell = (int64_t)(r0 + rr) * a.splits + part;
-            if (a.splits == 1) {
-                finish(a, r0 + rr, s, best[k].key, lane);
-            } else {
-                if (lane == 0) {
-                    float *o = a.stats + cell * 3;
-                    o[0] = s.m; o[1] = s.s; o[2] = s.w;
-                }
-                if (lane < p.top) a.keys[cell * p.top + lane] = best[k].key;
-            }
+        for (int k = 0; k < UNITS; ++k) {
+            const int unit = k * WAVES + wave;
+            if (unit < nr * a.subs)
+                leave(a, r0 + unit % nr, part * a.subs + unit / nr, over_wave(st[k], a.scale), best[k].key, lane);
         }
     }
 }
 
 // The parts of a row, joined in a fixed order: a block a row.
-__global__ void __launch_bounds__(THREADS) probs_join_kernel(Args a) {
+__global__ void __launch_bounds__(64 * WAVES) probs_join_kernel(Args a) {
+    __shared__ Shared<WAVES> sh;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = blockIdx.x, top = a.p.top;
     Stats st{-INFINITY, 0, 0};
     Best best;
     best.clear();
-    for (int i = threadIdx.x; i < a.splits; i += THREADS) {
+    const int per = (a.splits + WAVES - 1) / WAVES, first = min(wave * per, a.splits), count = min(per, a.splits - first);
+    if (top) gather(a.keys + ((int64_t)row * a.splits + first) * top, count * top, best, top, lane, sh.sort[wave]);
+    for (int i = threadIdx.x; i < a.splits; i += 64 * WAVES) {
         const float *s = a.stats + ((int64_t)row * a.splits + i) * 3;
         join(st, Stats{s[0], s[1], s[2]}, a.scale);
     }
-    if (top)
-        for (int i = wave; i < a.splits; i += WAVES)
-            best.offer(lane < top ? a.keys[((int64_t)row * a.splits + i) * top + lane] : 0, top, lane);
-    if (join_waves(st, best, a, lane, wave)) finish(a, row, st, best.key, lane);
+    if (join_waves(st, best, a, sh, lane, wave)) finish(a, row, st, best.key, lane);
 }
 
-// How a call is cut into parts.
-struct Plan { bool few; int splits, span; };
+// How a call is cut: `splits` parts a row, `span` tokens to a block.
+struct Plan { bool few; int splits, span, subs; };
 Plan plan_of(const Probs &p) {
-    Plan pl;
-    pl.few = p.z.elem != 1;
+    Plan pl{p.z.elem != 1, 1, 0, 1};
+    if (pl.few) pl.subs = std::max(1, std::min(WAVES / std::min(p.rows, FEW), (p.vocab + STEP - 1) / STEP));
     const int64_t units = pl.few ? (p.rows + FEW - 1) / FEW : p.rows;
-    const int64_t want = std::max<int64_t>(1, 2 * device_cus() / units);
-    const int unit = pl.few ? TILE : 1024;
-    int64_t splits = std::min<int64_t>(want, (p.vocab + unit - 1) / unit);
-    pl.span = (int)((p.vocab + splits - 1) / splits);
-    pl.span = (pl.span + unit - 1) / unit * unit;
-    pl.splits = (p.vocab + pl.span - 1) / pl.span;
+    const int64_t grain = pl.few ? STEP * pl.subs : STEP * ROW_WAVES;
+    const int64_t want = std::max<int64_t>(1, 2 * device_cus() / units), grains = (p.vocab + grain - 1) / grain;
+    const int64_t span = (grains + std::min(want, grains) - 1) / std::min(want, grains) * grain;
+    pl.span = (int)std::min<int64_t>(span, INT32_MAX);
+    pl.splits = (int)((p.vocab + span - 1) / span) * pl.subs;
     return pl;
 }
 
@@ -311,14 +441,21 @@ hipError_t launch_probs(const Probs &p, void *workspace, hipStream_t st) {
     using namespace probs;
     const Plan pl = plan_of(p);
     uint64_t *keys = (uint64_t *)workspace;
-    const Args a{p, p.scale * 1.44269504088896f, pl.splits, pl.span,
+    const Args a{p, p.scale * 1.44269504088896f, pl.splits, pl.span, pl.subs,
                  reinterpret_cast<float *>(keys + (int64_t)p.rows * pl.splits * p.top), keys};
     const int64_t units = pl.few ? (p.rows + FEW - 1) / FEW : p.rows;
-    const unsigned blocks = (unsigned)std::min<int64_t>(units * pl.splits, 1 << 22);  // (a grid stays below 2^32 threads)
-    if (pl.few) hipLaunchKernelGGL(probs_few_kernel, dim3(blocks), dim3(THREADS), 0, st, a);
-    else if (p.z.f16) hipLaunchKernelGGL(probs_row_kernel<true>, dim3(blocks), dim3(THREADS), 0, st, a);
-    else hipLaunchKernelGGL(probs_row_kernel<false>, dim3(blocks), dim3(THREADS), 0, st, a);
-    if (pl.splits > 1) hipLaunchKernelGGL(probs_join_kernel, dim3((unsigned)p.rows), dim3(THREADS), 0, st, a);
+    const unsigned blocks = (unsigned)std::min<int64_t>(units * pl.splits / pl.subs, 1 << 22);  // (a grid stays below 2^32 threads)
+    if (pl.few) {
+        const hipError_t e = lds_opt_in<probs_few_kernel>(FEW * (STEP + 1) * 4);
+        if (e != hipSuccess) return e;
+        const int lds = std::min(p.rows, FEW) * (STEP * pl.subs + 1) * 4;
+        hipLaunchKernelGGL(probs_few_kernel, dim3(blocks), dim3(64 * WAVES), lds, st, a);
+    } else if (p.z.f16) {
+        hipLaunchKernelGGL(probs_row_kernel<true>, dim3(blocks), dim3(64 * ROW_WAVES), 0, st, a);
+    } else {
+        hipLaunchKernelGGL(probs_row_kernel<false>, dim3(blocks), dim3(64 * ROW_WAVES), 0, st, a);
+    }
+    if (pl.splits > 1) hipLaunchKernelGGL(probs_join_kernel, dim3((unsigned)p.rows), dim3(64 * WAVES), 0, st, a);
     return hipGetLastError();
 }
 
