@@ -12,7 +12,7 @@ namespace conv {
 
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 constexpr int R = 16;         // rows of a tile
-constexpr int THREADS = 256;
+constexpr int THREADS = 64;   // a wave: few channels fill the chip too
 
 struct Args {
     StateSeqs q;
@@ -106,22 +106,31 @@ template <int T, int C> __global__ void __launch_bounds__(THREADS) conv_kernel(A
             for (int j = 0; j < B; ++j) load<C>(a.x, sq.first + i0 - B + j, c, x[j]);
         }
         if (!a.y.p) continue;
-#pragma unroll 4
-        for (int i = i0; i < i1; ++i) {
-            load<C>(a.x, sq.first + i, c, x[B]);
-            float y[C];
+        // H rows are loaded before the first of them is worked on
+        constexpr int H = C == 4 ? 8 : R;
+        for (int h0 = i0; h0 < i1; h0 += H) {
+            float next[H][C];
 #pragma unroll
-            for (int e = 0; e < C; ++e) {
-                float s = bias[e];
+            for (int i = 0; i < H; ++i)
+                if (h0 + i < i1) load<C>(a.x, sq.first + h0 + i, c, next[i]);
 #pragma unroll
-                for (int j = 0; j < T; ++j) s = fmaf(w[e][j], x[j][e], s);
-                y[e] = a.act ? s / (1.f + expf(-s)) : s;
+            for (int i = 0; i < H; ++i) {
+                if (h0 + i >= i1) break;
+                float y[C];
+#pragma unroll
+                for (int e = 0; e < C; ++e) {
+                    x[B][e] = next[i][e];
+                    float s = bias[e];
+#pragma unroll
+                    for (int j = 0; j < T; ++j) s = fmaf(w[e][j], x[j][e], s);
+                    y[e] = a.act ? s / (1.f + expf(-s)) : s;
+                }
+                store<C>(a.y, sq.first + h0 + i, c, y);
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+#pragma unroll
+                    for (int e = 0; e < C; ++e) x[j][e] = x[j + 1][e];
             }
-            store<C>(a.y, sq.first + i, c, y);
-#pragma unroll
-            for (int j = 0; j < B; ++j)
-#pragma unroll
-                for (int e = 0; e < C; ++e) x[j][e] = x[j + 1][e];
         }
     }
 }
