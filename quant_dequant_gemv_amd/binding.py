@@ -10,7 +10,9 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import functools
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libqkgemv.so")
@@ -855,8 +857,33 @@ def kv_attn(cache: KVCache, q, pages, kv_len, q_start=None, scale: float | None 
 
 
 # ------------------------------------------------ the rest of a token (torch)
+# The same, in fewer steps still: structures are packed as bytes (laid out as
+# the classes above, which name their fields) and go to C as they are.
 
 _ACTS = {"none": ACT_NONE, "silu": ACT_SILU, "sigmoid": ACT_SIGMOID}
+_HEADS = struct.Struct("PqqqiI").pack           # qk_heads
+_BLOCK = struct.Struct("PPffiI").pack           # qk_block
+_STATE_SEQS = struct.Struct("iiPPPPP").pack     # qk_state_seqs
+_CONV = struct.Struct("PqiiPP").pack            # qk_conv
+_DELTA = struct.Struct("Pqiiii").pack           # qk_delta
+_DELTA_TAIL = struct.Struct("PPffiI").pack      # qk_delta_rows behind its five views
+_PROBS = struct.Struct("PPPPPPii").pack         # qk_probs
+
+
+@functools.lru_cache(None)
+def _packed_calls():
+    """The library's functions that the helpers below call, taking packed structures."""
+    load_library()
+    lib = ctypes.CDLL(LIB_PATH)
+    S, P, i64, c_int, f32 = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    for f, restype, args in ((lib.qk_block_norm, c_int, [S, c_int, c_int, c_int, S, S, S, S, S, P]),
+                             (lib.qk_conv_silu, c_int, [S, S, c_int, S, S, P]),
+                             (lib.qk_delta_workspace_bytes, i64, [S, S]),
+                             (lib.qk_delta_rule, c_int, [S, S, S, S, P, i64, P]),
+                             (lib.qk_logprobs_workspace_bytes, i64, [S, c_int, i64, c_int]),
+                             (lib.qk_logprobs, c_int, [S, c_int, i64, f32, S, P, i64, P])):
+        f.argtypes, f.restype = args, restype
+    return lib
 
 
 def _act_arg(act, allowed):
@@ -865,24 +892,30 @@ def _act_arg(act, allowed):
     return _ACTS[act]
 
 
-def _float_arg(t, name, shape):
-    """The address of a contiguous float32 tensor of this shape, or None for None."""
-    if t is None:
-        return None
-    _need(t, name, _torch.float32)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {list(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+def _number(x):
+    """x as a float32 field takes it: beyond its range an infinity, which the library refuses."""
+    x = float(x)
+    return x if -3.4e38 < x < 3.4e38 else x * float("inf")
+
+
+def _view_arg(t, name, shape):
+    """The packed qk_heads of a tensor [rows, heads, D]."""
+    try:
+        if t.shape == shape:
+            return _HEADS(t.data_ptr(), *t.stride(), _f16[t.dtype], 0)
+    except (AttributeError, KeyError):
+        pass
+    return bytes(_heads_arg(t, name, *shape))
 
 
 def _matrix_arg(t, name, rows=None, n=None, by_head=False):
-    """The qk_heads of a tensor [rows, n] of any strides: n elements of one head, or (by_head) one element of n heads."""
+    """The packed qk_heads of a tensor [rows, n] of any strides: n elements of one head, or (by_head) one of n heads."""
     try:
         f16 = _f16[t.dtype]
         r, m = t.shape
         if (rows is None or r == rows) and (n is None or m == n):
             s, e = t.stride()
-            return qk_heads(t.data_ptr(), s, e, 0, f16) if by_head else qk_heads(t.data_ptr(), s, 0, e, f16)
+            return _HEADS(t.data_ptr(), s, e, 0, f16, 0) if by_head else _HEADS(t.data_ptr(), s, 0, e, f16, 0)
     except (AttributeError, KeyError, ValueError):
         pass
     if not isinstance(t, _torch.Tensor):
@@ -893,23 +926,61 @@ def _matrix_arg(t, name, rows=None, n=None, by_head=False):
                      f"got {tuple(t.shape)}")
 
 
+def _float_arg(t, name, shape):
+    """The address of a contiguous float32 tensor of this shape, 0 for None."""
+    if t is None:
+        return 0
+    try:
+        if t.dtype is _torch.float32 and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, _torch.float32)
+    raise ValueError(f"{name} must have shape {list(shape)}, got {tuple(t.shape)}")
+
+
 def _state_seqs_arg(rows, slots, slots_out, q_start, kv_len, commit):
-    """The qk_state_seqs of a call."""
+    """The packed qk_state_seqs of a call."""
     if rows > _INT_MAX:
         raise QKError(QK_EINVAL_SHAPE, "qk_state_seqs")
-    p = _int32_arg(slots, "slots", (None,))
+    try:
+        i32, shape = _torch.int32, slots.shape
+        nseq, = shape
+        p = [rows, nseq, 0]
+        for t in (slots, slots_out, kv_len, commit):
+            if t is None:
+                p.append(0)
+            elif t.dtype is i32 and t.shape == shape and t.is_contiguous():
+                p.append(t.data_ptr())
+            else:
+                break
+        else:
+            if slots is not None:
+                if q_start is None:
+                    return _STATE_SEQS(*p)
+                if q_start.dtype is i32 and q_start.shape == (nseq + 1,) and q_start.is_contiguous():
+                    p[2] = q_start.data_ptr()
+                    return _STATE_SEQS(*p)
+    except (AttributeError, ValueError):
+        pass
+    _int32_arg(slots, "slots", (None,))
     nseq = slots.shape[0]
-    return qk_state_seqs(rows, nseq, None if q_start is None else _int32_arg(q_start, "q_start", (nseq + 1,)), p,
-                         *(None if t is None else _int32_arg(t, name, (nseq,))
-                           for t, name in ((slots_out, "slots_out"), (kv_len, "kv_len"), (commit, "commit"))))
+    for t, name, n in ((slots_out, "slots_out", nseq), (kv_len, "kv_len", nseq), (commit, "commit", nseq),
+                       (q_start, "q_start", nseq + 1)):
+        if t is not None:
+            _int32_arg(t, name, (n,))
+    raise ValueError("bad sequences")
 
 
-def _workspace(workspace, need, device):
-    """The tensor (or None) and its bytes: the caller's, or one allocated here."""
+def _workspace(workspace, need, like):
+    """The address (or None) and bytes of the caller's workspace, or of one allocated here (and the tensor)."""
     if workspace is None:
-        return (_torch.empty(need, dtype=_torch.uint8, device=device) if need > 0 else None), max(need, 0)
-    _need(workspace, "workspace", _torch.uint8)
-    return workspace, workspace.numel()
+        if need <= 0:
+            return None, 0, None
+        workspace = like.new_empty(need, dtype=_torch.uint8)
+    else:
+        _need(workspace, "workspace", _torch.uint8)
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 def block_norm(y, post_norm=None, gate=None, act: str = "silu", scale: float = 1.0, residual=None, pre_norm=None,
@@ -923,23 +994,30 @@ def block_norm(y, post_norm=None, gate=None, act: str = "silu", scale: float = 1
     h_out is given (it may be residual).  Returns (h_out, x_out): x float16
     contiguous unless given, None where h_out is given and neither pre_norm
     nor x_out."""
-    torch = _start()
-    ya = _heads_arg(y, "y")
-    shape = rows, groups, dim = y.shape
-    block = qk_block(_float_arg(post_norm, "post_norm", (dim,)), _float_arg(pre_norm, "pre_norm", (dim,)), eps, scale,
-                     _act_arg(act, _ACTS))
+    if _torch is None:
+        _start()
+    try:
+        shape = y.shape
+        rows, groups, dim = shape
+    except (AttributeError, ValueError):
+        _heads_arg(y, "y")
+        raise
+    ya = _view_arg(y, "y", shape)
+    block = _BLOCK(_float_arg(post_norm, "post_norm", (dim,)), _float_arg(pre_norm, "pre_norm", (dim,)), _number(eps),
+                   _number(scale), _act_arg(act, _ACTS), 0)
     dev = _one_device(y, post_norm, gate, residual, pre_norm, h_out, x_out,
                       names="y post_norm gate residual pre_norm h_out x_out")
     if (ctx := _elsewhere(dev, stream)) is not None:
         with ctx:
             return block_norm(y, post_norm, gate, act, scale, residual, pre_norm, eps, h_out, x_out)
-    if max(shape) > _INT_MAX:
+    if rows > _INT_MAX or groups > _INT_MAX or dim > _INT_MAX:
         raise QKError(QK_EINVAL_SHAPE, "qk_block_norm")
     if x_out is None and (h_out is None or pre_norm is not None):
-        x_out = torch.empty(shape, dtype=torch.float16, device=y.device)
-    rc = _lib.qk_block_norm(block, rows, groups, dim, ya, *(None if t is None else _heads_arg(t, name, *shape) for t, name in
-                                                           ((gate, "gate"), (residual, "residual"), (h_out, "h_out"),
-                                                            (x_out, "x_out"))), _current(dev))
+        x_out = _torch.empty(shape, dtype=_torch.float16, device=y.device)
+    rc = _packed_calls().qk_block_norm(block, rows, groups, dim, ya, None if gate is None else _view_arg(gate, "gate", shape),
+                                       None if residual is None else _view_arg(residual, "residual", shape),
+                                       None if h_out is None else _view_arg(h_out, "h_out", shape),
+                                       None if x_out is None else _view_arg(x_out, "x_out", shape), _current(dev))
     if rc != QK_OK:
         raise QKError(rc, "qk_block_norm")
     return h_out, x_out
@@ -961,10 +1039,10 @@ class ConvState:
             raise QKError(QK_EINVAL_SHAPE, "ConvState")
         if pool is None:
             pool = torch.zeros((num_slots, taps - 1, C), dtype=torch.float32, device=weight.device)
-        _float_arg(pool, "pool", (num_slots, taps - 1, C))
         self.pool, self.weight, self.bias = pool, weight, bias
         self.num_slots, self.channels, self.taps = num_slots, C, taps
-        self._c = qk_conv(pool.data_ptr(), num_slots, C, taps, weight.data_ptr(), _float_arg(bias, "bias", (C,)))
+        self._c = _CONV(_float_arg(pool, "pool", (num_slots, taps - 1, C)), num_slots, C, taps, weight.data_ptr(),
+                        _float_arg(bias, "bias", (C,)))
 
 
 class DeltaState:
@@ -978,14 +1056,13 @@ class DeltaState:
         shape = (num_slots, v_heads, value_dim, key_dim)
         if not all(1 <= n <= _INT_MAX for n in (*shape, k_heads)):
             raise QKError(QK_EINVAL_SHAPE, "DeltaState")
-        self._c = qk_delta(None, num_slots, k_heads, v_heads, key_dim, value_dim)
-        if qk_delta_workspace_bytes(self._c, qk_state_seqs(0, 1)) < 0:
+        if qk_delta_workspace_bytes(qk_delta(None, num_slots, k_heads, v_heads, key_dim, value_dim), qk_state_seqs(0, 1)) < 0:
             raise QKError(QK_EINVAL_SHAPE, "DeltaState")
         if pool is None:
             pool = torch.zeros(shape, dtype=torch.float32, device=device)
-        self._c.pool = _float_arg(pool, "pool", shape)
         self.pool = pool
         self.num_slots, self.k_heads, self.v_heads, self.key_dim, self.value_dim = num_slots, k_heads, v_heads, key_dim, value_dim
+        self._c = _DELTA(_float_arg(pool, "pool", shape), num_slots, k_heads, v_heads, key_dim, value_dim)
 
 
 def conv_silu(conv: ConvState, x, slots, slots_out=None, q_start=None, kv_len=None, commit=None, act: str = "silu",
@@ -996,7 +1073,6 @@ def conv_silu(conv: ConvState, x, slots, slots_out=None, q_start=None, kv_len=No
     "none": without).  Returns out, [rows, channels] of the type of x unless
     given, None with state_only.  Rows of no sequence are left as they were:
     undefined in an out that is allocated here."""
-    torch = _torch
     xa = _matrix_arg(x, "x", None, conv.channels)
     rows = x.shape[0]
     a = _act_arg(act, ("silu", "none"))
@@ -1009,9 +1085,9 @@ def conv_silu(conv: ConvState, x, slots, slots_out=None, q_start=None, kv_len=No
     if state_only and out is not None:
         raise ValueError("an out with state_only")
     if out is None and not state_only:
-        out = torch.empty_like(x)
-    rc = _lib.qk_conv_silu(conv._c, seqs, a, xa, None if out is None else _matrix_arg(out, "out", rows, conv.channels),
-                           _current(dev))
+        out = _torch.empty_like(x)
+    rc = _packed_calls().qk_conv_silu(conv._c, seqs, a, xa,
+                                      None if out is None else _matrix_arg(out, "out", rows, conv.channels), _current(dev))
     if rc != QK_OK:
         raise QKError(rc, "qk_conv_silu")
     return out
@@ -1029,14 +1105,16 @@ def delta_rule(state: DeltaState, q, k, v, alpha, beta, slots, slots_out=None, q
     workspace: uint8 device tensor of at least qk_delta_workspace_bytes bytes
     (None: allocated for the call).  Rows of no sequence are left as they were:
     undefined in an out that is allocated here."""
-    torch = _torch
-    hk, hv, dk, dv = state.k_heads, state.v_heads, state.key_dim, state.value_dim
-    qa = _heads_arg(q, "q", None, hk, dk)
-    rows = q.shape[0]
-    ins = qk_delta_rows(qa, _heads_arg(k, "k", rows, hk, dk), _heads_arg(v, "v", rows, hv, dv),
-                        _matrix_arg(alpha, "alpha", rows, hv, True), _matrix_arg(beta, "beta", rows, hv, True),
-                        _float_arg(A, "A", (hv,)), _float_arg(dt_bias, "dt_bias", (hv,)), eps,
-                        dk ** -0.5 if scale is None else scale, int(norm))
+    hk, hv, dk = state.k_heads, state.v_heads, state.key_dim
+    try:
+        rows = q.shape[0]
+    except (AttributeError, IndexError):
+        rows = 0  # (refused below, in words)
+    kshape, vshape = (rows, hk, dk), (rows, hv, state.value_dim)
+    ins = b"".join((_view_arg(q, "q", kshape), _view_arg(k, "k", kshape), _view_arg(v, "v", vshape),
+                    _matrix_arg(alpha, "alpha", rows, hv, True), _matrix_arg(beta, "beta", rows, hv, True),
+                    _DELTA_TAIL(_float_arg(A, "A", (hv,)), _float_arg(dt_bias, "dt_bias", (hv,)), _number(eps),
+                                dk ** -0.5 if scale is None else _number(scale), int(norm), 0)))
     if dt_bias is not None and A is None:
         raise ValueError("dt_bias without A")
     seqs = _state_seqs_arg(rows, slots, slots_out, q_start, kv_len, commit)
@@ -1049,10 +1127,10 @@ def delta_rule(state: DeltaState, q, k, v, alpha, beta, slots, slots_out=None, q
     if state_only and out is not None:
         raise ValueError("an out with state_only")
     if out is None and not state_only:
-        out = torch.empty((rows, hv, dv), dtype=torch.float32, device=q.device)
-    ws, need = _workspace(workspace, _lib.qk_delta_workspace_bytes(state._c, seqs), q.device)
-    rc = _lib.qk_delta_rule(state._c, seqs, ins, None if out is None else _heads_arg(out, "out", rows, hv, dv),
-                            None if ws is None else ws.data_ptr(), need, _current(dev))
+        out = q.new_empty(vshape, dtype=_torch.float32)
+    lib = _packed_calls()
+    ws, need, keep = _workspace(workspace, lib.qk_delta_workspace_bytes(state._c, seqs) if workspace is None else 0, q)
+    rc = lib.qk_delta_rule(state._c, seqs, ins, None if out is None else _view_arg(out, "out", vshape), ws, need, _current(dev))
     if rc != QK_OK:
         raise QKError(rc, "qk_delta_rule")
     return out
@@ -1068,25 +1146,36 @@ def logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, workspace=No
     tokens top_ids int32 and top_lp float32 [rows, top] (None for top 0).
     workspace: uint8 device tensor of at least qk_logprobs_workspace_bytes
     bytes (None: allocated for the call)."""
-    torch = _start()
+    if _torch is None:
+        _start()
     za = _matrix_arg(logits, "logits")
     rows, vocab = logits.shape
-    tp = None if tokens is None else _int32_arg(tokens, "tokens", (rows, None))
-    ntok = 0 if tokens is None else tokens.shape[1]
-    if max(rows, ntok) > _INT_MAX or not 0 <= top <= 64:
+    tp = ntok = 0
+    if tokens is not None:
+        tp = _int32_arg(tokens, "tokens", (rows, None))
+        ntok = tokens.shape[1]
+    if rows > _INT_MAX or ntok > _INT_MAX or not 0 <= top <= 64:
         raise QKError(QK_EINVAL_SHAPE, "qk_logprobs")
     dev = _one_device(logits, tokens, workspace, names="logits tokens workspace")
     if (ctx := _elsewhere(dev, stream)) is not None:
         with ctx:
             return logprobs(logits, tokens, top, scale, workspace)
-    f32 = dict(dtype=torch.float32, device=logits.device)
-    r = LogProbs(None if tokens is None else torch.empty((rows, ntok), **f32), torch.empty(rows, **f32),
-                 torch.empty(rows, **f32), torch.empty((rows, top), dtype=torch.int32, device=logits.device) if top else None,
-                 torch.empty((rows, top), **f32) if top else None)
-    ws, need = _workspace(workspace, _lib.qk_logprobs_workspace_bytes(za, rows, vocab, top), logits.device)
-    out = qk_probs(tp if ntok else None, r.token_lp.data_ptr() if ntok else None, r.lse.data_ptr(), r.entropy.data_ptr(),
-                   r.top_ids.data_ptr() if top else None, r.top_lp.data_ptr() if top else None, ntok, top)
-    rc = _lib.qk_logprobs(za, rows, vocab, scale, out, None if ws is None else ws.data_ptr(), need, _current(dev))
+    empty, f32 = logits.new_empty, _torch.float32
+    lse, entropy = empty(rows, dtype=f32), empty(rows, dtype=f32)
+    token_lp = ids = top_lp = None
+    pt = pi = pl = 0
+    if tokens is not None:
+        token_lp = empty((rows, ntok), dtype=f32)
+        if ntok:
+            pt = token_lp.data_ptr()
+    if top:
+        ids, top_lp = empty((rows, top), dtype=_torch.int32), empty((rows, top), dtype=f32)
+        pi, pl = ids.data_ptr(), top_lp.data_ptr()
+    lib = _packed_calls()
+    ws, need, keep = _workspace(workspace, lib.qk_logprobs_workspace_bytes(za, rows, vocab, top) if workspace is None else 0,
+                                logits)
+    out = _PROBS(tp if ntok else 0, pt, lse.data_ptr(), entropy.data_ptr(), pi, pl, ntok, top)
+    rc = lib.qk_logprobs(za, rows, vocab, scale, out, ws, need, _current(dev))
     if rc != QK_OK:
         raise QKError(rc, "qk_logprobs")
-    return r
+    return LogProbs(token_lp, lse, entropy, ids, top_lp)
