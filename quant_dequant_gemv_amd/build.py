@@ -13,7 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqkgemv.so")
 SOURCES = ["qk_api.hip", "qk_kernels.hip", "qk_verify.hip", "qk_verify_q4k.hip", "qk_verify_q5k.hip",
            "qk_verify_q6k.hip", "qk_verify_iq4xs.hip", "qk_kv.hip", "qk_kv_attn.hip", "qk_block.hip",
-           "qk_conv.hip", "qk_delta.hip", "qk_probs.hip"]
+           "qk_conv.hip", "qk_delta.hip", "qk_delta_chunk.hip", "qk_probs.hip"]
 CALIB_LIB = os.path.join(HERE, "libqkcalib.so")
 CALIB_SOURCES = ["qk_stream_read.hip"]
 ARCH = "gfx950"

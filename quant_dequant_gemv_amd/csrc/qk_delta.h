@@ -53,24 +53,28 @@ __device__ __forceinline__ void store1(const Heads &x, int64_t t, int h, int i, 
     if (x.f16) reinterpret_cast<_Float16 *>(x.p)[o] = (_Float16)v;
     else reinterpret_cast<float *>(x.p)[o] = v;
 }
-// Dimensions 64 p + 4 l .. + 3 of a row's head.
-template <int P>
-__device__ __forceinline__ void load_row(bool vec, const Heads &x, int64_t t, int h, int l, float (*r)[4]) {
+// P pieces of 4 dimensions of a row's head, from dimension i on, STEP apart.
+template <int P, int STEP>
+__device__ __forceinline__ void load_pieces(bool vec, const Heads &x, int64_t t, int h, int i, float (*r)[4]) {
     const int64_t o = t * x.row + h * x.head;
+    if (vec && x.f16) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const int i = 64 * p + 4 * l;
-        if (vec && x.f16) {
-            const h4 v = *reinterpret_cast<const h4 *>(reinterpret_cast<const _Float16 *>(x.p) + o + i);
+        for (int p = 0; p < P; ++p) {
+            const h4 v = *reinterpret_cast<const h4 *>(reinterpret_cast<const _Float16 *>(x.p) + o + i + STEP * p);
 #pragma unroll
             for (int e = 0; e < 4; ++e) r[p][e] = (float)v[e];
-        } else if (vec) {
-            const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(x.p) + o + i);
-            r[p][0] = v.x; r[p][1] = v.y; r[p][2] = v.z; r[p][3] = v.w;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) r[p][e] = load1(x, t, h, i + e);
         }
+    } else if (vec) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(x.p) + o + i + STEP * p);
+            r[p][0] = v.x; r[p][1] = v.y; r[p][2] = v.z; r[p][3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[p][e] = load1(x, t, h, i + STEP * p + e);
     }
 }
 
@@ -89,4 +93,9 @@ __device__ __forceinline__ Gate gates(const Args &a, int h, float al, float be) 
 }
 
 }  // namespace delta
+
+// Long sequences (qk_delta_chunk.hip); rows of length 1 and raw gates only.
+int64_t delta_chunk_workspace(const StateSeqs &q, const DeltaState &d);
+hipError_t launch_delta_chunk(const delta::Args &a, int hk, int dk, void *workspace, hipStream_t st);
+
 }  // namespace qk

@@ -51,8 +51,8 @@ template <int DK, int CPL> __global__ void __launch_bounds__(THREADS) delta_rows
         if (r < m) {
             const int t = sq.first + i0 + r;
             float q[P][4], k[P][4], v[COLS / 16];
-            load_row<P>(a.q_vec, a.qh, t, hk, l, q);
-            load_row<P>(a.k_vec, a.kh, t, hk, l, k);
+            load_pieces<P, 64>(a.q_vec, a.qh, t, hk, 4 * l, q);
+            load_pieces<P, 64>(a.k_vec, a.kh, t, hk, 4 * l, k);
 #pragma unroll
             for (int c = 0; c < COLS / 16; ++c) v[c] = load1(a.vh, t, h, c0 + l + 16 * c);
             const float al = load1(a.alpha, t, h, 0), be = load1(a.beta, t, h, 0);
@@ -140,12 +140,17 @@ template <int DK, int CPL> hipError_t go(const Args &a, int nseq, hipStream_t st
 
 }  // namespace delta
 
-int64_t delta_workspace(const StateSeqs &, const DeltaState &) { return 0; }
+// Long sequences go in tiles of 64 rows on matrix cores.
+static bool in_tiles(const StateSeqs &q) { return q.rows / q.nseq >= 64; }
 
-hipError_t launch_delta(const StateSeqs &q, const DeltaState &d, const DeltaIn &in, const Heads &out, void *,
+int64_t delta_workspace(const StateSeqs &q, const DeltaState &d) { return in_tiles(q) ? delta_chunk_workspace(q, d) : 0; }
+
+hipError_t launch_delta(const StateSeqs &q, const DeltaState &d, const DeltaIn &in, const Heads &out, void *workspace,
                         hipStream_t st) {
     using namespace delta;
     const Args a = make_args(q, d, in, out);
+    // (of rows brought to length 1 with steps in 0..1, which keep what a tile's inverse holds in fp16's range)
+    if (in_tiles(q) && in.norm && in.A) return launch_delta_chunk(a, d.hk, d.dk, workspace, st);
     // a lane's columns: few where latency counts, more where rows are made ready for many
     const int64_t columns = (int64_t)q.nseq * d.hv * d.dv;
     const int cpl = d.dv % 64 == 0 && columns >= 64 * 8 * device_cus() ? 4 : columns >= 32 * 8 * device_cus() ? 2 : 1;

@@ -215,6 +215,18 @@ def test_delta(ns, hk, hv, dk, dv, layout, dt):
                 commit=True if dk == 128 else None, fresh=hv != 1, holes=dv != 96)
 
 
+LONG = [[64], [65], [200], [63, 130, 0, 64, 129], [128] * 3, [700, 1, 66]]
+
+
+@pytest.mark.parametrize("ns", LONG)
+@pytest.mark.parametrize("hk,hv,dk,dv", [(1, 1, 128, 128), (2, 6, 128, 64), (9, 9, 64, 96), (1, 2, 64, 256)])
+@pytest.mark.parametrize("layout,dt", [("plain", F32), ("column", F32), ("odd", F16), ("wide", F16)])
+def test_delta_long(ns, hk, hv, dk, dv, layout, dt):
+    rng = np.random.default_rng(len(ns) + hv + dv)
+    check_delta(rng, ns, hk, hv, dk, dv, layout, dt, out_dt=F16 if layout == "wide" else F32, commit=True if dk == 128 else None,
+                fresh=hv != 1, holes=dv != 96)
+
+
 # ------------------------------------------------------------------ log probabilities
 
 def check_probs(z, tokens, top, scale, layout):
