@@ -21,6 +21,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "qk_delta.h"
 
@@ -92,6 +93,23 @@ template <int M> __device__ __forceinline__ void settle(f4 (&c)[M]) {
     asm volatile("s_nop 15\n\ts_nop 7" : "+v"(c[0]), "+v"(c[M - 1]));
 #pragma unroll
     for (int i = 0; i < M; ++i) asm volatile("" : "+v"(c[i]));
+}
+
+// c[i] += (a_i in two parts) (b in two parts), operand a_i at a(i): the M
+// results take turns, so no instruction waits for the one before it.
+template <int M, typename F> __device__ __forceinline__ void mma3_all(F a, h8 bh, h8 bl, f4 *c) {
+    h8 ah[M], al[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        ah[i] = a(2 * i);
+        al[i] = a(2 * i + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < M; ++i) c[i] = mma(al[i], bh, c[i]);
+#pragma unroll
+    for (int i = 0; i < M; ++i) c[i] = mma(ah[i], bl, c[i]);
+#pragma unroll
+    for (int i = 0; i < M; ++i) c[i] = mma(ah[i], bh, c[i]);
 }
 
 __device__ __forceinline__ void split(float x, _Float16 &hi, _Float16 &lo) {
@@ -345,7 +363,7 @@ template <int DK> __global__ void __launch_bounds__(TILE_THREADS) delta_tile_ker
 
 // ------------------------------------------------------------------ scan
 
-constexpr int SCAN_WAVES = 4;
+constexpr int SCAN_WAVES = 6, LOADERS = 2;
 
 // 16 bytes a lane from memory to LDS, the lanes' side by side from `to` on.
 __device__ __forceinline__ void to_lds(const void *from, void *to) {
@@ -357,8 +375,9 @@ __device__ __forceinline__ void to_lds(const void *from, void *to) {
 // have 16 columns each: K^ S0 -> U -> the next state; waves 2 and 3 make the
 // same columns' outputs from the states and U that those leave in LDS.  A tile
 // is two phases with a barrier behind each; the operands of one phase come to
-// LDS during the other.
-template <int DK> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_kernel(Args a, Chunks ck) {
+// LDS during the other, brought by waves 4 and 5 (a wave that brings them waits
+// for them all at its next read of LDS).
+template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_kernel(Args a, Chunks ck) {
     constexpr int KB = DK / 32, DT = DK / 16, PART = Sizes<DK>::PART;
     constexpr int PIECES = PART * 2 / 1024, TRI_PIECES = TRI * 2;  // of 1 KB
     extern __shared__ __align__(16) uint8_t lds[];
@@ -384,9 +403,9 @@ template <int DK> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_
     // 1 KB pieces of an operand to LDS, wave after wave
     auto bring = [&](const _Float16 *from, _Float16 *to, int pieces) {
 #pragma unroll
-        for (int i = 0; i < (pieces + SCAN_WAVES - 1) / SCAN_WAVES; ++i) {
-            const int p = i * SCAN_WAVES + w;
-            if (p < pieces) to_lds(from + p * FRAG + lane * 8, to + p * FRAG);
+        for (int i = 0; i < pieces / LOADERS; ++i) {
+            const int p = i * LOADERS + w - 4;
+            to_lds(from + p * FRAG + lane * 8, to + p * FRAG);
         }
     };
     auto tile_rows = [&](int j) { return ck.rows + ((int64_t)(t0 + j - ck.first) * hk_n + hk) * 3 * PART; };
@@ -395,7 +414,7 @@ template <int DK> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_
         bring(tile_rows(j), K_s, PIECES);
         bring(tile_rows(j) + PART, Q_s, PIECES);
         bring(tile_tri(j), T_s, TRI_PIECES);
-        if (w == 3) to_lds(ck.vec + ((int64_t)(t0 + j - ck.first) * a.hv + h) * 256 + lane * 4, vec_s + (j & 1) * 256);
+        if (w == 4) to_lds(ck.vec + ((int64_t)(t0 + j - ck.first) * a.hv + h) * 256 + lane * 4, vec_s + (j & 1) * 256);
     };
     auto meet = [&]() {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -403,9 +422,17 @@ template <int DK> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_
     };
     auto frag = [&](const _Float16 *p, int i) { return reinterpret_cast<const h8 *>(p + i * FRAG)[lane]; };
 
+    // a lower triangle of 64 x 64 times 64 rows
+    auto triangle = [&](const _Float16 *p, const h8 *bh, const h8 *bl, f4(&c)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = f4{0, 0, 0, 0};
+        mma3_all<4>([&](int i) { return frag(p, tri_index(i >> 1, 0) * 2 + (i & 1)); }, bh[0], bl[0], c);
+        mma3_all<2>([&](int i) { return frag(p, tri_index(2 + (i >> 1), 1) * 2 + (i & 1)); }, bh[1], bl[1], c + 2);
+    };
+
     f4 S[DT];
     h8 sh[KB], sl[KB];
-    f4 V[4];
+    V_T raw[4][4];
     float down = 1.f;  // of the state's column
     auto part_state = [&]() {  // the state in two parts, for both waves of the columns
         float m = 0;
@@ -424,22 +451,31 @@ template <int DK> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_
         }
         if (g == 0) unit_s[w * 16 + x] = down;
     };
-    auto fetch = [&](int j) {  // values of tile j
+    auto fetch = [&](int j) {  // values of tile j (those past its end: of its last row)
         const int r0 = tile_row(sq, sp, j), n = tile_end(sq, sp, j) - r0;
+        const V_T *p = reinterpret_cast<const V_T *>(a.vh.p) + (int64_t)(sq.first + r0) * a.vh.row + h * a.vh.head + col * a.vh.elem;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = 16 * i + 4 * g + r;
-                V[i][r] = t < n ? load1(a.vh, sq.first + r0 + t, h, col) : 0.f;
-            }
+            for (int r = 0; r < 4; ++r) raw[i][r] = p[min(16 * i + 4 * g + r, n - 1) * a.vh.row];
     };
     auto leave = [&](float *p) {
 #pragma unroll
         for (int i = 0; i < DT; ++i) *reinterpret_cast<f4 *>(p + 16 * i) = S[i];
     };
 
-    bring_first(j0);
+    if (w >= 4) {
+        bring_first(j0);
+        meet();
+        for (int j = j0; j < j1; ++j) {
+            bring(tile_rows(j) + 2 * PART, KT_s, PIECES);
+            bring(tile_tri(j) + TRI * 2 * FRAG, A_s, TRI_PIECES);
+            meet();
+            if (j + 1 < j1) bring_first(j + 1);
+            meet();
+        }
+        return;
+    }
     if (chain) {
         const float *from = j0 > 0 ? ck.carry + (ck.turn ^ 1) * slot + cell : sq.src >= 0 ? a.pool + sq.src * slot + cell : nullptr;
 #pragma unroll
@@ -450,8 +486,6 @@ template <int DK> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_
     meet();
     for (int j = j0; j < j1; ++j) {
         const float *vec = vec_s + (j & 1) * 256;
-        bring(tile_rows(j) + 2 * PART, KT_s, PIECES);
-        bring(tile_tri(j) + TRI * 2 * FRAG, A_s, TRI_PIECES);
         f4 acc[4];
         if (chain || a.out.p) {  // K^ S0, or Q^ S0
             const _Float16 *X = chain ? K_s : Q_s;
@@ -464,24 +498,24 @@ template <int DK> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_
                 down = unit_s[(w - 2) * 16 + x];
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[i] = f4{0, 0, 0, 0};
+            for (int i = 0; i < 4; ++i) acc[i] = f4{0, 0, 0, 0};
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-                    acc[i] = mma3(frag(X, (i * KB + kb) * 2), frag(X, (i * KB + kb) * 2 + 1), sh[kb], sl[kb], acc[i]);
-            }
+            for (int kb = 0; kb < KB; ++kb)
+                mma3_all<4>([&](int i) { return frag(X, ((i >> 1) * KB + kb) * 2 + (i & 1)); }, sh[kb], sl[kb], acc);
             settle(acc);
         }
         f4 U[4];
         if (chain) {
             const float f = -down * (1.f / ROW_UNIT);
+            const int n = tile_end(sq, sp, j) - tile_row(sq, sp, j);
             float m = 0;
+            f4 V[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f4 ge = *reinterpret_cast<const f4 *>(vec + 16 * i + 4 * g);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    V[i][r] = fmaf(f * ge[r], acc[i][r], V[i][r]);
+                    V[i][r] = 16 * i + 4 * g + r < n ? fmaf(f * ge[r], acc[i][r], (float)raw[i][r]) : 0.f;
                     m = fmaxf(m, fabsf(V[i][r]));
                 }
             }
@@ -489,13 +523,7 @@ template <int DK> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_
             h8 rh[2], rl[2];
             split8(V[0], V[1], u.up, rh[0], rl[0]);
             split8(V[2], V[3], u.up, rh[1], rl[1]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                U[i] = f4{0, 0, 0, 0};
-#pragma unroll
-                for (int kb = 0; kb < (i < 2 ? 1 : 2); ++kb)
-                    U[i] = mma3(frag(T_s, tri_index(i, kb) * 2), frag(T_s, tri_index(i, kb) * 2 + 1), rh[kb], rl[kb], U[i]);
-            }
+            triangle(T_s, rh, rl, U);
             settle(U);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -505,7 +533,6 @@ template <int DK> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_
             }
         }
         meet();
-        if (j + 1 < j1) bring_first(j + 1);
         if (chain) {
             if (j + 1 < j1) fetch(j + 1);
             float m = 0;
@@ -525,12 +552,12 @@ template <int DK> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_
             const float keep = vec[192], f = u.down * (1.f / ROW_UNIT);
             f4 add[DT];
 #pragma unroll
-            for (int i = 0; i < DT; ++i) {
-                add[i] = f4{0, 0, 0, 0};
+            for (int i = 0; i < DT; ++i) add[i] = f4{0, 0, 0, 0};
+#pragma unroll
+            for (int i0 = 0; i0 < DT; i0 += 4)
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
-                    add[i] = mma3(frag(KT_s, (i * 2 + kb) * 2), frag(KT_s, (i * 2 + kb) * 2 + 1), uh[kb], ul[kb], add[i]);
-            }
+                    mma3_all<4>([&](int i) { return frag(KT_s, ((i0 + (i >> 1)) * 2 + kb) * 2 + (i & 1)); }, uh[kb], ul[kb], add + i0);
             settle(add);
 #pragma unroll
             for (int i = 0; i < DT; ++i)
@@ -553,23 +580,25 @@ template <int DK> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_
             const int r0 = tile_row(sq, sp, j), n = tile_end(sq, sp, j) - r0;
             const float f = a.scale * down * (1.f / ROW_UNIT), fu = a.scale * u.down * (1.f / TRI_UNIT);
             f4 o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                o[i] = f4{0, 0, 0, 0};
-#pragma unroll
-                for (int kb = 0; kb < (i < 2 ? 1 : 2); ++kb)
-                    o[i] = mma3(frag(A_s, tri_index(i, kb) * 2), frag(A_s, tri_index(i, kb) * 2 + 1), uh[kb], ul[kb], o[i]);
-            }
+            triangle(A_s, uh, ul, o);
             settle(o);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f4 we = *reinterpret_cast<const f4 *>(vec + 64 + 16 * i + 4 * g);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = 16 * i + 4 * g + r;
-                    if (t < n) store1(a.out, sq.first + r0 + t, h, col, fmaf(f * we[r], acc[i][r], fu * o[i][r]));
-                }
+                for (int r = 0; r < 4; ++r) o[i][r] = fmaf(f * we[r], acc[i][r], fu * o[i][r]);
             }
+            const int64_t at = (sq.first + r0 + 4 * g) * a.out.row + h * a.out.head + col * a.out.elem;
+            auto put = [&](auto *p) {
+                p += at;
+#pragma unroll
+                for (int i = 0; i < 4; ++i, p += 12 * a.out.row)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r, p += a.out.row)
+                        if (16 * i + 4 * g + r < n) *p = (std::remove_reference_t<decltype(*p)>)o[i][r];
+            };
+            if (a.out.f16) put(reinterpret_cast<_Float16 *>(a.out.p));
+            else put(reinterpret_cast<float *>(a.out.p));
         }
         meet();
     }
@@ -595,9 +624,9 @@ Plan plan_of(const StateSeqs &q, int hk, int hv, int dk, int dv) {
     return {tiles, each, each * one + (each < tiles ? 2 * (int64_t)hv * dv * dk * 4 : 0)};
 }
 
-template <int DK> hipError_t go(const Args &a, int hk, void *workspace, hipStream_t st) {
+template <int DK, typename V_T> hipError_t go(const Args &a, int hk, void *workspace, hipStream_t st) {
     const Plan pl = plan_of(a.q, hk, a.hv, DK, a.dv);
-    const hipError_t e = lds_opt_in<delta_scan_kernel<DK>>(scan_lds<DK>());
+    const hipError_t e = lds_opt_in<delta_scan_kernel<DK, V_T>>(scan_lds<DK>());
     if (e != hipSuccess) return e;
     uint8_t *p = (uint8_t *)workspace;
     Chunks ck;
@@ -614,7 +643,7 @@ template <int DK> hipError_t go(const Args &a, int hk, void *workspace, hipStrea
         ck.count = std::min(pl.each, pl.tiles - first);
         ck.turn = i & 1;
         hipLaunchKernelGGL(delta_tile_kernel<DK>, dim3((unsigned)((int64_t)ck.count * hk)), dim3(TILE_THREADS), 0, st, a, ck);
-        hipLaunchKernelGGL(delta_scan_kernel<DK>, dim3((unsigned)(groups * a.rep * (a.dv / N))), dim3(64 * SCAN_WAVES), scan_lds<DK>(), st,
+        hipLaunchKernelGGL((delta_scan_kernel<DK, V_T>), dim3((unsigned)(groups * a.rep * (a.dv / N))), dim3(64 * SCAN_WAVES), scan_lds<DK>(), st,
                            a, ck);
     }
     return hipGetLastError();
@@ -625,7 +654,8 @@ template <int DK> hipError_t go(const Args &a, int hk, void *workspace, hipStrea
 int64_t delta_chunk_workspace(const StateSeqs &q, const DeltaState &d) { return delta::plan_of(q, d.hk, d.hv, d.dk, d.dv).bytes; }
 
 hipError_t launch_delta_chunk(const delta::Args &a, int hk, int dk, void *workspace, hipStream_t st) {
-    return dk == 64 ? delta::go<64>(a, hk, workspace, st) : delta::go<128>(a, hk, workspace, st);
+    if (a.vh.f16) return dk == 64 ? delta::go<64, _Float16>(a, hk, workspace, st) : delta::go<128, _Float16>(a, hk, workspace, st);
+    return dk == 64 ? delta::go<64, float>(a, hk, workspace, st) : delta::go<128, float>(a, hk, workspace, st);
 }
 
 }  // namespace qk
