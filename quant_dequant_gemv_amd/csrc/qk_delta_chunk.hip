@@ -95,21 +95,22 @@ template <int M> __device__ __forceinline__ void settle(f4 (&c)[M]) {
     for (int i = 0; i < M; ++i) asm volatile("" : "+v"(c[i]));
 }
 
-// c[i] += (a_i in two parts) (b in two parts), operand a_i at a(i): the M
-// results take turns, so no instruction waits for the one before it.
-template <int M, typename F> __device__ __forceinline__ void mma3_all(F a, h8 bh, h8 bl, f4 *c) {
-    h8 ah[M], al[M];
+// c[2 i + ct] += (a_i in two parts) (b_ct in two parts), without the product
+// of the two small parts: M x 2 results that take turns, so no instruction
+// waits for the one before it.
+template <int M, typename F> __device__ __forceinline__ void mma3_grid(F a, const h8 *bh, const h8 *bl, f4 *c) {
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-        ah[i] = a(2 * i);
-        al[i] = a(2 * i + 1);
-    }
+    for (int i = 0; i < M; ++i)
 #pragma unroll
-    for (int i = 0; i < M; ++i) c[i] = mma(al[i], bh, c[i]);
+        for (int ct = 0; ct < 2; ++ct) c[2 * i + ct] = mma(a(i, 1), bh[ct], c[2 * i + ct]);
 #pragma unroll
-    for (int i = 0; i < M; ++i) c[i] = mma(ah[i], bl, c[i]);
+    for (int i = 0; i < M; ++i)
 #pragma unroll
-    for (int i = 0; i < M; ++i) c[i] = mma(ah[i], bh, c[i]);
+        for (int ct = 0; ct < 2; ++ct) c[2 * i + ct] = mma(a(i, 0), bl[ct], c[2 * i + ct]);
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) c[2 * i + ct] = mma(a(i, 0), bh[ct], c[2 * i + ct]);
 }
 
 __device__ __forceinline__ void split(float x, _Float16 &hi, _Float16 &lo) {
@@ -129,13 +130,26 @@ __device__ __forceinline__ void split8(f4 a, f4 b, float s, h8 &hi, h8 &lo) {
         lo[i + 4] = l;
     }
 }
-// The power of two that brings a column's largest value (over the four lanes
-// that have it) to 2^14 .. 2^15, and its inverse.
+__device__ __forceinline__ float most8(f4 a, f4 b) {
+    float m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(a[i]), fabsf(b[i])));
+    return m;
+}
+// The largest over the four lanes of equal lane & 15, of values >= 0 (whose
+// bits are ordered as they are).
+__device__ __forceinline__ float over_rows(float m) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, m);
+    const auto p = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    const uint32_t c = max(p[0], p[1]);
+    const auto q = __builtin_amdgcn_permlane32_swap(c, c, false, false);
+    return __builtin_bit_cast(float, max(q[0], q[1]));
+}
+// The power of two that brings values up to m (of its binade) below 2^15, and
+// its inverse.
 struct Unit { float up, down; };
-__device__ __forceinline__ Unit unit_of(float m) {
-    m = fmaxf(m, __shfl_xor(m, 16));
-    m = fmaxf(m, __shfl_xor(m, 32));
-    const int e = min(max((int)(__builtin_bit_cast(uint32_t, m) >> 23), 32), 254);  // exponent + 127
+__device__ __forceinline__ Unit unit_at(float m) {
+    const int e = min(max((int)(__builtin_bit_cast(uint32_t, m) >> 23), 32), 248);  // exponent + 127
     return {__builtin_bit_cast(float, (uint32_t)(268 - e) << 23), __builtin_bit_cast(float, (uint32_t)(e - 14) << 23)};
 }
 
@@ -363,250 +377,333 @@ template <int DK> __global__ void __launch_bounds__(TILE_THREADS) delta_tile_ker
 
 // ------------------------------------------------------------------ scan
 
-constexpr int SCAN_WAVES = 6, LOADERS = 2;
+constexpr int SCAN_WAVES = 8;
 
-// 16 bytes a lane from memory to LDS, the lanes' side by side from `to` on.
-__device__ __forceinline__ void to_lds(const void *from, void *to) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t *)from,
-                                     (__attribute__((address_space(3))) uint32_t *)to, 16, 0, 0);
+// LDS of a block is complete for every wave (loads from memory stay under way).
+__device__ __forceinline__ void meet() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// N columns of a head's state through the tiles of a sequence.  Waves 0 and 1
-// have 16 columns each: K^ S0 -> U -> the next state; waves 2 and 3 make the
-// same columns' outputs from the states and U that those leave in LDS.  A tile
-// is two phases with a barrier behind each; the operands of one phase come to
-// LDS during the other, brought by waves 4 and 5 (a wave that brings them waits
-// for them all at its next read of LDS).
+// What the waves of a scan block pass on: operands in two parts (16 columns x
+// twice, ct) and what they were scaled by.
+template <int KB> struct Passed {
+    h8 S[KB][2][2][64];
+    h8 R[2][2][2][64];   // [rows 0..31, 32..63]
+    h8 U[2][2][2][64];   // e^(G_last - G) c U
+    f4 out[4][2][64];    // U in fp32
+    float Sd[KB][2][16]; // a state's value is its parts times this
+    float Vm[4][2][16];  // largest |V| of a row tile's columns
+};
+
+// N columns of a head's state through the tiles of a sequence.  Waves 0..3
+// carry the state on: wave q has 32 of its dimensions (in registers, fp32; none
+// with DK = 64 and q > 1) and 16 of a tile's rows, waves 4..7 make the outputs
+// of 16 rows each.  So a matrix operand of the tile is read by one wave only,
+// straight from memory into registers, a tile ahead.
+//   phase 1  K^ S0 -> R = V - e^G c K^ S0    | Q^ S0
+//   phase 2  U = T R
+//   phase 3  the state, in two parts for the next tile | A U, outputs
+// R and U are scaled by bounds that are known before them (rows of K^ have
+// length 1, rows of T at most 64 elements up to 1), so no maximum is in the way.
 template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVES) delta_scan_kernel(Args a, Chunks ck) {
-    constexpr int KB = DK / 32, DT = DK / 16, PART = Sizes<DK>::PART;
-    constexpr int PIECES = PART * 2 / 1024, TRI_PIECES = TRI * 2;  // of 1 KB
-    extern __shared__ __align__(16) uint8_t lds[];
-    _Float16 *K_s = reinterpret_cast<_Float16 *>(lds), *Q_s = K_s + PART, *KT_s = Q_s + PART, *T_s = KT_s + PART,
-             *A_s = T_s + TRI * 2 * FRAG, *S_s = A_s + TRI * 2 * FRAG;   // S_s: [2][KB][2][FRAG]
-    float *U_s = reinterpret_cast<float *>(S_s + 2 * KB * 2 * FRAG);     // [2][4][64][4]
-    float *vec_s = U_s + 2 * 4 * 64 * 4;                                 // [2][256]
-    float *unit_s = vec_s + 2 * 256;                                     // [2][16]: of the state's columns
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), x = lane & 15, g = lane >> 4;
+    constexpr int KB = DK / 32, PART = Sizes<DK>::PART, F = FRAG / 8;
+    __shared__ Passed<KB> sh;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), x = lane & 15, g = lane >> 4, q = w & 3;
     // blocks of one key head and sequence are 8 apart: on one XCD, whose L2 they share
     const int hk_n = a.hv / a.rep, slabs = a.dv / N, per = a.rep * slabs;
     const int64_t b = blockIdx.x, group = b % 8 + 8 * (b / (8 * per));
     if (group >= (int64_t)a.q.nseq * hk_n) return;
     const int member = (int)(b / 8 % per), s = (int)(group / hk_n), hk = (int)(group % hk_n), h = hk * a.rep + member / slabs;
-    const int col = member % slabs * N + 16 * (w & 1) + x;
+    const int col = member % slabs * N + x;  // and 16 on
     const SeqState sq = seq_state(a.q, s);
     const Span sp = span_of(sq, a.out.p != nullptr);
     const int t0 = first_tile(a.q, s), j0 = max(ck.first - t0, 0), j1 = min(ck.first + ck.count - t0, sp.count);
     if (j0 >= j1) return;
-    const bool chain = w < 2;
-    const int64_t cell = ((int64_t)h * a.dv + col) * DK + 4 * g, slot = (int64_t)a.hv * a.dv * DK;
 
-    // 1 KB pieces of an operand to LDS, wave after wave
-    auto bring = [&](const _Float16 *from, _Float16 *to, int pieces) {
+    auto rows_of = [&](int j) { return reinterpret_cast<const h8 *>(ck.rows + ((int64_t)(t0 + j - ck.first) * hk_n + hk) * 3 * PART) + lane; };
+    auto tri_of = [&](int j) { return reinterpret_cast<const h8 *>(ck.tri + ((int64_t)(t0 + j - ck.first) * a.hv + h) * (2 * TRI * 2 * FRAG)) + lane; };
+    auto vec_of = [&](int j) { return ck.vec + ((int64_t)(t0 + j - ck.first) * a.hv + h) * 256; };
+    // (loads are waited for in the order they are issued in: none in the phase that issues it)
+    h8 X[KB][2], Y[2][2];  // the wave's rows of K^ or Q^, and of T or A
+    f4 ve;                 // of e^G c or e^G e
+    auto bring_rows = [&](int j, int which) {
+        const h8 *p = rows_of(j) + (which * 4 + q) * KB * 2 * F;
 #pragma unroll
-        for (int i = 0; i < pieces / LOADERS; ++i) {
-            const int p = i * LOADERS + w - 4;
-            to_lds(from + p * FRAG + lane * 8, to + p * FRAG);
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) X[kb][i] = p[(kb * 2 + i) * F];
+        ve = *reinterpret_cast<const f4 *>(vec_of(j) + 64 * which + 16 * q + 4 * g);
+    };
+    auto bring_tri = [&](int j, int which) {
+        const h8 *p = tri_of(j) + which * TRI * 2 * F;
+        const int first = q < 2 ? q : 2 * q - 2, second = q < 2 ? q : 2 * q - 1;  // (tri_index)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            Y[0][i] = p[(first * 2 + i) * F];
+            Y[1][i] = p[(second * 2 + i) * F];
         }
     };
-    auto tile_rows = [&](int j) { return ck.rows + ((int64_t)(t0 + j - ck.first) * hk_n + hk) * 3 * PART; };
-    auto tile_tri = [&](int j) { return ck.tri + ((int64_t)(t0 + j - ck.first) * a.hv + h) * (2 * TRI * 2 * FRAG); };
-    auto bring_first = [&](int j) {
-        bring(tile_rows(j), K_s, PIECES);
-        bring(tile_rows(j) + PART, Q_s, PIECES);
-        bring(tile_tri(j), T_s, TRI_PIECES);
-        if (w == 4) to_lds(ck.vec + ((int64_t)(t0 + j - ck.first) * a.hv + h) * 256 + lane * 4, vec_s + (j & 1) * 256);
-    };
-    auto meet = [&]() {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __syncthreads();
-    };
-    auto frag = [&](const _Float16 *p, int i) { return reinterpret_cast<const h8 *>(p + i * FRAG)[lane]; };
-
-    // a lower triangle of 64 x 64 times 64 rows
-    auto triangle = [&](const _Float16 *p, const h8 *bh, const h8 *bl, f4(&c)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = f4{0, 0, 0, 0};
-        mma3_all<4>([&](int i) { return frag(p, tri_index(i >> 1, 0) * 2 + (i & 1)); }, bh[0], bl[0], c);
-        mma3_all<2>([&](int i) { return frag(p, tri_index(2 + (i >> 1), 1) * 2 + (i & 1)); }, bh[1], bl[1], c + 2);
-    };
-
-    f4 S[DT];
-    h8 sh[KB], sl[KB];
-    V_T raw[4][4];
-    float down = 1.f;  // of the state's column
-    auto part_state = [&]() {  // the state in two parts, for both waves of the columns
-        float m = 0;
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(S[i][r]));
-        const Unit u = unit_of(m);
-        down = u.down;
+    // the wave's rows times the state
+    auto times_state = [&](f4(&c)[2]) {
+        f4 acc[KB][2];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-            split8(S[2 * kb], S[2 * kb + 1], u.up, sh[kb], sl[kb]);
-            h8 *o = reinterpret_cast<h8 *>(S_s + (w * KB + kb) * 2 * FRAG) + lane;
-            o[0] = sh[kb];
-            o[64] = sl[kb];
+            acc[kb][0] = acc[kb][1] = f4{0, 0, 0, 0};
+            const h8 bh[2] = {sh.S[kb][0][0][lane], sh.S[kb][1][0][lane]}, bl[2] = {sh.S[kb][0][1][lane], sh.S[kb][1][1][lane]};
+            mma3_grid<1>([&](int, int i) { return X[kb][i]; }, bh, bl, acc[kb]);
         }
-        if (g == 0) unit_s[w * 16 + x] = down;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) settle(acc[kb]);
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) {
+            c[ct] = f4{0, 0, 0, 0};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const float d = sh.Sd[kb][ct][x] * (1.f / ROW_UNIT);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) c[ct][r] = fmaf(d, acc[kb][ct][r], c[ct][r]);
+            }
+        }
     };
-    auto fetch = [&](int j) {  // values of tile j (those past its end: of its last row)
-        const int r0 = tile_row(sq, sp, j), n = tile_end(sq, sp, j) - r0;
-        const V_T *p = reinterpret_cast<const V_T *>(a.vh.p) + (int64_t)(sq.first + r0) * a.vh.row + h * a.vh.head + col * a.vh.elem;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) raw[i][r] = p[min(16 * i + 4 * g + r, n - 1) * a.vh.row];
+    // the wave's rows of a triangle times 64 rows, those from 32 on only where the triangle has them
+    auto times_rows = [&](auto rows, f4(&c)[2]) {
+        c[0] = c[1] = f4{0, 0, 0, 0};
+        h8 bh[2], bl[2];
+        rows(0, bh, bl);
+        mma3_grid<1>([&](int, int i) { return Y[0][i]; }, bh, bl, c);
+        settle(c);
+        if (q >= 2) {
+            rows(1, bh, bl);
+            mma3_grid<1>([&](int, int i) { return Y[1][i]; }, bh, bl, c);
+            settle(c);
+        }
     };
-    auto leave = [&](float *p) {
+    // bounds of R's columns: powers of two, from the state's and the tile's values
+    auto bound = [&](int ct) {
+        float m = sh.Sd[0][ct][x], v = sh.Vm[0][ct][x];
 #pragma unroll
-        for (int i = 0; i < DT; ++i) *reinterpret_cast<f4 *>(p + 16 * i) = S[i];
+        for (int kb = 1; kb < KB; ++kb) m = fmaxf(m, sh.Sd[kb][ct][x]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) v = fmaxf(v, sh.Vm[i][ct][x]);
+        return unit_at(fmaf(m, 12.f * 32768.f, v));  // |K^ S0| <= the length of S0's column < 12 times its largest value
     };
 
-    if (w >= 4) {
-        bring_first(j0);
+    if (w >= 4) {  // ---------------------------------------------- outputs
+        if (a.out.p) {
+            bring_rows(j0, 1);
+            bring_tri(j0, 1);
+        }
         meet();
         for (int j = j0; j < j1; ++j) {
-            bring(tile_rows(j) + 2 * PART, KT_s, PIECES);
-            bring(tile_tri(j) + TRI * 2 * FRAG, A_s, TRI_PIECES);
+            f4 qs[2];
+            Unit u[2];
+            if (a.out.p) {
+                times_state(qs);
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) qs[ct][r] *= ve[r];
+                    u[ct] = bound(ct);
+                }
+                if (j + 1 < j1) bring_rows(j + 1, 1);
+            }
             meet();
-            if (j + 1 < j1) bring_first(j + 1);
+            meet();
+            if (a.out.p) {
+                f4 au[2];
+                times_rows([&](int k, h8 *bh, h8 *bl) {
+#pragma unroll
+                    for (int ct = 0; ct < 2; ++ct)
+                        split8(sh.out[2 * k][ct][lane], sh.out[2 * k + 1][ct][lane], u[ct].up * (1.f / 64), bh[ct], bl[ct]);
+                }, au);
+                if (j + 1 < j1) bring_tri(j + 1, 1);
+                const int r0 = tile_row(sq, sp, j), n = tile_end(sq, sp, j) - r0 - 16 * q - 4 * g;
+                const int64_t at = (sq.first + r0 + 16 * q + 4 * g) * a.out.row + h * a.out.head + col * a.out.elem;
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) {
+                    const float f = u[ct].down * (64.f / TRI_UNIT);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) au[ct][r] = a.scale * fmaf(f, au[ct][r], qs[ct][r]);
+                }
+                auto put = [&](auto *p) {
+                    p += at;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r, p += a.out.row)
+                        if (r < n) {
+                            p[0] = (std::remove_reference_t<decltype(*p)>)au[0][r];
+                            p[16 * a.out.elem] = (std::remove_reference_t<decltype(*p)>)au[1][r];
+                        }
+                };
+                if (a.out.f16) put(reinterpret_cast<_Float16 *>(a.out.p));
+                else put(reinterpret_cast<float *>(a.out.p));
+            }
             meet();
         }
         return;
     }
-    if (chain) {
-        const float *from = j0 > 0 ? ck.carry + (ck.turn ^ 1) * slot + cell : sq.src >= 0 ? a.pool + sq.src * slot + cell : nullptr;
+
+    // ------------------------------------------------------------------ the state
+    const bool holds = q < KB;
+    h8 Z[2][2][2];  // K^ by the wave's dimensions, [16 of them][rows 0..31, 32..63]
+    f4 de;          // of e^(G_last - G) c
+    float keep;
+    auto bring_dims = [&](int j) {
+        const h8 *p = rows_of(j) + (2 * 4 * KB * 2 + (holds ? q : 0) * 8) * F;
 #pragma unroll
-        for (int i = 0; i < DT; ++i) S[i] = from ? *reinterpret_cast<const f4 *>(from + 16 * i) : f4{0, 0, 0, 0};
-        fetch(j0);
-        part_state();
-    }
+        for (int d = 0; d < 2; ++d)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) Z[d][k][i] = p[((d * 2 + k) * 2 + i) * F];
+        keep = vec_of(j)[192 + (lane >> 6)];  // (a vector load)
+    };
+    auto bring_de = [&](int j) { de = *reinterpret_cast<const f4 *>(vec_of(j) + 128 + 16 * q + 4 * g); };
+    V_T raw[2][4];
+    auto fetch = [&](int j) {  // values of the tile's rows (those past its end: of its last one)
+        const int r0 = tile_row(sq, sp, j), n = tile_end(sq, sp, j) - r0;
+        const V_T *p = reinterpret_cast<const V_T *>(a.vh.p) + (int64_t)(sq.first + r0) * a.vh.row + h * a.vh.head + col * a.vh.elem;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const V_T *v = p + min(16 * q + 4 * g + r, n - 1) * a.vh.row;
+            raw[0][r] = v[0];
+            raw[1][r] = v[16 * a.vh.elem];
+        }
+    };
+    auto most_v = [&]() {
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) {
+            float m = 0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf((float)raw[ct][r]));
+            m = over_rows(m);
+            if (g == 0) sh.Vm[q][ct][x] = m;
+        }
+    };
+    f4 S[2][2];  // [16 dimensions][ct]
+    auto part_state = [&]() {
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) {
+            const Unit u = unit_at(over_rows(most8(S[0][ct], S[1][ct])));
+            h8 hi, lo;
+            split8(S[0][ct], S[1][ct], u.up, hi, lo);
+            sh.S[q][ct][0][lane] = hi;
+            sh.S[q][ct][1][lane] = lo;
+            if (g == 0) sh.Sd[q][ct][x] = u.down;
+        }
+    };
+    const int64_t cell = ((int64_t)h * a.dv + col) * DK + 32 * q + 4 * g, slot = (int64_t)a.hv * a.dv * DK;
+    auto leave = [&](float *p) {
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+            for (int d = 0; d < 2; ++d) *reinterpret_cast<f4 *>(p + 16 * ct * DK + 16 * d) = S[d][ct];
+    };
+
+    const float *from = j0 > 0 ? ck.carry + (ck.turn ^ 1) * slot + cell : sq.src >= 0 ? a.pool + sq.src * slot + cell : nullptr;
+    if (!holds) from = nullptr;
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+        for (int d = 0; d < 2; ++d) S[d][ct] = from ? *reinterpret_cast<const f4 *>(from + 16 * ct * DK + 16 * d) : f4{0, 0, 0, 0};
+    fetch(j0);
+    bring_rows(j0, 0);
+    bring_tri(j0, 0);
+    bring_de(j0);
+    bring_dims(j0);
+    most_v();
+    if (holds) part_state();
     meet();
     for (int j = j0; j < j1; ++j) {
-        const float *vec = vec_s + (j & 1) * 256;
-        f4 acc[4];
-        if (chain || a.out.p) {  // K^ S0, or Q^ S0
-            const _Float16 *X = chain ? K_s : Q_s;
-            if (!chain) {
+        const int n = tile_end(sq, sp, j) - tile_row(sq, sp, j) - 16 * q - 4 * g;
+        // phase 1
+        Unit u[2];
+        {
+            f4 ks[2];
+            times_state(ks);
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    sh[kb] = frag(S_s, ((w - 2) * KB + kb) * 2);
-                    sl[kb] = frag(S_s, ((w - 2) * KB + kb) * 2 + 1);
-                }
-                down = unit_s[(w - 2) * 16 + x];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = f4{0, 0, 0, 0};
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-                mma3_all<4>([&](int i) { return frag(X, ((i >> 1) * KB + kb) * 2 + (i & 1)); }, sh[kb], sl[kb], acc);
-            settle(acc);
-        }
-        f4 U[4];
-        if (chain) {
-            const float f = -down * (1.f / ROW_UNIT);
-            const int n = tile_end(sq, sp, j) - tile_row(sq, sp, j);
-            float m = 0;
-            f4 V[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f4 ge = *reinterpret_cast<const f4 *>(vec + 16 * i + 4 * g);
+            for (int ct = 0; ct < 2; ++ct) {
+                u[ct] = bound(ct);
+                h4 hi, lo;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    V[i][r] = 16 * i + 4 * g + r < n ? fmaf(f * ge[r], acc[i][r], (float)raw[i][r]) : 0.f;
-                    m = fmaxf(m, fabsf(V[i][r]));
+                    const float R = r < n ? fmaf(-ve[r], ks[ct][r], (float)raw[ct][r]) : 0.f;
+                    _Float16 p, m;
+                    split(R * u[ct].up, p, m);
+                    hi[r] = p;
+                    lo[r] = m;
                 }
+                reinterpret_cast<h4 *>(&sh.R[q >> 1][ct][0][lane])[q & 1] = hi;
+                reinterpret_cast<h4 *>(&sh.R[q >> 1][ct][1][lane])[q & 1] = lo;
             }
-            const Unit u = unit_of(m);
-            h8 rh[2], rl[2];
-            split8(V[0], V[1], u.up, rh[0], rl[0]);
-            split8(V[2], V[3], u.up, rh[1], rl[1]);
-            triangle(T_s, rh, rl, U);
-            settle(U);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) U[i][r] *= u.down * (1.f / TRI_UNIT);
-                reinterpret_cast<f4 *>(U_s)[(w * 4 + i) * 64 + lane] = U[i];
+            if (j + 1 < j1) {
+                fetch(j + 1);
+                bring_rows(j + 1, 0);
             }
         }
         meet();
-        if (chain) {
-            if (j + 1 < j1) fetch(j + 1);
-            float m = 0;
+        // phase 2
+        {
+            f4 U[2];
+            times_rows([&](int k, h8 *bh, h8 *bl) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f4 de = *reinterpret_cast<const f4 *>(vec + 128 + 16 * i + 4 * g);
+                for (int ct = 0; ct < 2; ++ct) {
+                    bh[ct] = sh.R[k][ct][0][lane];
+                    bl[ct] = sh.R[k][ct][1][lane];
+                }
+            }, U);
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) {
+                const float f = u[ct].down * (1.f / TRI_UNIT), up = u[ct].up * (1.f / 64);
+                h4 hi, lo;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    U[i][r] *= de[r];
-                    m = fmaxf(m, fabsf(U[i][r]));
+                    U[ct][r] *= f;
+                    _Float16 p, m;
+                    split(de[r] * U[ct][r] * up, p, m);
+                    hi[r] = p;
+                    lo[r] = m;
                 }
+                sh.out[q][ct][lane] = U[ct];
+                reinterpret_cast<h4 *>(&sh.U[q >> 1][ct][0][lane])[q & 1] = hi;
+                reinterpret_cast<h4 *>(&sh.U[q >> 1][ct][1][lane])[q & 1] = lo;
             }
-            const Unit u = unit_of(m);
-            h8 uh[2], ul[2];
-            split8(U[0], U[1], u.up, uh[0], ul[0]);
-            split8(U[2], U[3], u.up, uh[1], ul[1]);
-            const float keep = vec[192], f = u.down * (1.f / ROW_UNIT);
-            f4 add[DT];
+            if (j + 1 < j1) {
+                bring_tri(j + 1, 0);
+                bring_de(j + 1);
+            }
+        }
+        meet();
+        // phase 3
+        if (holds) {
+            f4 add[4];
 #pragma unroll
-            for (int i = 0; i < DT; ++i) add[i] = f4{0, 0, 0, 0};
+            for (int i = 0; i < 4; ++i) add[i] = f4{0, 0, 0, 0};
 #pragma unroll
-            for (int i0 = 0; i0 < DT; i0 += 4)
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-                    mma3_all<4>([&](int i) { return frag(KT_s, ((i0 + (i >> 1)) * 2 + kb) * 2 + (i & 1)); }, uh[kb], ul[kb], add + i0);
+            for (int k = 0; k < 2; ++k) {
+                const h8 bh[2] = {sh.U[k][0][0][lane], sh.U[k][1][0][lane]}, bl[2] = {sh.U[k][0][1][lane], sh.U[k][1][1][lane]};
+                mma3_grid<2>([&](int d, int i) { return Z[d][k][i]; }, bh, bl, add);
+            }
             settle(add);
 #pragma unroll
-            for (int i = 0; i < DT; ++i)
+            for (int ct = 0; ct < 2; ++ct) {
+                const float f = u[ct].down * (64.f / ROW_UNIT);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[i][r] = fmaf(f, add[i][r], keep * S[i][r]);
+                for (int d = 0; d < 2; ++d)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[d][ct][r] = fmaf(f, add[2 * d + ct][r], keep * S[d][ct][r]);
+            }
             if (j + 1 == sp.before && sq.commit) leave(a.pool + sq.dst * slot + cell);
-            if (j + 1 < j1) part_state();
-        } else if (a.out.p) {
-            float m = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                U[i] = reinterpret_cast<const f4 *>(U_s)[((w - 2) * 4 + i) * 64 + lane];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(U[i][r]));
+            if (j + 1 < j1) {
+                bring_dims(j + 1);
+                part_state();
             }
-            const Unit u = unit_of(m);
-            h8 uh[2], ul[2];
-            split8(U[0], U[1], u.up, uh[0], ul[0]);
-            split8(U[2], U[3], u.up, uh[1], ul[1]);
-            const int r0 = tile_row(sq, sp, j), n = tile_end(sq, sp, j) - r0;
-            const float f = a.scale * down * (1.f / ROW_UNIT), fu = a.scale * u.down * (1.f / TRI_UNIT);
-            f4 o[4];
-            triangle(A_s, uh, ul, o);
-            settle(o);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f4 we = *reinterpret_cast<const f4 *>(vec + 64 + 16 * i + 4 * g);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[i][r] = fmaf(f * we[r], acc[i][r], fu * o[i][r]);
-            }
-            const int64_t at = (sq.first + r0 + 4 * g) * a.out.row + h * a.out.head + col * a.out.elem;
-            auto put = [&](auto *p) {
-                p += at;
-#pragma unroll
-                for (int i = 0; i < 4; ++i, p += 12 * a.out.row)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r, p += a.out.row)
-                        if (16 * i + 4 * g + r < n) *p = (std::remove_reference_t<decltype(*p)>)o[i][r];
-            };
-            if (a.out.f16) put(reinterpret_cast<_Float16 *>(a.out.p));
-            else put(reinterpret_cast<float *>(a.out.p));
         }
+        if (j + 1 < j1) most_v();
         meet();
     }
-    if (chain && j1 < sp.count) leave(ck.carry + ck.turn * slot + cell);
-}
-
-template <int DK> constexpr int scan_lds() {
-    return (3 * Sizes<DK>::PART + 2 * TRI * 2 * FRAG + 2 * (DK / 32) * 2 * FRAG) * 2 + (2 * 4 * 64 * 4 + 2 * 256 + 32) * 4;
+    if (holds && j1 < sp.count) leave(ck.carry + ck.turn * slot + cell);
 }
 
 template <int DK> int64_t tile_bytes(int hk, int hv) {
@@ -626,8 +723,6 @@ Plan plan_of(const StateSeqs &q, int hk, int hv, int dk, int dv) {
 
 template <int DK, typename V_T> hipError_t go(const Args &a, int hk, void *workspace, hipStream_t st) {
     const Plan pl = plan_of(a.q, hk, a.hv, DK, a.dv);
-    const hipError_t e = lds_opt_in<delta_scan_kernel<DK, V_T>>(scan_lds<DK>());
-    if (e != hipSuccess) return e;
     uint8_t *p = (uint8_t *)workspace;
     Chunks ck;
     ck.rows = (_Float16 *)p;
@@ -643,8 +738,7 @@ template <int DK, typename V_T> hipError_t go(const Args &a, int hk, void *works
         ck.count = std::min(pl.each, pl.tiles - first);
         ck.turn = i & 1;
         hipLaunchKernelGGL(delta_tile_kernel<DK>, dim3((unsigned)((int64_t)ck.count * hk)), dim3(TILE_THREADS), 0, st, a, ck);
-        hipLaunchKernelGGL((delta_scan_kernel<DK, V_T>), dim3((unsigned)(groups * a.rep * (a.dv / N))), dim3(64 * SCAN_WAVES), scan_lds<DK>(), st,
-                           a, ck);
+        hipLaunchKernelGGL((delta_scan_kernel<DK, V_T>), dim3((unsigned)(groups * a.rep * (a.dv / N))), dim3(64 * SCAN_WAVES), 0, st, a, ck);
     }
     return hipGetLastError();
 }
