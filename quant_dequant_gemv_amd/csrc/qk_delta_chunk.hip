@@ -386,15 +386,17 @@ __device__ __forceinline__ void meet() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 // What the waves of a scan block pass on: operands in two parts (16 columns x
 // twice, ct) and what they were scaled by.
 template <int KB> struct Passed {
-    h8 S[KB][2][2][64];
+    h8 S[2][KB][2][2][64]; // [turn]
     h8 R[2][2][2][64];   // [rows 0..31, 32..63]
     h8 U[2][2][2][64];   // e^(G_last - G) c U
     f4 out[4][2][64];    // U in fp32
-    float Sd[KB][2][16]; // a state's value is its parts times this
-    float Vm[4][2][16];  // largest |V| of a row tile's columns
+    float Sd[2][2][16][4]; // [turn][ct][x][kb]: a state's value is its parts times this (0 past KB)
+    float Vm[2][16][4];  // [ct][x][row tile]: largest |V|
 };
 
 // N columns of a head's state through the tiles of a sequence.  Waves 0..3
@@ -428,15 +430,14 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
     // (loads are waited for in the order they are issued in: none in the phase that issues it)
     h8 X[KB][2], Y[2][2];  // the wave's rows of K^ or Q^, and of T or A
     f4 ve;                 // of e^G c or e^G e
-    auto bring_rows = [&](int j, int which) {
-        const h8 *p = rows_of(j) + (which * 4 + q) * KB * 2 * F;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) X[kb][i] = p[(kb * 2 + i) * F];
-        ve = *reinterpret_cast<const f4 *>(vec_of(j) + 64 * which + 16 * q + 4 * g);
+    const int which = w >> 2;
+    auto bring_rows = [&](int j, int kb) {
+        const h8 *p = rows_of(j) + ((which * 4 + q) * KB + kb) * 2 * F;
+        X[kb][0] = p[0];
+        X[kb][1] = p[F];
     };
-    auto bring_tri = [&](int j, int which) {
+    auto bring_vec = [&](int j) { ve = *reinterpret_cast<const f4 *>(vec_of(j) + 64 * which + 16 * q + 4 * g); };
+    auto bring_tri = [&](int j) {
         const h8 *p = tri_of(j) + which * TRI * 2 * F;
         const int first = q < 2 ? q : 2 * q - 2, second = q < 2 ? q : 2 * q - 1;  // (tri_index)
 #pragma unroll
@@ -445,25 +446,37 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
             Y[1][i] = p[(second * 2 + i) * F];
         }
     };
-    // the wave's rows times the state
-    auto times_state = [&](f4(&c)[2]) {
-        f4 acc[KB][2];
+    // The wave's rows times the state, all of which is read from LDS before the first product.  Operands of the next tile
+    // come when this one's are used, into the same registers (the order is kept: others would be copied, and waited for).
+    auto times_state = [&](f4(&c)[2], int j, int jn) {
+        f4 acc[KB * 2];
+        h8 bh[KB][2], bl[KB][2];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            acc[kb][0] = acc[kb][1] = f4{0, 0, 0, 0};
-            const h8 bh[2] = {sh.S[kb][0][0][lane], sh.S[kb][1][0][lane]}, bl[2] = {sh.S[kb][0][1][lane], sh.S[kb][1][1][lane]};
-            mma3_grid<1>([&](int, int i) { return X[kb][i]; }, bh, bl, acc[kb]);
-        }
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) settle(acc[kb]);
+            for (int ct = 0; ct < 2; ++ct) {
+                bh[kb][ct] = sh.S[j & 1][kb][ct][0][lane];
+                bl[kb][ct] = sh.S[j & 1][kb][ct][1][lane];
+            }
+        in_order();
+#pragma unroll
+        for (int i = 0; i < KB * 2; ++i) acc[i] = mma(X[i / 2][1], bh[i / 2][i % 2], f4{0, 0, 0, 0});
+#pragma unroll
+        for (int i = 0; i < KB * 2; ++i) acc[i] = mma(X[i / 2][0], bl[i / 2][i % 2], acc[i]);
+#pragma unroll
+        for (int i = 0; i < KB * 2; ++i) acc[i] = mma(X[i / 2][0], bh[i / 2][i % 2], acc[i]);
+        in_order();
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) bring_rows(jn, kb);
+        settle(acc);
 #pragma unroll
         for (int ct = 0; ct < 2; ++ct) {
-            c[ct] = f4{0, 0, 0, 0};
+            const f4 d = *reinterpret_cast<const f4 *>(sh.Sd[j & 1][ct][x]) * (1.f / ROW_UNIT);
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                const float d = sh.Sd[kb][ct][x] * (1.f / ROW_UNIT);
+            for (int r = 0; r < 4; ++r) {
+                c[ct][r] = d[0] * acc[ct][r];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) c[ct][r] = fmaf(d, acc[kb][ct][r], c[ct][r]);
+                for (int kb = 1; kb < KB; ++kb) c[ct][r] = fmaf(d[kb], acc[2 * kb + ct][r], c[ct][r]);
             }
         }
     };
@@ -472,74 +485,92 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
         c[0] = c[1] = f4{0, 0, 0, 0};
         h8 bh[2], bl[2];
         rows(0, bh, bl);
+        in_order();
         mma3_grid<1>([&](int, int i) { return Y[0][i]; }, bh, bl, c);
-        settle(c);
+        if (q < 2) settle(c);
         if (q >= 2) {
             rows(1, bh, bl);
             mma3_grid<1>([&](int, int i) { return Y[1][i]; }, bh, bl, c);
             settle(c);
         }
+        in_order();
     };
     // bounds of R's columns: powers of two, from the state's and the tile's values
-    auto bound = [&](int ct) {
-        float m = sh.Sd[0][ct][x], v = sh.Vm[0][ct][x];
-#pragma unroll
-        for (int kb = 1; kb < KB; ++kb) m = fmaxf(m, sh.Sd[kb][ct][x]);
-#pragma unroll
-        for (int i = 1; i < 4; ++i) v = fmaxf(v, sh.Vm[i][ct][x]);
+    auto bound = [&](int ct, int j) {
+        const f4 m4 = *reinterpret_cast<const f4 *>(sh.Sd[j & 1][ct][x]), v4 = *reinterpret_cast<const f4 *>(sh.Vm[ct][x]);
+        const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), v = fmaxf(fmaxf(v4[0], v4[1]), fmaxf(v4[2], v4[3]));
         return unit_at(fmaf(m, 12.f * 32768.f, v));  // |K^ S0| <= the length of S0's column < 12 times its largest value
     };
 
     if (w >= 4) {  // ---------------------------------------------- outputs
+        // A U of the tile before in phase 1, its outputs in phase 2, Q^ S0 of this one in phase 3: what takes longest where
+        // the other waves have most to do.
+        f4 qs[2], au[2];
+        Unit u[2];
+        auto product = [&](int jn) {
+            times_rows([&](int k, h8 *bh, h8 *bl) {
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct)
+                    split8(sh.out[2 * k][ct][lane], sh.out[2 * k + 1][ct][lane], u[ct].up * (1.f / 64), bh[ct], bl[ct]);
+            }, au);
+            bring_tri(jn);
+        };
+        auto finish = [&](int j) {
+            const int r0 = tile_row(sq, sp, j), n = tile_end(sq, sp, j) - r0 - 16 * q - 4 * g;
+            const int64_t at = (sq.first + r0 + 16 * q + 4 * g) * a.out.row + h * a.out.head + col * a.out.elem;
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) {
+                const float f = u[ct].down * (64.f / TRI_UNIT);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) au[ct][r] = a.scale * fmaf(f, au[ct][r], qs[ct][r]);
+            }
+            // (rows past the tile's end go to the unused part of its decays: with branches around them the number of stores
+            // under way is not known, and loads from before them are waited for with all of them)
+            auto put = [&](auto *p) {
+                using T = std::remove_reference_t<decltype(*p)>;
+                T *none = reinterpret_cast<T *>(const_cast<float *>(vec_of(j)) + 196);
+                p += at;
+#pragma unroll
+                for (int r = 0; r < 4; ++r, p += a.out.row) {
+                    *(r < n ? p : none) = (T)au[0][r];
+                    *(r < n ? p + 16 * a.out.elem : none) = (T)au[1][r];
+                }
+            };
+            if (a.out.f16) put(reinterpret_cast<_Float16 *>(a.out.p));
+            else put(reinterpret_cast<float *>(a.out.p));
+        };
         if (a.out.p) {
-            bring_rows(j0, 1);
-            bring_tri(j0, 1);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) bring_rows(j0, kb);
+            bring_vec(j0);
+            bring_tri(j0);
         }
         meet();
+        meet();
         for (int j = j0; j < j1; ++j) {
-            f4 qs[2];
-            Unit u[2];
+            const int jn = min(j + 1, j1 - 1);
+            if (a.out.p && j > j0) product(j);
+            meet();
             if (a.out.p) {
-                times_state(qs);
+                if (j > j0) finish(j - 1);
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) {
+                for (int ct = 0; ct < 2; ++ct) u[ct] = bound(ct, j);
+            }
+            meet();
+            if (a.out.p) {
+                times_state(qs, j, jn);
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) qs[ct][r] *= ve[r];
-                    u[ct] = bound(ct);
-                }
-                if (j + 1 < j1) bring_rows(j + 1, 1);
+                in_order();
+                bring_vec(jn);
             }
             meet();
-            meet();
-            if (a.out.p) {
-                f4 au[2];
-                times_rows([&](int k, h8 *bh, h8 *bl) {
-#pragma unroll
-                    for (int ct = 0; ct < 2; ++ct)
-                        split8(sh.out[2 * k][ct][lane], sh.out[2 * k + 1][ct][lane], u[ct].up * (1.f / 64), bh[ct], bl[ct]);
-                }, au);
-                if (j + 1 < j1) bring_tri(j + 1, 1);
-                const int r0 = tile_row(sq, sp, j), n = tile_end(sq, sp, j) - r0 - 16 * q - 4 * g;
-                const int64_t at = (sq.first + r0 + 16 * q + 4 * g) * a.out.row + h * a.out.head + col * a.out.elem;
-#pragma unroll
-                for (int ct = 0; ct < 2; ++ct) {
-                    const float f = u[ct].down * (64.f / TRI_UNIT);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) au[ct][r] = a.scale * fmaf(f, au[ct][r], qs[ct][r]);
-                }
-                auto put = [&](auto *p) {
-                    p += at;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r, p += a.out.row)
-                        if (r < n) {
-                            p[0] = (std::remove_reference_t<decltype(*p)>)au[0][r];
-                            p[16 * a.out.elem] = (std::remove_reference_t<decltype(*p)>)au[1][r];
-                        }
-                };
-                if (a.out.f16) put(reinterpret_cast<_Float16 *>(a.out.p));
-                else put(reinterpret_cast<float *>(a.out.p));
-            }
-            meet();
+        }
+        if (a.out.p) {
+            product(j1 - 1);
+            finish(j1 - 1);
         }
         return;
     }
@@ -557,8 +588,8 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) Z[d][k][i] = p[((d * 2 + k) * 2 + i) * F];
-        keep = vec_of(j)[192 + (lane >> 6)];  // (a vector load)
     };
+    auto bring_keep = [&](int j) { keep = vec_of(j)[192 + (lane >> 6)]; };  // (a vector load)
     auto bring_de = [&](int j) { de = *reinterpret_cast<const f4 *>(vec_of(j) + 128 + 16 * q + 4 * g); };
     V_T raw[2][4];
     auto fetch = [&](int j) {  // values of the tile's rows (those past its end: of its last one)
@@ -578,19 +609,19 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
 #pragma unroll
             for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf((float)raw[ct][r]));
             m = over_rows(m);
-            if (g == 0) sh.Vm[q][ct][x] = m;
+            if (g == 0) sh.Vm[ct][x][q] = m;
         }
     };
     f4 S[2][2];  // [16 dimensions][ct]
-    auto part_state = [&]() {
+    auto part_state = [&](int j) {
 #pragma unroll
         for (int ct = 0; ct < 2; ++ct) {
             const Unit u = unit_at(over_rows(most8(S[0][ct], S[1][ct])));
             h8 hi, lo;
             split8(S[0][ct], S[1][ct], u.up, hi, lo);
-            sh.S[q][ct][0][lane] = hi;
-            sh.S[q][ct][1][lane] = lo;
-            if (g == 0) sh.Sd[q][ct][x] = u.down;
+            sh.S[j & 1][q][ct][0][lane] = hi;
+            sh.S[j & 1][q][ct][1][lane] = lo;
+            if (g == 0) sh.Sd[j & 1][ct][x][q] = u.down;
         }
     };
     const int64_t cell = ((int64_t)h * a.dv + col) * DK + 32 * q + 4 * g, slot = (int64_t)a.hv * a.dv * DK;
@@ -607,24 +638,29 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
     for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
         for (int d = 0; d < 2; ++d) S[d][ct] = from ? *reinterpret_cast<const f4 *>(from + 16 * ct * DK + 16 * d) : f4{0, 0, 0, 0};
+    if (KB < 4) (&sh.Sd[0][0][0][0])[tid] = 0;
+    meet();
     fetch(j0);
-    bring_rows(j0, 0);
-    bring_tri(j0, 0);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) bring_rows(j0, kb);
+    bring_vec(j0);
+    bring_tri(j0);
     bring_de(j0);
     bring_dims(j0);
+    bring_keep(j0);
     most_v();
-    if (holds) part_state();
+    if (holds) part_state(j0);
     meet();
     for (int j = j0; j < j1; ++j) {
-        const int n = tile_end(sq, sp, j) - tile_row(sq, sp, j) - 16 * q - 4 * g;
+        const int n = tile_end(sq, sp, j) - tile_row(sq, sp, j) - 16 * q - 4 * g, jn = min(j + 1, j1 - 1);
         // phase 1
         Unit u[2];
         {
             f4 ks[2];
-            times_state(ks);
+            times_state(ks, j, jn);
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
-                u[ct] = bound(ct);
+                u[ct] = bound(ct, j);
                 h4 hi, lo;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -637,10 +673,9 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
                 reinterpret_cast<h4 *>(&sh.R[q >> 1][ct][0][lane])[q & 1] = hi;
                 reinterpret_cast<h4 *>(&sh.R[q >> 1][ct][1][lane])[q & 1] = lo;
             }
-            if (j + 1 < j1) {
-                fetch(j + 1);
-                bring_rows(j + 1, 0);
-            }
+            in_order();
+            fetch(jn);
+            bring_vec(jn);
         }
         meet();
         // phase 2
@@ -669,10 +704,9 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
                 reinterpret_cast<h4 *>(&sh.U[q >> 1][ct][0][lane])[q & 1] = hi;
                 reinterpret_cast<h4 *>(&sh.U[q >> 1][ct][1][lane])[q & 1] = lo;
             }
-            if (j + 1 < j1) {
-                bring_tri(j + 1, 0);
-                bring_de(j + 1);
-            }
+            in_order();
+            bring_tri(jn);
+            bring_de(jn);
         }
         meet();
         // phase 3
@@ -680,11 +714,19 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
             f4 add[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) add[i] = f4{0, 0, 0, 0};
+            h8 bh[2][2], bl[2][2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const h8 bh[2] = {sh.U[k][0][0][lane], sh.U[k][1][0][lane]}, bl[2] = {sh.U[k][0][1][lane], sh.U[k][1][1][lane]};
-                mma3_grid<2>([&](int d, int i) { return Z[d][k][i]; }, bh, bl, add);
-            }
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) {
+                    bh[k][ct] = sh.U[k][ct][0][lane];
+                    bl[k][ct] = sh.U[k][ct][1][lane];
+                }
+            in_order();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) mma3_grid<2>([&](int d, int i) { return Z[d][k][i]; }, bh[k], bl[k], add);
+            in_order();
+            bring_dims(jn);
             settle(add);
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
@@ -695,12 +737,11 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
                     for (int r = 0; r < 4; ++r) S[d][ct][r] = fmaf(f, add[2 * d + ct][r], keep * S[d][ct][r]);
             }
             if (j + 1 == sp.before && sq.commit) leave(a.pool + sq.dst * slot + cell);
-            if (j + 1 < j1) {
-                bring_dims(j + 1);
-                part_state();
-            }
+            in_order();
+            bring_keep(jn);
+            part_state(j + 1);
         }
-        if (j + 1 < j1) most_v();
+        most_v();
         meet();
     }
     if (holds && j1 < sp.count) leave(ck.carry + ck.turn * slot + cell);
