@@ -676,9 +676,17 @@ typedef struct qk_delta_rows {
  *   workspace  qk_delta_workspace_bytes bytes (16-byte aligned; NULL when that is
  *          0), for this call until it has run: calls that may overlap, captured
  *          ones among them, need workspaces of their own
- * States, sums and decays are fp32.  Sums of squares of rows of q and k must be
- * below 2^126.  A non-finite value of a row makes that head's later rows of its
- * sequence and its state undefined, and touches no other sequence or head.
+ * States, sums and decays are fp32.  Sequences of many rows with norm 1 and
+ * raw gates go 64 rows at a time through the matrix instructions, every factor
+ * a sum of two fp16 values.  Accuracy, for exact S, u, a in 0..1, b in 0..1 and
+ * |k| <= 1: a column j of the state within E_t, E_t = a_t E_{t-1} + 2^-18 (a_t (1 +
+ * |g_t|) |S_{t-1,j}| + b_t |v_tj|), of its length, an output within |scale| |q_t| (E_t
+ * + 2^-18 |S_tj|) and its rounding; where 64 rows are worked on together, both also
+ * within 2^-25 of the largest |v_j| and 24 |S_j| among the last 64 rows, however
+ * small the decays have made them.  Sums of squares of rows of q and k must be
+ * below 2^126, values and states below 2^110.  A non-finite value of a row makes
+ * the rows of its head and sequence, from up to 63 rows before it on, and their
+ * state undefined, and touches no other sequence or head.
  */
 int64_t qk_delta_workspace_bytes(const qk_delta *delta, const qk_state_seqs *seqs);
 int qk_delta_rule(const qk_delta *delta, const qk_state_seqs *seqs, const qk_delta_rows *in, const qk_heads *out,

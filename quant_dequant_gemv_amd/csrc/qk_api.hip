@@ -662,10 +662,10 @@ int qk_logprobs(const qk_heads *logits, int rows, int64_t vocab, float scale, co
     int rc = check_probs(logits, rows, vocab, o->top);
     if (rc) return rc;
     if (!(scale > 0.f && scale <= 0x1p64f) || o->ntok < 0 || o->ntok > 1024) return QK_EINVAL_SHAPE;
+    if (rows == 0) return QK_OK;
     if (!o->ntok != !o->tokens || !o->ntok != !o->token_lp || !o->top != !o->top_ids || !o->top != !o->top_lp)
         return QK_EINVAL_PTR;
     if (!o->ntok && !o->top && !o->lse && !o->entropy) return QK_EINVAL_PTR;
-    if (rows == 0) return QK_OK;
     Span in[2] = {{o->tokens, 4 * (int64_t)rows * o->ntok}, {}};
     if ((rc = check_heads(logits, rows, 1, vocab, false, &in[1]))) return rc;
     const qk::Probs p = to_probs(logits, rows, vocab, scale, o, o->top);

@@ -63,7 +63,7 @@ template <int T, int C> __global__ void __launch_bounds__(THREADS) conv_kernel(A
         const int64_t tile = u / a.chunks;
         const int c = ((int)(u % a.chunks) * THREADS + threadIdx.x) * C;
         const Tile tl = state_tile(a.q, tile, R, lane);
-        if (tl.s < 0) continue;
+        if (tl.s < 0 || tl.j < 0) continue;  // (below 0: of starts that decrease)
         const SeqState sq = seq_state(a.q, tl.s);
         const int i0 = tl.j * R, i1 = min(i0 + R, sq.n);
         if (i0 >= i1 || c >= a.c.channels) continue;

@@ -78,25 +78,40 @@ template <int DK, int CPL> __global__ void __launch_bounds__(THREADS) delta_rows
             if (l == 0) g_s[r] = make_float4(expf(g.g), g.b, kq * rq * rk, 0);
         }
         __syncthreads();
-        for (int i = 0; i < m; ++i) {
-            const float4 g = g_s[i];
-            float4 q[P], k[P];
+        // with one column a lane a row's numbers come from LDS while the row before is worked on
+        struct Now {
+            float4 q[P], k[P], g;
+            float v[CPL];
+        };
+        auto read = [&](int i, Now &r) {
+            r.g = g_s[i];
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                q[p] = q_s[i][p][l];
-                k[p] = k_s[i][p][l];
+                r.q[p] = q_s[i][p][l];
+                r.k[p] = k_s[i][p][l];
             }
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) r.v[c] = v_s[i][col + 4 * c];
+        };
+        auto step = [&](int i, const Now &r) {
+            const float4 g = r.g, *q = r.q, *k = r.k;
             float d[CPL], e[CPL];
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
-                d[c] = e[c] = 0;
+                float d1 = k[0].z * S[c][0][2], e1 = q[0].z * S[c][0][2];
+                d[c] = k[0].x * S[c][0][0];
+                e[c] = q[0].x * S[c][0][0];
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
-                    d[c] = fmaf(k[p].x, S[c][p][0], d[c]); e[c] = fmaf(q[p].x, S[c][p][0], e[c]);
+                    if (p) {
+                        d[c] = fmaf(k[p].x, S[c][p][0], d[c]); e[c] = fmaf(q[p].x, S[c][p][0], e[c]);
+                        d1 = fmaf(k[p].z, S[c][p][2], d1);     e1 = fmaf(q[p].z, S[c][p][2], e1);
+                    }
                     d[c] = fmaf(k[p].y, S[c][p][1], d[c]); e[c] = fmaf(q[p].y, S[c][p][1], e[c]);
-                    d[c] = fmaf(k[p].z, S[c][p][2], d[c]); e[c] = fmaf(q[p].z, S[c][p][2], e[c]);
-                    d[c] = fmaf(k[p].w, S[c][p][3], d[c]); e[c] = fmaf(q[p].w, S[c][p][3], e[c]);
+                    d1 = fmaf(k[p].w, S[c][p][3], d1);     e1 = fmaf(q[p].w, S[c][p][3], e1);
                 }
+                d[c] += d1;
+                e[c] += e1;
             }
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
@@ -105,7 +120,7 @@ template <int DK, int CPL> __global__ void __launch_bounds__(THREADS) delta_rows
             }
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
-                const float u = g.y * fmaf(-g.x, d[c], v_s[i][col + 4 * c]);
+                const float u = g.y * fmaf(-g.x, d[c], r.v[c]);
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
                     S[c][p][0] = fmaf(k[p].x, u, g.x * S[c][p][0]);
@@ -122,6 +137,23 @@ template <int DK, int CPL> __global__ void __launch_bounds__(THREADS) delta_rows
                     for (int p = 0; p < P; ++p)
                         *reinterpret_cast<float4 *>(a.pool + sq.dst * slot + cell + 4 * c * DK + 64 * p) =
                             make_float4(S[c][p][0], S[c][p][1], S[c][p][2], S[c][p][3]);
+            }
+        };
+        if constexpr (CPL == 1) {
+            Now even, odd;
+            read(0, even);
+            for (int i = 0; i < m; i += 2) {
+                read(min(i + 1, m - 1), odd);
+                step(i, even);
+                if (i + 1 >= m) break;
+                read(min(i + 2, m - 1), even);
+                step(i + 1, odd);
+            }
+        } else {  // (registers for more waves instead: 32 sequences of 32 rows 135 us, 155 with the next row's numbers ahead)
+            for (int i = 0; i < m; ++i) {
+                Now now;
+                read(i, now);
+                step(i, now);
             }
         }
         __syncthreads();
@@ -140,8 +172,12 @@ template <int DK, int CPL> hipError_t go(const Args &a, int nseq, hipStream_t st
 
 }  // namespace delta
 
-// Long sequences go in tiles of 64 rows on matrix cores.
-static bool in_tiles(const StateSeqs &q) { return q.rows / q.nseq >= 64; }
+// Long sequences go in tiles of 64 rows on matrix cores (16 key and 48 value
+// heads of 128 x 128, in a graph; rows / tiles: 1 sequence of 64 rows 25 / 34 us, of
+// 128 47 / 37, of 256 91 / 44; 8 of 64 95 / 74; 32 of 64 248 / 270, of 128 479 /
+// 383).  Where lengths differ they may be all in one sequence, which takes
+// 0.35 us a row one by one, while tiles lose less than half at 32 rows each.
+static bool in_tiles(const StateSeqs &q) { return q.rows / q.nseq >= (q.q_start ? 32 : 80); }
 
 int64_t delta_workspace(const StateSeqs &q, const DeltaState &d) { return in_tiles(q) ? delta_chunk_workspace(q, d) : 0; }
 

@@ -5,7 +5,7 @@
 // the state before it, k^ and q^ of length 1 and c, e the rows' lengths, the
 // rows of a tile solve
 //   (I + L) U = b (V - e^G c (K^ S0)),      L_tj = b_t c_t c_j e^(G_t - G_j) k^_t.k^_j   (j < t)
-//   O = scale (e^G e (Q^ S0) + A U),         A_tj = e_t c_j e^(G_t - G_j) q^_t.k^_j       (j <= t)
+//   O = scale e (e^G (Q^ S0) + A U),         A_tj = c_j e^(G_t - G_j) q^_t.k^_j           (j <= t)
 //   S = e^G_last S0 + K^T (e^(G_last - G) c U)
 // What does not depend on the state -- T = (I + L)^-1 b, A, the rows brought to
 // length 1 -- is made for all tiles at once (delta_tile_kernel); then a block
@@ -35,6 +35,7 @@ constexpr int C = 64;             // rows of a tile
 constexpr int FRAG = 512;         // halves of a matrix operand: 64 lanes x 8
 constexpr int TRI = 6;            // operands of a lower triangle of 4 x 2 (row tile, 32 columns)
 constexpr int N = 32;             // columns of a scan block
+constexpr int VEC = 5 * C;        // fp32 numbers of a tile and head
 constexpr float ROW_UNIT = 1024.f, TRI_UNIT = 16384.f;
 
 // A matrix operand's lane has row (or column) lane & 15 and, with g = lane >>
@@ -46,7 +47,7 @@ constexpr int tri_index(int row, int k) { return row < 2 ? row : row == 2 ? 2 + 
 struct Chunks {
     _Float16 *rows;   // [tiles][hk][3][...]: K^, Q^ by rows, K^ by dimensions
     _Float16 *tri;    // [tiles][hv][2][TRI][2][FRAG]: T, A
-    float *vec;       // [tiles][hv][256]: e^G c, e^G e, e^(G_last - G) c, e^G_last
+    float *vec;       // [tiles][hv][VEC]: e^G c, e^G, e^(G_last - G) c, e (64 each), e^G_last; behind it nothing is kept
     float *carry;     // [2][hv][dv][DK]: states between two launches
     int first, count; // tiles of this launch
     int turn;         // of `carry`
@@ -175,7 +176,7 @@ template <int DK> __global__ void __launch_bounds__(TILE_THREADS) delta_tile_ker
     const SeqState sq = seq_state(a.q, s);
     const Span sp = span_of(sq, a.out.p != nullptr);
     const int j = id - first_tile(a.q, s);
-    if (j < 0 || j >= sp.count) return;
+    if (j < 0 || j >= sp.count) return;  // (below 0: of starts that decrease)
     const int r0 = tile_row(sq, sp, j), n = tile_end(sq, sp, j) - r0;
 
     // Rows: a quarter of a row to a thread.
@@ -295,24 +296,25 @@ template <int DK> __global__ void __launch_bounds__(TILE_THREADS) delta_tile_ker
             G_s[lane] = G;
             b_s[lane] = b;
             const double last = __shfl(G, 63);
-            float *o = ck.vec + ((int64_t)local * a.hv + h) * 256;
+            float *o = ck.vec + ((int64_t)local * a.hv + h) * VEC;
             const float eg = expf((float)G);
             o[lane] = eg * c_s[lane];
-            o[64 + lane] = eg * e_s[lane];
+            o[64 + lane] = eg;
             o[128 + lane] = expf((float)(last - G)) * c_s[lane];
-            if (lane == 0) o[192] = expf((float)last);
+            o[192 + lane] = e_s[lane];
+            if (lane == 0) o[256] = expf((float)last);
         }
         __syncthreads();
         f4 At[4];
         const double Gt = G_s[tl];
-        const float bt = b_s[tl], ct = c_s[tl], et = e_s[tl];
+        const float bt = b_s[tl], ct = c_s[tl];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int jl = 16 * i + 4 * g + r;
                 const float d = jl <= tl ? expf((float)(Gt - G_s[jl])) * c_s[jl] : 0.f;
-                At[i][r] = d * et * kq[i][r] * (TRI_UNIT / (ROW_UNIT * ROW_UNIT));
+                At[i][r] = d * kq[i][r] * (TRI_UNIT / (ROW_UNIT * ROW_UNIT));
                 L[tl][jl] = jl < tl ? d * (bt * ct) * kk[i][r] * (1.f / (ROW_UNIT * ROW_UNIT)) : 0.f;
             }
         }
@@ -426,17 +428,20 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
 
     auto rows_of = [&](int j) { return reinterpret_cast<const h8 *>(ck.rows + ((int64_t)(t0 + j - ck.first) * hk_n + hk) * 3 * PART) + lane; };
     auto tri_of = [&](int j) { return reinterpret_cast<const h8 *>(ck.tri + ((int64_t)(t0 + j - ck.first) * a.hv + h) * (2 * TRI * 2 * FRAG)) + lane; };
-    auto vec_of = [&](int j) { return ck.vec + ((int64_t)(t0 + j - ck.first) * a.hv + h) * 256; };
+    auto vec_of = [&](int j) { return ck.vec + ((int64_t)(t0 + j - ck.first) * a.hv + h) * VEC; };
     // (loads are waited for in the order they are issued in: none in the phase that issues it)
     h8 X[KB][2], Y[2][2];  // the wave's rows of K^ or Q^, and of T or A
-    f4 ve;                 // of e^G c or e^G e
+    f4 ve, le;             // of e^G c or e^G; of e (outputs)
     const int which = w >> 2;
     auto bring_rows = [&](int j, int kb) {
         const h8 *p = rows_of(j) + ((which * 4 + q) * KB + kb) * 2 * F;
         X[kb][0] = p[0];
         X[kb][1] = p[F];
     };
-    auto bring_vec = [&](int j) { ve = *reinterpret_cast<const f4 *>(vec_of(j) + 64 * which + 16 * q + 4 * g); };
+    auto bring_vec = [&](int j) {
+        ve = *reinterpret_cast<const f4 *>(vec_of(j) + 64 * which + 16 * q + 4 * g);
+        if (which) le = *reinterpret_cast<const f4 *>(vec_of(j) + 192 + 16 * q + 4 * g);
+    };
     auto bring_tri = [&](int j) {
         const h8 *p = tri_of(j) + which * TRI * 2 * F;
         const int first = q < 2 ? q : 2 * q - 2, second = q < 2 ? q : 2 * q - 1;  // (tri_index)
@@ -505,7 +510,7 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
     if (w >= 4) {  // ---------------------------------------------- outputs
         // A U of the tile before in phase 1, its outputs in phase 2, Q^ S0 of this one in phase 3: what takes longest where
         // the other waves have most to do.
-        f4 qs[2], au[2];
+        f4 qs[2], au[2], es;  // es: the rows' lengths and the outputs' scale
         Unit u[2];
         auto product = [&](int jn) {
             times_rows([&](int k, h8 *bh, h8 *bl) {
@@ -522,13 +527,13 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
             for (int ct = 0; ct < 2; ++ct) {
                 const float f = u[ct].down * (64.f / TRI_UNIT);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) au[ct][r] = a.scale * fmaf(f, au[ct][r], qs[ct][r]);
+                for (int r = 0; r < 4; ++r) au[ct][r] = es[r] * fmaf(f, au[ct][r], qs[ct][r]);
             }
             // (rows past the tile's end go to the unused part of its decays: with branches around them the number of stores
             // under way is not known, and loads from before them are waited for with all of them)
             auto put = [&](auto *p) {
                 using T = std::remove_reference_t<decltype(*p)>;
-                T *none = reinterpret_cast<T *>(const_cast<float *>(vec_of(j)) + 196);
+                T *none = reinterpret_cast<T *>(const_cast<float *>(vec_of(j)) + 260);
                 p += at;
 #pragma unroll
                 for (int r = 0; r < 4; ++r, p += a.out.row) {
@@ -563,6 +568,7 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
                 for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) qs[ct][r] *= ve[r];
+                es = le * a.scale;
                 in_order();
                 bring_vec(jn);
             }
@@ -589,7 +595,7 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
 #pragma unroll
                 for (int i = 0; i < 2; ++i) Z[d][k][i] = p[((d * 2 + k) * 2 + i) * F];
     };
-    auto bring_keep = [&](int j) { keep = vec_of(j)[192 + (lane >> 6)]; };  // (a vector load)
+    auto bring_keep = [&](int j) { keep = vec_of(j)[256 + (lane >> 6)]; };  // (a vector load)
     auto bring_de = [&](int j) { de = *reinterpret_cast<const f4 *>(vec_of(j) + 128 + 16 * q + 4 * g); };
     V_T raw[2][4];
     auto fetch = [&](int j) {  // values of the tile's rows (those past its end: of its last one)
@@ -748,7 +754,7 @@ template <int DK, typename V_T> __global__ void __launch_bounds__(64 * SCAN_WAVE
 }
 
 template <int DK> int64_t tile_bytes(int hk, int hv) {
-    return (int64_t)hk * 3 * Sizes<DK>::PART * 2 + (int64_t)hv * (2 * TRI * 2 * FRAG * 2 + 256 * 4);
+    return (int64_t)hk * 3 * Sizes<DK>::PART * 2 + (int64_t)hv * (2 * TRI * 2 * FRAG * 2 + VEC * 4);
 }
 
 // All tiles at once, or as many as have this much (a sequence's state is
@@ -771,7 +777,7 @@ template <int DK, typename V_T> hipError_t go(const Args &a, int hk, void *works
     ck.tri = (_Float16 *)p;
     p += (int64_t)pl.each * a.hv * 2 * TRI * 2 * FRAG * 2;
     ck.vec = (float *)p;
-    p += (int64_t)pl.each * a.hv * 256 * 4;
+    p += (int64_t)pl.each * a.hv * VEC * 4;
     ck.carry = (float *)p;
     const int64_t groups = ((int64_t)a.q.nseq * hk + 7) / 8 * 8;
     for (int first = 0, i = 0; first < pl.tiles; first += pl.each, ++i) {

@@ -74,11 +74,16 @@ def conv_silu(pool, weight, bias, x, seqs, act):
     return y, err, new
 
 
-def delta_rule(pool, q, k, v, alpha, beta, seqs, A, dt, norm, eps, scale, unit=2.0 ** -18):
+def delta_rule(pool, q, k, v, alpha, beta, seqs, A, dt, norm, eps, scale, unit=2.0 ** -18, floor=2.0 ** -26):
     """out, its bound, the new pool and its bound (columns), in fp64.
 
     Every step's error, at most `unit` of what it adds up, then shrinks with the state: a (I - b k k^T) has norm <= a
-    for 0 <= b <= 2 and |k| <= 1."""
+    for 0 <= b <= 2 and |k| <= 1.
+
+    floor: where 64 rows are worked on together, V - K S0 and U are fp16 pairs on one scale a column, set by m <= max|v| + 24
+    max|S0| over those rows so that m is below 2^15 (U: 64 m): a pair ends at 2^-25, 2^-39 m (2^-33 m) of a value.  U = T R
+    sums 64 entries up to 1: 2^-33 m; with its own end 2^-32 m; a state and an output sum 64 rows of U: 2^-26 m.  Nothing of
+    that shrinks with the decays inside the 64 rows."""
     q, k, v, alpha, beta = (t.astype(np.float64) for t in (q, k, v, alpha, beta))
     rows, hv, dv = v.shape
     rep = hv // k.shape[1]
@@ -95,15 +100,21 @@ def delta_rule(pool, q, k, v, alpha, beta, seqs, A, dt, norm, eps, scale, unit=2
     for first, n, src, dst, m in seqs:
         S = np.zeros(pool.shape[1:]) if src is None else pool[src].astype(np.float64)
         E = np.zeros(S.shape[:2])  # of a column, in its norm
+        last = []                  # of the last 64 rows: |v| and 24 |S|
         for i in range(n):
             t = first + i
             a = np.exp(g[t])[:, None]
+            before = np.abs(S).max(-1)
             size = a * np.sqrt((S * S).sum(-1)) * (1 + np.abs(np.maximum(g[t], -200))[:, None])
             u = b[t][:, None] * (v[t] - a * np.einsum("hvk,hk->hv", S, k[t]))
             S = a[..., None] * S + u[..., None] * k[t][:, None]
             E = a * E + unit * (size + np.abs(b[t][:, None] * v[t])) + 2.0 ** -130
             out[t] = scale * np.einsum("hvk,hk->hv", S, q[t])
-            err[t] = abs(scale) * np.sqrt((q[t] ** 2).sum(-1))[:, None] * (E + unit * np.sqrt((S * S).sum(-1)))
+            last = last[-63:] + [np.maximum(np.abs(v[t]), 24 * before)]
+            F = 2 * floor * np.max(last, 0)
+            if i % 64 == 63 or i + 1 == m:
+                E = E + F  # (a tile's end)
+            err[t] = abs(scale) * np.sqrt((q[t] ** 2).sum(-1))[:, None] * (E + F + unit * np.sqrt((S * S).sum(-1)))
             if dst is not None and i + 1 == m:
                 new[dst], new_err[dst] = S, E
     return out, err, new, new_err
