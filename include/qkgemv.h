@@ -575,11 +575,12 @@ typedef struct qk_block {
  * any other overlap of an output with what the call reads or writes is
  * QK_EINVAL_PTR, judged by the address ranges that the views span.
  *
- * Sums of squares are fp64, and a quotient is rounded once to fp32; the rest
- * is fp32.  x is made of the fp32 h, whatever the type of h_out.  For exact n,
- * h and x of the row: n within 2^-22 |n|; h within 2^-21 |scale n act| + 2^-23
- * |h|, its e; x within 2^-22 |x| + |pre_norm| e / sqrt(mean(h^2) + eps) + 2^-20
- * |x| max_i(e_i) / sqrt(mean(h^2) + eps); each then rounded to its type.
+ * Sums of squares are fp32 in a thread and fp64 over the row (fp64 throughout
+ * where they leave 1e-25 .. 1e37), the rest is fp32.  x is made of the fp32 h,
+ * whatever the type of h_out.  For exact n, h and x of the row: n within 2^-21
+ * |n|; h within e = 2^-20 |scale n act| + 2^-23 |h|; x within 2^-21 |x| +
+ * |pre_norm| e / r + 2^-20 |x| max_i(e_i) / r, r = sqrt(mean(h^2) + eps); each then rounded
+ * to its type.  (Gates below -87: act is off by up to 2^-125 (1 + |gate|).)
  */
 int qk_block_norm(const qk_block *block, int rows, int groups, int dim, const qk_heads *y, const qk_heads *gate,
                   const qk_heads *residual, const qk_heads *h_out, const qk_heads *x_out, void *stream);

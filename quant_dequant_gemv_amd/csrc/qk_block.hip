@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#include "qk_act.h"
 #include "qk_launch.h"
 
 namespace qk {
@@ -14,8 +15,9 @@ typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 
 struct Args {
     BlockNorm b;
-    int64_t units;  // rows x groups
+    uint32_t units;  // rows x groups (at most 2^25)
     int groups, dim;
+    double inv;     // 1 / dim
     Heads y, gate, res, h, x;
 };
 
@@ -83,10 +85,20 @@ __device__ __forceinline__ void store(char *p, int64_t elem, bool f16, int tid, 
     }
 }
 
+// v of the lane `CTRL` away inside a row of 16 lanes
+template <int CTRL> __device__ __forceinline__ double dpp(double v) {
+    const uint2 w = __builtin_bit_cast(uint2, v);
+    return __builtin_bit_cast(double, make_uint2(__builtin_amdgcn_update_dpp(0, (int)w.x, CTRL, 0xf, 0xf, true),
+                                                 __builtin_amdgcn_update_dpp(0, (int)w.y, CTRL, 0xf, 0xf, true)));
+}
 // Sum over the TPG threads of a group: every one gets it.  Fixed order.
 template <int TPG, int THREADS> __device__ __forceinline__ double group_sum(double v, double *part, int tid) {
-#pragma unroll
-    for (int m = 1; m < (TPG < 64 ? TPG : 64); m *= 2) v += __shfl_xor(v, m);
+    v += dpp<0xB1>(v);   // quad_perm [1,0,3,2]
+    v += dpp<0x4E>(v);   // quad_perm [2,3,0,1]
+    v += dpp<0x141>(v);  // half row mirrored
+    v += dpp<0x140>(v);  // row mirrored
+    if (TPG > 16) v += __shfl_xor(v, 16);
+    if (TPG > 32) v += __shfl_xor(v, 32);
     if constexpr (TPG > 64) {
         static_assert(TPG == THREADS, "one group a block above a wave");
         __syncthreads();
@@ -100,22 +112,40 @@ template <int TPG, int THREADS> __device__ __forceinline__ double group_sum(doub
 }
 
 __device__ __forceinline__ float gate_of(float z, int act) {
-    return act == 0 ? z : (act == 1 ? z : 1.f) / (1.f + expf(-z));
+    return act == 0 ? z : (act == 1 ? z : 1.f) * logistic(z);
 }
-// (fp64: no row overflows or vanishes under its root)
-__device__ __forceinline__ double root(double ss, int dim, float eps) { return 1.0 / sqrt(ss / dim + (double)eps); }
 
-// x <- x / sqrt(mean x^2 + eps) * w.  The sum of squares and the product with
-// its root are fp64: no row overflows or vanishes, and the row's elements are
-// rounded twice in all (the quotient, its weight).
+// What brings a row of mean square m to length 1 an element: fp32 (the
+// hardware's root refined once) for the sums of squares that fp32 holds, 1e-25
+// to 1e37, fp64 for the others: no row overflows or vanishes.
+__device__ __forceinline__ bool ordinary(double ss) { return ss >= 1e-25 && ss <= 1e37; }
+__device__ __forceinline__ float root32(double ss, double inv, float eps) {
+    const float m = (float)fma(ss, inv, (double)eps), r = rsqrtf(m);
+    return fmaf(r, 0.5f * fmaf(-m * r, r, 1.f), r);
+}
+__device__ __forceinline__ double root64(double ss, double inv, float eps) { return 1.0 / sqrt(fma(ss, inv, (double)eps)); }
+
+// x <- x / sqrt(mean x^2 + eps) * w.  A thread's squares (E of them) are summed
+// in fp32, the threads' sums in fp64: the root is off by E / 2 + 2 halves of
+// 2^-23, an element by two more.
 template <int TPG, int THREADS, int E, bool VEC>
-__device__ __forceinline__ void norm(float *x, const float *w, float eps, int dim, int tid, double *part) {
+__device__ __forceinline__ void norm(float *x, const float *w, float eps, int dim, double inv, int tid, double *part) {
     float wv[E];
     load<TPG, E, VEC>(reinterpret_cast<const char *>(w), 1, false, tid, dim, wv);
-    double ss = 0;
+    float s = 0;
+#pragma unroll
+    for (int j = 0; j < E; ++j) s = fmaf(x[j], x[j], s);
+    double ss = group_sum<TPG, THREADS>(s, part, tid);
+    if (ordinary(ss)) {
+        const float r = root32(ss, inv, eps);
+#pragma unroll
+        for (int j = 0; j < E; ++j) x[j] = x[j] * r * wv[j];
+        return;
+    }
+    ss = 0;
 #pragma unroll
     for (int j = 0; j < E; ++j) ss = fma((double)x[j], (double)x[j], ss);
-    const double r = root(group_sum<TPG, THREADS>(ss, part, tid), dim, eps);
+    const double r = root64(group_sum<TPG, THREADS>(ss, part, tid), inv, eps);
 #pragma unroll
     for (int j = 0; j < E; ++j) x[j] = (float)((double)x[j] * r) * wv[j];
 }
@@ -126,15 +156,15 @@ template <int TPG, int THREADS, int E, bool VEC> __global__ void __launch_bounds
     __shared__ double part[THREADS / 64];
     const int tid = threadIdx.x % TPG;
     constexpr int PER = THREADS / TPG;
-    for (int64_t u0 = (int64_t)blockIdx.x * PER; u0 < a.units; u0 += (int64_t)gridDim.x * PER) {
+    for (uint32_t u0 = blockIdx.x * PER; u0 < a.units; u0 += gridDim.x * PER) {
         // (units past the end work on the last one and store nothing: all threads meet at the sums)
-        const int64_t u = u0 + threadIdx.x / TPG, uc = u < a.units ? u : a.units - 1;
-        const int64_t t = uc / a.groups, g = uc % a.groups;
+        const uint32_t u = u0 + threadIdx.x / TPG, uc = u < a.units ? u : a.units - 1;
+        const uint32_t t = uc / (uint32_t)a.groups, g = uc - t * a.groups;
         float y[E], z[E], r[E];
         load<TPG, E, VEC>(at(a.y, t, g), a.y.elem, a.y.f16, tid, a.dim, y);
         if (a.gate.p) load<TPG, E, VEC>(at(a.gate, t, g), a.gate.elem, a.gate.f16, tid, a.dim, z);
         if (a.res.p) load<TPG, E, VEC>(at(a.res, t, g), a.res.elem, a.res.f16, tid, a.dim, r);
-        if (a.b.post) norm<TPG, THREADS, E, VEC>(y, a.b.post, a.b.eps, a.dim, tid, part);
+        if (a.b.post) norm<TPG, THREADS, E, VEC>(y, a.b.post, a.b.eps, a.dim, a.inv, tid, part);
         if (a.gate.p) {
 #pragma unroll
             for (int j = 0; j < E; ++j) y[j] *= gate_of(z[j], a.b.act);
@@ -143,7 +173,7 @@ template <int TPG, int THREADS, int E, bool VEC> __global__ void __launch_bounds
         for (int j = 0; j < E; ++j) y[j] = a.res.p ? fmaf(a.b.scale, y[j], r[j]) : a.b.scale * y[j];
         if (a.h.p && u < a.units) store<TPG, E, VEC>(at(a.h, t, g), a.h.elem, a.h.f16, tid, a.dim, y);
         if (a.x.p) {
-            if (a.b.pre) norm<TPG, THREADS, E, VEC>(y, a.b.pre, a.b.eps, a.dim, tid, part);
+            if (a.b.pre) norm<TPG, THREADS, E, VEC>(y, a.b.pre, a.b.eps, a.dim, a.inv, tid, part);
             if (u < a.units) store<TPG, E, VEC>(at(a.x, t, g), a.x.elem, a.x.f16, tid, a.dim, y);
         }
     }
@@ -156,8 +186,8 @@ template <bool VEC> __global__ void __launch_bounds__(1024) block_norm_wide_kern
     extern __shared__ float row[];
     __shared__ double part[T / 64];
     const int tid = threadIdx.x;
-    for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
-        const int64_t t = u / a.groups, g = u % a.groups;
+    for (uint32_t u = blockIdx.x; u < a.units; u += gridDim.x) {
+        const uint32_t t = u / (uint32_t)a.groups, g = u - t * a.groups;
         double ss = 0, r = 1;
         // element i of a view, and E from it on
         auto from = [&](const Heads &v, int i) { return at(v, t, g) + ((i * v.elem) << (v.f16 ? 1 : 2)); };
@@ -170,7 +200,7 @@ template <bool VEC> __global__ void __launch_bounds__(1024) block_norm_wide_kern
                 ss = fma((double)y[e], (double)y[e], ss);
             }
         }
-        if (a.b.post) r = root(group_sum<T, T>(ss, part, tid), a.dim, a.b.eps);
+        if (a.b.post) r = root64(group_sum<T, T>(ss, part, tid), a.inv, a.b.eps);
         ss = 0;
         for (int i = E * tid; i < a.dim; i += E * T) {
             float z[E], s[E];
@@ -187,7 +217,7 @@ template <bool VEC> __global__ void __launch_bounds__(1024) block_norm_wide_kern
             if (a.h.p) store<T, E, VEC>(from(a.h, i), 1, a.h.f16, 0, E, z);
         }
         if (!a.x.p) continue;
-        if (a.b.pre) r = root(group_sum<T, T>(ss, part, tid), a.dim, a.b.eps);
+        if (a.b.pre) r = root64(group_sum<T, T>(ss, part, tid), a.inv, a.b.eps);
         for (int i = E * tid; i < a.dim; i += E * T) {
             float y[E];
 #pragma unroll
@@ -203,7 +233,7 @@ bool whole4(const Heads &v) {
 
 template <int TPG, int THREADS, int E> hipError_t go(const Args &a, bool vec, hipStream_t st) {
     constexpr int PER = THREADS / TPG;
-    const int64_t blocks = std::min<int64_t>((a.units + PER - 1) / PER, 1 << 20);  // (a grid stays below 2^32 threads)
+    const int64_t blocks = std::min<int64_t>(((int64_t)a.units + PER - 1) / PER, 1 << 20);  // (a grid stays below 2^32 threads)
     if (vec) hipLaunchKernelGGL((block_norm_kernel<TPG, THREADS, E, true>), dim3((unsigned)blocks), dim3(THREADS), 0, st, a);
     else hipLaunchKernelGGL((block_norm_kernel<TPG, THREADS, E, false>), dim3((unsigned)blocks), dim3(THREADS), 0, st, a);
     return hipGetLastError();
@@ -214,7 +244,7 @@ template <int TPG, int THREADS, int E> hipError_t go(const Args &a, bool vec, hi
 hipError_t launch_block_norm(const BlockNorm &b, int rows, int groups, int dim, const Heads &y, const Heads &gate,
                              const Heads &res, const Heads &h, const Heads &x, hipStream_t st) {
     using namespace block;
-    const Args a{b, (int64_t)rows * groups, groups, dim, y, gate, res, h, x};
+    const Args a{b, (uint32_t)(rows * groups), groups, dim, 1.0 / dim, y, gate, res, h, x};
     const bool vec = dim % 4 == 0 && whole4(y) && whole4(gate) && whole4(res) && whole4(h) && whole4(x) &&
                      (((uintptr_t)b.post | (uintptr_t)b.pre) & 15) == 0;
     if (dim <= 64) return go<16, 256, 4>(a, vec, st);
