@@ -248,7 +248,8 @@ hipError_t launch_block_norm(const BlockNorm &b, int rows, int groups, int dim, 
     const bool vec = dim % 4 == 0 && whole4(y) && whole4(gate) && whole4(res) && whole4(h) && whole4(x) &&
                      (((uintptr_t)b.post | (uintptr_t)b.pre) & 15) == 0;
     if (dim <= 64) return go<16, 256, 4>(a, vec, st);
-    if (dim <= 128) return go<32, 256, 4>(a, vec, st);
+    if (dim <= 128) return go<16, 256, 8>(a, vec, st);
+    if (dim <= 256) return go<32, 256, 8>(a, vec, st);
     if (dim <= 512) return go<64, 256, 8>(a, vec, st);
     if (dim <= 2048) return go<256, 256, 8>(a, vec, st);
     if (dim <= 8192) return go<1024, 1024, 8>(a, vec, st);
