@@ -488,6 +488,53 @@ def attention_stream(torch, tensors, entries, groups, fused, context):
     return out
 
 
+def token_stream(torch, tensors, entries, groups, attention, hres):
+    """The attention_stream with the rest of the layers' own work, as ("call",
+    function of a stream): a norm of the residual stream into the x of what
+    reads it; behind a DeltaNet layer's projections the short convolution of 4
+    taps over q, k and v, the recurrence (16 key and 48 value heads of 128 x 128)
+    and the norm of its heads into ssm_out's x; the gates beside the query heads
+    applied to the attention's output, in place.  (The DeltaNet layers' output
+    gates have no projection in the stream and are left out.)"""
+    from quant_dequant_gemv_amd import binding
+    hk, hv, d = 16, 48, 128
+    slot = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w_in, w_head = torch.ones(hres.numel(), device="cuda"), torch.ones(d, device="cuda")
+    A, dt = -torch.rand(hv, device="cuda"), torch.full((hv,), -3.0, device="cuda")
+    rows = lambda t, *shape: t.view(1, *shape)  # noqa: E731
+    out, at = [], 0
+
+    def call(f, *args, **kw):
+        out.append(("call", lambda h: f(*args, **kw, stream=h)))
+
+    for kind, a in attention:
+        if kind == "keep":
+            continue
+        if kind == "heads":
+            out.append((kind, a))
+            idx = groups[at - 1]
+            x = tensors[idx[-1] + 1]["x"].view(1, 24, 256)
+            call(binding.block_norm, x, gate=tensors[idx[0]]["y"].view(24, 2, 256)[None, :, 1], act="sigmoid", x_out=x)
+            continue
+        idx = groups[at]
+        at += 1
+        names = [entries[i]["name"] for i in idx]
+        if names[0] in ("attn_qkv", "attn_q", "ffn_gate"):
+            call(binding.block_norm, rows(hres, 1, -1), pre_norm=w_in, x_out=rows(tensors[idx[0]]["x"], 1, -1))
+        out.append((kind, a))
+        if names[0] == "attn_qkv":
+            qkv, alpha, beta = (rows(tensors[i]["y"], -1) for i in idx)
+            conv = binding.ConvState(1, 0.3 * torch.randn(qkv.shape[1], 4, device="cuda"))
+            state = binding.DeltaState(1, hk, hv, d, d)
+            y, o = torch.empty_like(qkv), torch.empty(1, hv, d, device="cuda")
+            q, k, v = (t.unflatten(1, (n, d)) for t, n in zip(y.split([hk * d, hk * d, hv * d], 1), (hk, hk, hv)))
+            call(binding.conv_silu, conv, qkv, slot, out=y)
+            call(binding.delta_rule, state, q, k, v, alpha, beta, slot, A=A, dt_bias=dt, out=o)
+            call(binding.block_norm, o, post_norm=w_head, x_out=tensors[idx[-1] + 1]["x"].view(1, hv, d))
+    out.append(("keep", [attention[-1], slot, w_in, w_head, A, dt]))
+    return out
+
+
 def attention_launches(stream):
     """Launches of the attention layers' own work in an attention_stream: the
     append, the attention and, where its contexts are cut into splits (it then
@@ -587,17 +634,26 @@ def run_stream(torch, launcher, warm=2, only=None, tokens=1, context=32768):
     # projections: q and k normed and rotated, k and v appended to a 4-bit
     # cache of `context` positions, attention into attn_output's x
     attention = attention_stream(torch, tensors, entries, groups, fused, context) \
-        if only is not None and only.startswith("attention") else []
+        if only is not None and only.startswith(("attention", "token")) else []
+    whole = token_stream(torch, tensors, entries, groups, attention, hres) \
+        if only is not None and only.startswith("token") else []
 
-    def one_token_attention(st=None):
+    def one_token_attention(st=None, steps=attention):
         h = sh if st is None else st
-        for kind, a in attention[:-1]:
-            if kind == "heads":
+        for kind, a in steps[:-1]:
+            if kind == "call":
+                a(h)
+            elif kind == "heads":
                 rc = lib.qk_kv_append(*a[0], h) or lib.qk_kv_attn(*a[1], h)
                 if rc != 0:
                     raise binding.QKError(rc, "attention")
             else:
                 run_fused([(kind, a)], h)
+
+    # ... and with the norms, the DeltaNet layers' convolution and recurrence
+    # and the attention's gates: a whole token but for embedding and head
+    def one_token_whole(st=None):
+        one_token_attention(st, whole)
 
     # the same fused steps as one chain launch (qk_gemv_chain): one step per
     # group, a barrier between steps, each step's first weights issued before
@@ -683,13 +739,15 @@ def run_stream(torch, launcher, warm=2, only=None, tokens=1, context=32768):
         # one variant, `tokens` tokens back to back after a warm-up (for a
         # kernel trace: the last tokens * launches dispatches are the timed ones)
         fns = {"launches": one_token, "batched": one_token_batched, "fused": one_token_fused,
-               "fused_planar": one_token_fused_planar, "attention": one_token_attention, "chain": chain_token("chain"),
-               "chain_planar": chain_token("chain_planar")}
+               "fused_planar": one_token_fused_planar, "attention": one_token_attention, "token": one_token_whole,
+               "chain": chain_token("chain"), "chain_planar": chain_token("chain_planar")}
         graph = only.endswith("_graph")
         fn = fns[only[:-6] if graph else only]
         launches = len(entries) if fn is one_token else 2 if only.startswith("chain") else len(groups)
         if fn is one_token_attention:
             launches += attention_launches(attention)
+        elif fn is one_token_whole:
+            launches += attention_launches(whole) + sum(kind == "call" for kind, _ in whole)
         if graph:
             s2 = torch.cuda.Stream()
             gr = torch.cuda.CUDAGraph()
@@ -714,7 +772,7 @@ def run_stream(torch, launcher, warm=2, only=None, tokens=1, context=32768):
         b.record(stream)
         torch.cuda.synchronize()
         sp = a.elapsed_time(b) * 1e-3 / tokens
-        more = {"context": context} if fn is one_token_attention else {}
+        more = {"context": context} if fn in (one_token_attention, one_token_whole) else {}
         return {"variant": only, **more, "tokens": tokens, "launches_per_token": launches, "warm_tokens": warm,
                 "token_ms": round(sp * 1e3, 4), "tok_s": round(1 / sp, 2)}
 
@@ -756,12 +814,12 @@ def main():
     ap.add_argument("--no-cpu", action="store_true", help="skip the CPU oracle baseline")
     ap.add_argument("--stream-only", metavar="VARIANT",
                     choices=["launches", "launches_graph", "batched", "batched_graph", "fused", "fused_graph",
-                             "fused_planar", "fused_planar_graph", "attention", "attention_graph", "chain",
-                             "chain_planar"],
+                             "fused_planar", "fused_planar_graph", "attention", "attention_graph", "token",
+                             "token_graph", "chain", "chain_planar"],
                     help="only time this decode-stream variant for --tokens tokens (for a kernel trace); "
                          "prints its own JSON line instead of the benchmark's")
     ap.add_argument("--tokens", type=int, default=5)
-    ap.add_argument("--context", type=int, default=32768, help="cache positions of the attention variants")
+    ap.add_argument("--context", type=int, default=32768, help="cache positions of the attention and token variants")
     args = ap.parse_args()
 
     if args.gpus != 1 or int(os.environ.get("WORLD_SIZE", "1")) != 1:
