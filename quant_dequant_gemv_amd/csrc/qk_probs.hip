@@ -172,13 +172,27 @@ struct Best {
 struct Args {
     Probs p;
     float scale;       // in units of log 2
-    int splits, span, subs;  // parts of a row, tokens of a block, parts of a row of one
+    int splits, span, subs;  // parts of a row, tokens of a block, parts of a row that a block leaves
     float *stats;      // [rows][splits][3]
     uint64_t *keys;    // [rows][splits][top]
 };
 
-// A row's results, from its statistics (every lane) and its sorted keys.
-__device__ __forceinline__ void finish(const Args &a, int row, const Stats &st, uint64_t key, int lane) {
+// A row's i-th asked token and its logit, two loads after one another: begun
+// before the row's statistics are there.
+struct Asked { int v; float z; };
+__device__ __forceinline__ Asked asked(const Probs &p, int row, int i) {
+    Asked q{-1, 0.f};
+    if (i >= p.ntok) return q;
+    q.v = p.tokens[(int64_t)row * p.ntok + i];
+    if (q.v < 0 || q.v >= p.vocab) return Asked{-1, 0.f};
+    const int64_t o = (int64_t)row * p.z.row + (int64_t)q.v * p.z.elem;
+    q.z = p.z.f16 ? (float)reinterpret_cast<const _Float16 *>(p.z.p)[o] : reinterpret_cast<const float *>(p.z.p)[o];
+    return q;
+}
+
+// A row's results, from its statistics (every lane), its sorted keys and the
+// first 64 asked tokens, one a lane.
+__device__ __forceinline__ void finish(const Args &a, int row, const Stats &st, uint64_t key, Asked q, int lane) {
     const Probs &p = a.p;
     const bool none = st.m == -INFINITY && st.s == 0.f;  // every token masked
     const float l2 = __builtin_amdgcn_logf(st.s), ln = l2 * LN2;  // (base 2)
@@ -188,13 +202,8 @@ __device__ __forceinline__ void finish(const Args &a, int row, const Stats &st, 
         if (p.entropy) p.entropy[row] = none ? 0.f : (l2 - st.w / st.s) * LN2;
     }
     for (int i = lane; i < p.ntok; i += 64) {
-        const int v = p.tokens[(int64_t)row * p.ntok + i];
-        float out = 0.f;  // no token
-        if (v >= 0 && v < p.vocab) {
-            const int64_t o = (int64_t)row * p.z.row + (int64_t)v * p.z.elem;
-            out = lp(p.z.f16 ? (float)reinterpret_cast<const _Float16 *>(p.z.p)[o] : reinterpret_cast<const float *>(p.z.p)[o]);
-        }
-        p.token_lp[(int64_t)row * p.ntok + i] = out;
+        if (i != lane) q = asked(p, row, i);
+        p.token_lp[(int64_t)row * p.ntok + i] = q.v < 0 ? 0.f : lp(q.z);
     }
     if (lane < p.top) {
         const int64_t o = (int64_t)row * p.top + lane;
@@ -265,7 +274,6 @@ __device__ __forceinline__ bool join_waves(Stats &st, Best &best, const Args &a,
 }
 
 __device__ __forceinline__ void leave(const Args &a, int row, int part, const Stats &st, uint64_t key, int lane) {
-    if (a.splits == 1) return finish(a, row, st, key, lane);
     const int64_t cell = (int64_t)row * a.splits + part;
     if (lane == 0) {
         float *o = a.stats + cell * 3;
@@ -275,7 +283,9 @@ __device__ __forceinline__ void leave(const Args &a, int row, int part, const St
 }
 
 // Rows whose tokens lie side by side: a block for a part of a row, STEP tokens
-// of it to a wave at a time.
+// of it to a wave at a time.  A row of one block is joined in it; of more, each
+// wave leaves a part of its own, since the join to come sorts once more anyway
+// (one row of 160000, top 20: the kernel 8.5 us with a join of the block's waves).
 template <bool F16> __global__ void __launch_bounds__(64 * ROW_WAVES) probs_row_kernel(Args a) {
     using T = std::conditional_t<F16, _Float16, float>;
     constexpr int THREADS = 64 * ROW_WAVES, N = 16 / sizeof(T), J = LANE / N;  // tokens of a piece, pieces of a lane
@@ -283,10 +293,13 @@ template <bool F16> __global__ void __launch_bounds__(64 * ROW_WAVES) probs_row_
     __shared__ Shared<ROW_WAVES> sh;
     const Probs &p = a.p;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (int64_t u = blockIdx.x; u < (int64_t)p.rows * a.splits; u += gridDim.x) {
-        const int row = (int)(u / a.splits), part = (int)(u % a.splits);
+    const int blocks_row = a.splits == 1 ? 1 : a.splits / ROW_WAVES;
+    for (int64_t u = blockIdx.x; u < (int64_t)p.rows * blocks_row; u += gridDim.x) {
+        const int row = (int)(u / blocks_row), part = (int)(u % blocks_row);
         const int v0 = part * a.span, v1 = min(v0 + a.span, p.vocab);
         const T *z = reinterpret_cast<const T *>(p.z.p) + (int64_t)row * p.z.row;
+        Asked q{-1, 0.f};
+        if (a.splits == 1 && wave == 0) q = asked(p, row, lane);
         Stats st{-INFINITY, 0, 0};
         Best best;
         best.clear();
@@ -299,13 +312,13 @@ template <bool F16> __global__ void __launch_bounds__(64 * ROW_WAVES) probs_row_
             for (int j = 0; j < J; ++j)
                 if (i + 64 * j + lane < pieces) q[j] = *reinterpret_cast<const Vec *>(z + head + (i + 64 * j + lane) * N);
         };
-        Vec q[J], nx[J];
-        load(wave * 64 * J, q);
+        Vec cur[J], nx[J];
+        load(wave * 64 * J, cur);
         for (int i = wave * 64 * J; i < pieces; i += THREADS * J) {
             load(i + THREADS * J, nx);
             float x[LANE];
 #pragma unroll
-            for (int e = 0; e < LANE; ++e) x[e] = (float)q[e / N][e % N];
+            for (int e = 0; e < LANE; ++e) x[e] = (float)cur[e / N][e % N];
             if (i + 64 * J > pieces) {
 #pragma unroll
                 for (int e = 0; e < LANE; ++e) x[e] = i + 64 * (e / N) + lane < pieces ? x[e] : -INFINITY;
@@ -314,7 +327,7 @@ template <bool F16> __global__ void __launch_bounds__(64 * ROW_WAVES) probs_row_
                        sh.sort[wave]);
             fresh = false;
 #pragma unroll
-            for (int j = 0; j < J; ++j) q[j] = nx[j];
+            for (int j = 0; j < J; ++j) cur[j] = nx[j];
         }
         auto rest = [&](int from, int to) {
             if (from >= to) return;
@@ -324,7 +337,11 @@ template <bool F16> __global__ void __launch_bounds__(64 * ROW_WAVES) probs_row_
         };
         if (wave == 0) rest(v0, head);
         if (wave == ROW_WAVES - 1) rest(tail, v1);
-        if (join_waves(st, best, a, sh, lane, wave)) leave(a, row, part, st, best.key, lane);
+        if (a.splits > 1) {
+            leave(a, row, part * ROW_WAVES + wave, over_wave(st, a.scale), best.key, lane);
+            continue;
+        }
+        if (join_waves(st, best, a, sh, lane, wave)) finish(a, row, st, best.key, q, lane);
         __syncthreads();
     }
 }
@@ -391,8 +408,11 @@ __global__ void __launch_bounds__(64 * WAVES) probs_few_kernel(Args a) {
 #pragma unroll
         for (int k = 0; k < UNITS; ++k) {
             const int unit = k * WAVES + wave;
-            if (unit < nr * a.subs)
-                leave(a, r0 + unit % nr, part * a.subs + unit / nr, over_wave(st[k], a.scale), best[k].key, lane);
+            if (unit >= nr * a.subs) continue;
+            const int row = r0 + unit % nr;
+            const Stats all = over_wave(st[k], a.scale);
+            if (a.splits == 1) finish(a, row, all, best[k].key, asked(p, row, lane), lane);
+            else leave(a, row, part * a.subs + unit / nr, all, best[k].key, lane);
         }
     }
 }
@@ -406,12 +426,14 @@ __global__ void __launch_bounds__(64 * WAVES) probs_join_kernel(Args a) {
     Best best;
     best.clear();
     const int per = (a.splits + WAVES - 1) / WAVES, first = min(wave * per, a.splits), count = min(per, a.splits - first);
-    if (top) gather(a.keys + ((int64_t)row * a.splits + first) * top, count * top, best, top, lane, sh.sort[wave]);
+    Asked q{-1, 0.f};
+    if (wave == 0) q = asked(a.p, row, lane);
     for (int i = threadIdx.x; i < a.splits; i += 64 * WAVES) {
         const float *s = a.stats + ((int64_t)row * a.splits + i) * 3;
         join(st, Stats{s[0], s[1], s[2]}, a.scale);
     }
-    if (join_waves(st, best, a, sh, lane, wave)) finish(a, row, st, best.key, lane);
+    if (top) gather(a.keys + ((int64_t)row * a.splits + first) * top, count * top, best, top, lane, sh.sort[wave]);
+    if (join_waves(st, best, a, sh, lane, wave)) finish(a, row, st, best.key, q, lane);
 }
 
 // How a call is cut: `splits` parts a row, `span` tokens to a block.
@@ -424,7 +446,9 @@ Plan plan_of(const Probs &p) {
     const int64_t want = std::max<int64_t>(1, 2 * device_cus() / units), grains = (p.vocab + grain - 1) / grain;
     const int64_t span = (grains + std::min(want, grains) - 1) / std::min(want, grains) * grain;
     pl.span = (int)std::min<int64_t>(span, INT32_MAX);
-    pl.splits = (int)((p.vocab + span - 1) / span) * pl.subs;
+    pl.splits = (int)((p.vocab + span - 1) / span);
+    if (!pl.few && pl.splits > 1) pl.subs = ROW_WAVES;
+    pl.splits *= pl.subs;
     return pl;
 }
 
