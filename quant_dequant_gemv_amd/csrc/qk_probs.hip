@@ -1,5 +1,6 @@
 // qk_probs.hip -- log probabilities of given tokens, entropy and the largest
 // alternatives of rows of logits.
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -30,6 +31,13 @@ __device__ __forceinline__ float key_value(uint64_t k) {
     const uint32_t b = (uint32_t)(k >> 32);
     return __builtin_bit_cast(float, b ^ (b >> 31 ? 0x80000000u : 0xffffffffu));
 }
+
+// A value's place in the order of values (-0 below 0), and back.
+__device__ __forceinline__ int order_of(float z) {
+    const int b = __builtin_bit_cast(int, z);
+    return b ^ (b >> 31 & 0x7fffffff);
+}
+__device__ __forceinline__ float of_order(int o) { return __builtin_bit_cast(float, o ^ (o >> 31 & 0x7fffffff)); }
 
 // Statistics of a softmax under way, t = (z - m) * scale in units of log 2:
 // the maximum, sum 2^t, sum t 2^t.
@@ -84,6 +92,15 @@ template <typename F> __device__ __forceinline__ float over_lanes(float v, F f) 
     v = f(v, dpp<0x140>(v));  // row mirrored
     return f(f(lane_of(v, 0), lane_of(v, 16)), f(lane_of(v, 32), lane_of(v, 48)));
 }
+__device__ __forceinline__ int over_lanes_max(int v) {
+    auto f = [](int a, int b) { return max(a, b); };
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xf, 0xf, true));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xf, 0xf, true));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xf, 0xf, true));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x140, 0xf, 0xf, true));
+    return f(f(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+             f(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+}
 __device__ __forceinline__ float wave_max(float v) {
     return over_lanes(v, [](float a, float b) { return fmaxf(a, b); });
 }
@@ -124,36 +141,43 @@ struct Best {
             if (lane == l) c = 0;
         }
     }
-    // The first batch: N tokens a lane, value(e) of the e-th one (-inf: none),
-    // key(e) its key, `most` the lane's largest value.  At least `top` tokens
-    // are at or above the top-th largest `most`, and few more: those go to LDS
-    // and are sorted by counting.
-    template <int N, typename V, typename K>
-    __device__ __forceinline__ void first(V value, K keyed, float most, int top, int lane, uint64_t *lds) {
-        int above = 0;
-#pragma unroll
-        for (int j = 0; j < 64; ++j)
-            above += lane_of(most, j) >= most;
-        // the largest of what at least `top` lanes reach (-inf: every token)
-        float floor = above >= top ? most : -INFINITY;
-        floor = wave_max(floor);
+    // The first batch: N tokens a lane, value(e) and token(e) of the e-th one
+    // (-inf: none), `most` the lane's largest value.  At least `top` tokens are
+    // at or above a value that `top` lanes reach with their largest, and few
+    // more: those go to LDS and are sorted by counting.  That value is found by
+    // halving, and where it leaves up to EASY lanes (about 30 tokens) it will
+    // do (comparing every lane's with every other's: 3 times the instructions).
+    template <int N, typename V, typename T>
+    __device__ __forceinline__ void first(V value, T token, float most, int top, int lane, uint64_t *lds) {
+        constexpr int EASY = 24;
+        const int o = order_of(most > -INFINITY ? most : -INFINITY), all = over_lanes_max(o);
+        int lo = ~over_lanes_max(~o), hi = all + 1;  // `top` lanes reach lo, fewer hi
+        int count = 64;
+        while (count > max(top, EASY) && (uint32_t)hi - (uint32_t)lo > 1) {
+            const int mid = (int)((uint32_t)lo + ((uint32_t)hi - (uint32_t)lo) / 2), c = __popcll(__ballot(o >= mid));
+            if (c >= top) { lo = mid; count = c; }
+            else hi = mid;
+        }
+        const float floor = fmaxf(of_order(lo), -FLT_MAX);
         int n = 0;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             const float z = value(e);
-            const bool in = z >= floor && z > -INFINITY;
-            const uint64_t m = __ballot(in);
-            const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
-            if (in && at < 64) lds[at] = keyed(e);
+            const uint64_t m = __ballot(z >= floor);
+            const int at = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, n));
+            if (z >= floor) lds[at & 63] = (uint64_t)(uint32_t)token(e) << 32 | __builtin_bit_cast(uint32_t, z);
             n += __popcll(m);
         }
         wave_sync();
         if (n <= 64) {
-            const uint64_t mine = lane < n ? lds[lane] : 0;
+            const uint64_t c = lds[lane], mine = lane < n ? key_of(__builtin_bit_cast(float, (uint32_t)c), (int)(c >> 32)) : 0;
+            wave_sync();
+            lds[lane] = mine;
+            wave_sync();
             int rank = 0;
-            for (int j = 0; j < n; j += 4) {  // (lanes from n on hold 0)
+            for (int j = 0; j < n; j += 8) {  // (lanes from n on hold 0)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) rank += lane_key(mine, j + i) > mine;
+                for (int i = 0; i < 8; ++i) rank += lds[j + i] > mine;
             }
             wave_sync();
             if (lane < n) lds[rank] = mine;
@@ -162,7 +186,7 @@ struct Best {
         } else {  // (many equals, or many asked for)
             clear();
 #pragma unroll
-            for (int e = 0; e < N; ++e) offer(value(e) >= floor && value(e) > -INFINITY ? keyed(e) : 0, top, lane);
+            for (int e = 0; e < N; ++e) offer(value(e) >= floor ? key_of(value(e), token(e)) : 0, top, lane);
         }
         limit(top);
         wave_sync();
@@ -222,7 +246,7 @@ __device__ __forceinline__ void take(const float *z, F at, bool fresh, Stats &st
     add<N>(st, z, most, scale);
     if (!top) return;
     if (fresh) {
-        best.first<N>([&](int e) { return z[e]; }, [&](int e) { return key_of(z[e], at(e)); }, most, top, lane, lds);
+        best.first<N>([&](int e) { return z[e]; }, at, most, top, lane, lds);
     } else if (__ballot(most > best.low)) {
 #pragma unroll
         for (int e = 0; e < N; ++e)
@@ -245,7 +269,7 @@ template <typename P> __device__ __forceinline__ void gather(P p, int count, Bes
             float most = value(0);
 #pragma unroll
             for (int e = 1; e < N; ++e) most = fmaxf(most, value(e));
-            best.first<N>(value, [&](int e) { return k[e]; }, most, top, lane, lds);
+            best.first<N>(value, [&](int e) { return key_token(k[e]); }, most, top, lane, lds);
         } else {
 #pragma unroll
             for (int e = 0; e < N; ++e) best.offer(k[e], top, lane);
