@@ -13,10 +13,11 @@ namespace qk {
 namespace probs {
 
 constexpr int ROW_WAVES = 4;       // waves of a block where a row's tokens lie side by side
-constexpr int WAVES = 16;          // where rows do, and where parts are joined
+constexpr int WAVES = 8;           // where rows do
+constexpr int JOIN_WAVES = 8;      // and where parts are joined
 constexpr int LANE = 16;           // tokens a lane has at a time
 constexpr int STEP = 64 * LANE;    // and a wave
-constexpr int FEW = 32;            // rows that lie side by side (elem > 1) a block has at most
+constexpr int FEW = WAVES;         // rows that lie side by side (elem > 1) a block has at most, a wave a row or more
 constexpr float LN2 = 0.693147180559945f;
 constexpr float LOW = -1e4f;  // 2^LOW is 0: terms below say nothing, and never as inf * 0
 
@@ -175,9 +176,9 @@ struct Best {
             lds[lane] = mine;
             wave_sync();
             int rank = 0;
-            for (int j = 0; j < n; j += 8) {  // (lanes from n on hold 0)
+            for (int j = 0; j < n; j += 4) {  // (lanes from n on hold 0)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) rank += lds[j + i] > mine;
+                for (int i = 0; i < 4; ++i) rank += lds[j + i] > mine;
             }
             wave_sync();
             if (lane < n) lds[rank] = mine;
@@ -379,80 +380,72 @@ __global__ void __launch_bounds__(64 * WAVES) probs_few_kernel(Args a) {
     __shared__ uint64_t sort[WAVES][64];
     const Probs &p = a.p;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int groups = (p.rows + FEW - 1) / FEW, blocks_row = a.splits / a.subs, tile = STEP * a.subs, pitch = tile + 1;
-    constexpr int UNITS = FEW / WAVES;
+    const int groups = (p.rows + FEW - 1) / FEW, per = (p.rows + groups - 1) / groups;
+    const int blocks_row = a.splits / a.subs, tile = STEP * a.subs, pitch = tile + 1;
     for (int64_t u = blockIdx.x; u < (int64_t)groups * blocks_row; u += gridDim.x) {
-        const int r0 = (int)(u / blocks_row) * FEW, nr = min(FEW, p.rows - r0), part = (int)(u % blocks_row);
+        const int r0 = (int)(u / blocks_row) * per, nr = min(per, p.rows - r0), part = (int)(u % blocks_row);
         const int v0 = part * a.span, v1 = min(v0 + a.span, p.vocab);
-        Stats st[UNITS];
-        Best best[UNITS];
-#pragma unroll
-        for (int k = 0; k < UNITS; ++k) {
-            st[k] = Stats{-INFINITY, 0, 0};
-            best[k].clear();
-        }
+        const bool mine = wave < nr * a.subs;
+        const int row = wave % nr, t0 = wave / nr * STEP;
+        Stats st{-INFINITY, 0, 0};
+        Best best;
+        best.clear();
         for (int v = v0; v < v1; v += tile) {
             const int n = min(tile, v1 - v), total = n * nr;
             // element e of the tile: token e / nr, row e % nr
-            int i = threadIdx.x / nr, r = threadIdx.x % nr;
-            const int di = THREADS / nr, dr = THREADS % nr;
+            const int i = threadIdx.x / nr, di = THREADS / nr, dr = THREADS % nr;
+            int r = threadIdx.x % nr, to = r * pitch + i;
+            int64_t from = (int64_t)(r0 + r) * p.z.row + (int64_t)(v + i) * p.z.elem;
+            const int64_t on = (int64_t)di * p.z.elem + (int64_t)dr * p.z.row, wrap = p.z.elem - nr * p.z.row;
             auto each = [&](auto get) {
                 for (int e = threadIdx.x; e < total; e += THREADS * AHEAD) {
                     float x[AHEAD];
-                    int to[AHEAD];
+                    int at[AHEAD];
 #pragma unroll
                     for (int k = 0; k < AHEAD; ++k) {
-                        to[k] = r * pitch + i;
-                        if (e + THREADS * k < total) x[k] = get((int64_t)(r0 + r) * p.z.row + (int64_t)(v + i) * p.z.elem);
-                        i += di;
-                        r += dr;
-                        if (r >= nr) { r -= nr; ++i; }
+                        if (e + THREADS * k < total) x[k] = get(from);
+                        at[k] = to;
+                        const bool next = (r += dr) >= nr;
+                        r -= next ? nr : 0;
+                        from += on + (next ? wrap : 0);
+                        to += dr * pitch + di + (next ? 1 - nr * pitch : 0);
                     }
 #pragma unroll
                     for (int k = 0; k < AHEAD; ++k)
-                        if (e + THREADS * k < total) z[to[k]] = x[k];
+                        if (e + THREADS * k < total) z[at[k]] = x[k];
                 }
             };
             if (p.z.f16) each([&](int64_t o) { return (float)reinterpret_cast<const _Float16 *>(p.z.p)[o]; });
             else each([&](int64_t o) { return reinterpret_cast<const float *>(p.z.p)[o]; });
             __syncthreads();
-#pragma unroll
-            for (int k = 0; k < UNITS; ++k) {
-                const int unit = k * WAVES + wave;
-                if (unit >= nr * a.subs) continue;
-                const int t0 = unit / nr * STEP;
-                const float *row = z + unit % nr * pitch;
+            if (mine) {
+                const float *tokens = z + row * pitch;
                 float x[LANE];
 #pragma unroll
-                for (int e = 0; e < LANE; ++e) x[e] = t0 + 64 * e + lane < n ? row[t0 + 64 * e + lane] : -INFINITY;
-                take<LANE>(x, [&](int e) { return v + t0 + 64 * e + lane; }, v == v0, st[k], best[k], a.scale, p.top, lane, sort[wave]);
+                for (int e = 0; e < LANE; ++e) x[e] = t0 + 64 * e + lane < n ? tokens[t0 + 64 * e + lane] : -INFINITY;
+                take<LANE>(x, [&](int e) { return v + t0 + 64 * e + lane; }, v == v0, st, best, a.scale, p.top, lane, sort[wave]);
             }
             __syncthreads();
         }
-#pragma unroll
-        for (int k = 0; k < UNITS; ++k) {
-            const int unit = k * WAVES + wave;
-            if (unit >= nr * a.subs) continue;
-            const int row = r0 + unit % nr;
-            const Stats all = over_wave(st[k], a.scale);
-            if (a.splits == 1) finish(a, row, all, best[k].key, asked(p, row, lane), lane);
-            else leave(a, row, part * a.subs + unit / nr, all, best[k].key, lane);
-        }
+        if (!mine) continue;
+        st = over_wave(st, a.scale);
+        if (a.splits == 1) finish(a, r0 + row, st, best.key, asked(p, r0 + row, lane), lane);
+        else leave(a, r0 + row, part * a.subs + wave / nr, st, best.key, lane);
     }
 }
 
 // The parts of a row, joined in a fixed order: a block a row.
-__global__ void __launch_bounds__(64 * WAVES) probs_join_kernel(Args a) {
-    __shared__ Shared<WAVES> sh;
+__global__ void __launch_bounds__(64 * JOIN_WAVES) probs_join_kernel(Args a) {
+    __shared__ Shared<JOIN_WAVES> sh;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = blockIdx.x, top = a.p.top;
     Stats st{-INFINITY, 0, 0};
     Best best;
     best.clear();
-    const int per = (a.splits + WAVES - 1) / WAVES, first = min(wave * per, a.splits), count = min(per, a.splits - first);
+    const int per = (a.splits + JOIN_WAVES - 1) / JOIN_WAVES, first = min(wave * per, a.splits), count = min(per, a.splits - first);
     Asked q{-1, 0.f};
     if (wave == 0) q = asked(a.p, row, lane);
-    for (int i = threadIdx.x; i < a.splits; i += 64 * WAVES) {
+    for (int i = threadIdx.x; i < a.splits; i += 64 * JOIN_WAVES) {
         const float *s = a.stats + ((int64_t)row * a.splits + i) * 3;
         join(st, Stats{s[0], s[1], s[2]}, a.scale);
     }
@@ -503,7 +496,7 @@ hipError_t launch_probs(const Probs &p, void *workspace, hipStream_t st) {
     } else {
         hipLaunchKernelGGL(probs_row_kernel<false>, dim3(blocks), dim3(64 * ROW_WAVES), 0, st, a);
     }
-    if (pl.splits > 1) hipLaunchKernelGGL(probs_join_kernel, dim3((unsigned)p.rows), dim3(64 * WAVES), 0, st, a);
+    if (pl.splits > 1) hipLaunchKernelGGL(probs_join_kernel, dim3((unsigned)p.rows), dim3(64 * JOIN_WAVES), 0, st, a);
     return hipGetLastError();
 }
 
