@@ -125,17 +125,22 @@ __device__ __forceinline__ float root32(double ss, double inv, float eps) {
 }
 __device__ __forceinline__ double root64(double ss, double inv, float eps) { return 1.0 / sqrt(fma(ss, inv, (double)eps)); }
 
-// x <- x / sqrt(mean x^2 + eps) * w.  A thread's squares (E of them) are summed
-// in fp32, the threads' sums in fp64: the root is off by E / 2 + 2 halves of
-// 2^-23, an element by two more.
+// x <- x / sqrt(mean x^2 + eps) * w.  Up to 8 squares of a thread are summed in
+// fp32, those sums in fp64: the root is off by 8 / 2 + 2 halves of 2^-23, an
+// element by two more.
 template <int TPG, int THREADS, int E, bool VEC>
 __device__ __forceinline__ void norm(float *x, const float *w, float eps, int dim, double inv, int tid, double *part) {
     float wv[E];
     load<TPG, E, VEC>(reinterpret_cast<const char *>(w), 1, false, tid, dim, wv);
-    float s = 0;
+    double ss = 0;
 #pragma unroll
-    for (int j = 0; j < E; ++j) s = fmaf(x[j], x[j], s);
-    double ss = group_sum<TPG, THREADS>(s, part, tid);
+    for (int j0 = 0; j0 < E; j0 += 8) {
+        float s = 0;
+#pragma unroll
+        for (int j = j0; j < (E < j0 + 8 ? E : j0 + 8); ++j) s = fmaf(x[j], x[j], s);
+        ss += s;
+    }
+    ss = group_sum<TPG, THREADS>(ss, part, tid);
     if (ordinary(ss)) {
         const float r = root32(ss, inv, eps);
 #pragma unroll
@@ -151,7 +156,11 @@ __device__ __forceinline__ void norm(float *x, const float *w, float eps, int di
 }
 
 // TPG threads a group of `dim` values, E of them each, in registers from the
-// loads to the stores: every input is read once.
+// loads to the stores: every input is read once, so memory bounds it.  2048 rows
+// of 48 gated heads of 128 (126 MB): 21-22 us, 5.8 TB/s, 353 instructions a wave
+// and 80% of the issue slots.  One row of 5120: 3.4 us, a launch's and two
+// round trips' time.  17 rows side by side (4 bytes of each line a row): 11 us,
+// lines that every row's block fetches again.
 template <int TPG, int THREADS, int E, bool VEC> __global__ void __launch_bounds__(THREADS) block_norm_kernel(Args a) {
     __shared__ double part[THREADS / 64];
     const int tid = threadIdx.x % TPG;
@@ -247,12 +256,17 @@ hipError_t launch_block_norm(const BlockNorm &b, int rows, int groups, int dim, 
     const Args a{b, (uint32_t)(rows * groups), groups, dim, 1.0 / dim, y, gate, res, h, x};
     const bool vec = dim % 4 == 0 && whole4(y) && whole4(gate) && whole4(res) && whole4(h) && whole4(x) &&
                      (((uintptr_t)b.post | (uintptr_t)b.pre) & 15) == 0;
+    // Threads a group: enough loads at once in each, few waves to meet at the sums (one row of 5120
+    // with 8 / 16 values a thread: 4.5 / 4.2 us, 2048 rows 36.4 / 35.1; 2048 rows of 1024: 8.2 / 5.9;
+    // 2048 rows of 4096: 32.4 / 21.4, but of 2048 11.5 / 13.6)
     if (dim <= 64) return go<16, 256, 4>(a, vec, st);
     if (dim <= 128) return go<16, 256, 8>(a, vec, st);
     if (dim <= 256) return go<32, 256, 8>(a, vec, st);
     if (dim <= 512) return go<64, 256, 8>(a, vec, st);
+    if (dim <= 1024) return go<64, 256, 16>(a, vec, st);
     if (dim <= 2048) return go<256, 256, 8>(a, vec, st);
-    if (dim <= 8192) return go<1024, 1024, 8>(a, vec, st);
+    if (dim <= 4096) return go<256, 256, 16>(a, vec, st);
+    if (dim <= 8192) return go<512, 512, 16>(a, vec, st);
     const unsigned blocks = (unsigned)std::min<int64_t>(a.units, 1 << 20);
     auto wide = [&](auto kern, hipError_t e) {
         if (e != hipSuccess) return e;

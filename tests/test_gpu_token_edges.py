@@ -318,3 +318,45 @@ def test_logprobs_of_many_columns_and_strides():
         ref.near(host(got.entropy), ent, ee)
         assert (host(got.top_ids) == ids).all()
         ref.near(host(got.top_lp), tl, te)
+
+
+@pytest.mark.parametrize("dim", [256, 257, 512, 1023, 1024, 1025, 2049, 2560, 4096, 4097, 8192, 8193])
+@pytest.mark.parametrize("skew", [0, 1])
+def test_block_norm_lengths_where_the_threads_change(dim, skew):
+    rng = np.random.default_rng(dim)
+    y, r = (rng.standard_normal((5, 1, dim)).astype(F32) for _ in range(2))
+    y[2], y[3, :, ::2] = 1e25, 0  # (squares beyond fp32; half a row of zeros)
+    w = (1 + 0.1 * rng.standard_normal(dim)).astype(F32)
+    h, x, eh, ex = ref.block_norm(y, w, None, "none", 0.5, r, w, 1e-6)
+    lay = lambda a: dev(np.pad(a, ((0, 0), (0, 0), (skew, 0))))[:, :, skew:]  # noqa: E731  (rows off 16 bytes)
+    ho, xo = (lay(np.zeros_like(y)) for _ in range(2))
+    binding.block_norm(lay(y), dev(w), residual=lay(r), scale=0.5, pre_norm=dev(w), eps=1e-6, h_out=ho, x_out=xo)
+    torch.cuda.synchronize()
+    ref.rounded(host(ho), h, eh, F32)
+    ref.rounded(host(xo), x, ex, F32)
+
+
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 16, 17, 33])
+@pytest.mark.parametrize("vocab", [1000, 8200, 70001])
+def test_logprobs_of_rows_side_by_side_in_unequal_groups(rows, vocab):
+    rng = np.random.default_rng(rows + vocab)
+    z = (4 * rng.standard_normal((rows, vocab))).astype(F32)
+    z[:, 5:40] = z[:, 4:5]         # equals
+    z[rows // 2, 7:] = -np.inf     # fewer than are asked for
+    tok = rng.integers(-1, vocab, (rows, 70)).astype(I32)
+    for zd in (dev(z), dev(z.T.copy()).t()):
+        got = binding.logprobs(zd, dev(tok), top=12)
+        torch.cuda.synchronize()
+        m = z.max(1, keepdims=True).astype(np.float64)
+        lse = m[:, 0] + np.log(np.exp(z - m).sum(1))
+        order = np.lexsort((np.broadcast_to(np.arange(vocab), z.shape), -z), axis=1)[:, :12]
+        best = np.take_along_axis(z, order, 1)
+        ids = np.where(best > -np.inf, order, -1)
+        assert np.array_equal(host(got.top_ids), ids)
+        tol = 2.0 ** -20 * (1 + np.abs(lse) + np.abs(m[:, 0]))  # a logit, its maximum and a log, each off by a few 2^-23
+        assert np.all(np.abs(host(got.lse) - lse) <= tol)
+        want = np.where(tok >= 0, np.take_along_axis(z, np.maximum(tok, 0), 1) - lse[:, None], 0.0)
+        have = host(got.token_lp)
+        fin = np.isfinite(want)
+        assert np.array_equal(have[~fin], want[~fin])
+        assert np.all(np.abs(have - want)[fin] <= (2.0 ** -20 * (1 + np.abs(want) + np.abs(lse)[:, None] + np.abs(m)))[fin])
