@@ -20,6 +20,9 @@ constexpr int R = 16;  // rows made ready at once: 16 lanes each
 // so that only one sum over lanes lies between a state and the next one.  What
 // does not depend on the state -- normed queries and keys, k.q, gates -- is
 // made ready for R rows at once, a row to 16 lanes, and waits in LDS.
+// One token of 48 heads of 128 x 128 (6.4 MB of state read and written) is 5 us,
+// latency; 64 sequences (407 MB) 82-87 us, 4.7-4.9 TB/s: memory.  Of many rows
+// each takes 0.35 us, the chain from state to state.
 template <int DK, int CPL> __global__ void __launch_bounds__(THREADS) delta_rows_kernel(Args a) {
     constexpr int P = DK / 64;                 // pieces of 4 dimensions a lane has
     constexpr int COLS = 4 * WAVES * CPL;      // columns of a block
@@ -187,9 +190,13 @@ hipError_t launch_delta(const StateSeqs &q, const DeltaState &d, const DeltaIn &
     const Args a = make_args(q, d, in, out);
     // (of rows brought to length 1 with steps in 0..1, which keep what a tile's inverse holds in fp16's range)
     if (in_tiles(q) && in.norm && in.A) return launch_delta_chunk(a, d.hk, d.dk, workspace, st);
-    // a lane's columns: few where latency counts, more where rows are made ready for many
-    const int64_t columns = (int64_t)q.nseq * d.hv * d.dv;
-    const int cpl = d.dv % 64 == 0 && columns >= 64 * 8 * device_cus() ? 4 : columns >= 32 * 8 * device_cus() ? 2 : 1;
+    // A lane's columns: more as soon as that leaves 2 blocks a CU, since what is made ready a row then
+    // serves more of them; 4 of many rows, whose chain more waves hide, from 4 blocks on.  1 / 2 / 4
+    // columns, 48 heads of 128 x 128: 2 sequences of 1 token 6.1 / 6.0 / 6.2 us, 3 8.5 / 6.8 / 7.1,
+    // 8 14.6 / 11.0 / 9.3, 64 84 / - / 70; 2 of 17 rows 12.6 / 13.6 / 15.9, 3 18.2 / 16.5 / 19.8,
+    // 12 46.7 / 39.1 / 41.9, 16 64.7 / 51.4 / 50.6.
+    const int64_t columns = (int64_t)q.nseq * d.hv * d.dv, many = q.rows > 8 * (int64_t)q.nseq ? 4 : 2;
+    const int cpl = d.dv % 64 == 0 && columns >= 64 * many * device_cus() ? 4 : columns >= 32 * 2 * device_cus() ? 2 : 1;
     if (d.dk == 64) return cpl == 4 ? go<64, 4>(a, q.nseq, st) : cpl == 2 ? go<64, 2>(a, q.nseq, st) : go<64, 1>(a, q.nseq, st);
     return cpl == 4 ? go<128, 4>(a, q.nseq, st) : cpl == 2 ? go<128, 2>(a, q.nseq, st) : go<128, 1>(a, q.nseq, st);
 }

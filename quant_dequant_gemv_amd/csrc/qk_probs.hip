@@ -1,5 +1,11 @@
 // qk_probs.hip -- log probabilities of given tokens, entropy and the largest
 // alternatives of rows of logits.
+//
+// One pass: with a running maximum m, s = sum 2^t and w = sum t 2^t of t =
+// (z - m) scale log2 e; lse = m scale + ln s, entropy = ln 2 (log2 s - w / s).
+// 1021 fp16 rows of 131071 (268 MB): 61-66 us, 4.1-4.4 TB/s, vector
+// instructions (about 6 a logit, 70% of the issue slots) beside the loads; one
+// row of 160000: 6.0 + 5.6 us, two launches whose waves sort once each.
 #include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -12,7 +18,8 @@
 namespace qk {
 namespace probs {
 
-constexpr int ROW_WAVES = 4;       // waves of a block where a row's tokens lie side by side
+// waves of a block where a row's tokens lie side by side (2048 rows of 131071 181 us, 8 waves 212; one row 10.4, 10.8)
+constexpr int ROW_WAVES = 4;
 constexpr int WAVES = 8;           // where rows do: two blocks a CU (17 rows of 160000: 11.2 us, one of 16 waves 15.0)
 constexpr int JOIN_WAVES = 8;      // where parts are joined (160 parts of 20: 5.6 us; 4 waves 6.8, 16 waves 6.0)
 constexpr int LANE = 16;           // tokens a lane has at a time
@@ -453,7 +460,9 @@ __global__ void __launch_bounds__(64 * JOIN_WAVES) probs_join_kernel(Args a) {
     if (join_waves(st, best, a, sh, lane, wave)) finish(a, row, st, best.key, q, lane);
 }
 
-// How a call is cut: `splits` parts a row, `span` tokens to a block.
+// How a call is cut: `splits` parts a row, `span` tokens to a block.  Two blocks
+// a CU where the rows alone are fewer; else a row is one block's, and no join
+// follows.
 struct Plan { bool few; int splits, span, subs; };
 Plan plan_of(const Probs &p) {
     Plan pl{p.z.elem != 1, 1, 0, 1};

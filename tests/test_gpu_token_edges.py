@@ -359,4 +359,4 @@ def test_logprobs_of_rows_side_by_side_in_unequal_groups(rows, vocab):
         have = host(got.token_lp)
         fin = np.isfinite(want)
         assert np.array_equal(have[~fin], want[~fin])
-        assert np.all(np.abs(have - want)[fin] <= (2.0 ** -20 * (1 + np.abs(want) + np.abs(lse)[:, None] + np.abs(m)))[fin])
+        assert np.all(np.abs(have[fin] - want[fin]) <= (2.0 ** -20 * (1 + np.abs(want) + np.abs(lse)[:, None] + np.abs(m)))[fin])
