@@ -580,7 +580,7 @@ typedef struct qk_block {
  * whatever the type of h_out.  For exact n, h and x of the row: n within 2^-21
  * |n|; h within e = 2^-20 |scale n act| + 2^-23 |h|; x within 2^-21 |x| +
  * |pre_norm| e / r + 2^-20 |x| max_i(e_i) / r, r = sqrt(mean(h^2) + eps); each then rounded
- * to its type.  (Gates below -87: act is off by up to 2^-125 (1 + |gate|).)
+ * to its type.  (Gates below -87, -inf among them: act is off by up to 2^-119.)
  */
 int qk_block_norm(const qk_block *block, int rows, int groups, int dim, const qk_heads *y, const qk_heads *gate,
                   const qk_heads *residual, const qk_heads *h_out, const qk_heads *x_out, void *stream);

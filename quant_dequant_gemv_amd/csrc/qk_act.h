@@ -19,5 +19,7 @@ __device__ __forceinline__ float logistic(float z) {
     const float r = __builtin_amdgcn_rcpf(e);
     return z != z ? z : fmaf(fmaf(-e, r, 1.f), r, r);
 }
+// z below -87 as -87: what a gate of -inf or of the lowest value leaves is 0 to 2^-119.
+__device__ __forceinline__ float silu(float z) { return fmaxf(z, -87.f) * logistic(z); }
 
 }  // namespace qk

@@ -112,7 +112,7 @@ template <int TPG, int THREADS> __device__ __forceinline__ double group_sum(doub
 }
 
 __device__ __forceinline__ float gate_of(float z, int act) {
-    return act == 0 ? z : (act == 1 ? z : 1.f) * logistic(z);
+    return act == 0 ? z : act == 1 ? silu(z) : logistic(z);
 }
 
 // What brings a row of mean square m to length 1 an element: fp32 (the

@@ -127,7 +127,7 @@ template <int T, int C> __global__ void __launch_bounds__(THREADS) conv_kernel(A
                     float s = bias[e];
 #pragma unroll
                     for (int j = 0; j < T; ++j) s = fmaf(w[e][j], x[j][e], s);
-                    y[e] = a.act ? s * logistic(s) : s;
+                    y[e] = a.act ? silu(s) : s;
                 }
                 store<C>(a.y, sq.first + h0 + i, c, y);
 #pragma unroll

@@ -360,3 +360,39 @@ def test_logprobs_of_rows_side_by_side_in_unequal_groups(rows, vocab):
         fin = np.isfinite(want)
         assert np.array_equal(have[~fin], want[~fin])
         assert np.all(np.abs(have[fin] - want[fin]) <= (2.0 ** -20 * (1 + np.abs(want) + np.abs(lse)[:, None] + np.abs(m)))[fin])
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("dim", [64, 9000])
+def test_gates_of_any_size(act, dim):
+    far = np.array([-np.inf, np.finfo(F32).min, -1e30, -65504, -1000, -104, -100, -88, -87.1, -87, -86.9, -30, -1e-30, -0.0, 0, 1e-30,
+                    30, 86.9, 87, 88, 100, 65504, 1e30], F32)
+    rng = np.random.default_rng(dim)
+    y = rng.standard_normal((4, 1, dim)).astype(F32)
+    z = rng.choice(far, (4, 1, dim))
+    z[0, 0, :far.size] = far
+    w = np.ones(dim, F32)
+    with np.errstate(over="ignore", invalid="ignore"):
+        n = y / np.sqrt((y.astype(np.float64) ** 2).mean(-1, keepdims=True) + 1e-6)
+        s = 1 / (1 + np.exp(-z.astype(np.float64)))
+        a = s if act == "sigmoid" else np.where(z == -np.inf, 0, z.astype(np.float64) * s)
+    h = torch.empty(4, 1, dim, device="cuda")
+    binding.block_norm(dev(y), dev(w), dev(z), act, eps=1e-6, h_out=h)
+    torch.cuda.synchronize()
+    ref.rounded(host(h), n * a, 2.0 ** -20 * np.abs(n * a) + 2.0 ** -119 * np.abs(n), F32)  # the header's terms
+    z[1, 0, 3] = np.nan
+    binding.block_norm(dev(y), dev(w), dev(z), act, eps=1e-6, h_out=h)
+    torch.cuda.synchronize()
+    assert list(zip(*np.where(np.isnan(host(h))))) == [(1, 0, 3)]
+
+
+def test_convolution_far_below_zero():
+    C = 256
+    x = np.zeros((6, C), F32)
+    x[:, 0::4], x[:, 1::4], x[:, 2::4], x[:, 3::4] = -1e30, np.finfo(F32).min, -90, -60000
+    w = np.zeros((C, 4), F32)
+    w[:, 3] = 1
+    conv = binding.ConvState(1, dev(w))
+    y = binding.conv_silu(conv, dev(x), dev(np.zeros(1, I32)))
+    torch.cuda.synchronize()
+    assert y.dtype == torch.float32 and np.all(np.abs(host(y)) <= 2.0 ** -119)
