@@ -1027,7 +1027,10 @@ class ConvState:
     """The short causal convolution of a recurrent layer (qk_conv) and its
     state: weight float32 [channels, taps] (the current row's last), bias
     float32 [channels] or None.  pool: float32 device tensor [num_slots,
-    taps - 1, channels], oldest row first (None: allocated here, zeros)."""
+    taps - 1, channels], oldest row first (None: allocated here, zeros).
+    Tensors may be written to, not exchanged: calls have their addresses."""
+
+    pool, weight, bias = (property(lambda self, name=name: self.__dict__[name]) for name in ("pool", "weight", "bias"))
 
     def __init__(self, num_slots: int, weight, bias=None, pool=None):
         torch = _start()
@@ -1039,7 +1042,7 @@ class ConvState:
             raise QKError(QK_EINVAL_SHAPE, "ConvState")
         if pool is None:
             pool = torch.zeros((num_slots, taps - 1, C), dtype=torch.float32, device=weight.device)
-        self.pool, self.weight, self.bias = pool, weight, bias
+        self.__dict__.update(pool=pool, weight=weight, bias=bias)
         self.num_slots, self.channels, self.taps = num_slots, C, taps
         self._c = _CONV(_float_arg(pool, "pool", (num_slots, taps - 1, C)), num_slots, C, taps, weight.data_ptr(),
                         _float_arg(bias, "bias", (C,)))
@@ -1048,7 +1051,9 @@ class ConvState:
 class DeltaState:
     """The state of a gated delta recurrence (qk_delta): pool, a float32 device
     tensor [num_slots, v_heads, value_dim, key_dim] (None: allocated here,
-    zeros)."""
+    zeros), that may be written to, not exchanged: calls have its address."""
+
+    pool = property(lambda self: self.__dict__["pool"])
 
     def __init__(self, num_slots: int, k_heads: int, v_heads: int, key_dim: int = 128, value_dim: int = 128, device="cuda",
                  pool=None):
@@ -1060,7 +1065,7 @@ class DeltaState:
             raise QKError(QK_EINVAL_SHAPE, "DeltaState")
         if pool is None:
             pool = torch.zeros(shape, dtype=torch.float32, device=device)
-        self.pool = pool
+        self.__dict__["pool"] = pool
         self.num_slots, self.k_heads, self.v_heads, self.key_dim, self.value_dim = num_slots, k_heads, v_heads, key_dim, value_dim
         self._c = _DELTA(_float_arg(pool, "pool", shape), num_slots, k_heads, v_heads, key_dim, value_dim)
 

@@ -251,3 +251,14 @@ def test_struct_layouts_match_the_header():
         fields = [re.sub(r"^(float|int|void|char) ", "", f).strip(" *") for f in fields]
         assert fields == [f for f, _ in getattr(b, name)._fields_], name
         assert ctypes.sizeof(getattr(b, name)) == size, name
+
+
+def test_states_keep_their_tensors():
+    c = b.ConvState(3, z(64, 4), z(64))
+    d = b.DeltaState(3, 1, 2, 64, 64, pool=z(3, 2, 64, 64))
+    for o, name in ((c, "pool"), (c, "weight"), (c, "bias"), (d, "pool")):
+        t = getattr(o, name)
+        with pytest.raises(AttributeError):
+            setattr(o, name, t.clone())
+        assert getattr(o, name) is t
+        t.fill_(1)
