@@ -159,8 +159,8 @@ __device__ __forceinline__ void norm(float *x, const float *w, float eps, int di
 // loads to the stores: every input is read once, so memory bounds it.  2048 rows
 // of 48 gated heads of 128 (126 MB): 21-22 us, 5.8 TB/s, 335 instructions a wave
 // and 76% of the issue slots.  One row of 5120: 3.4 us, a launch's and two
-// round trips' time.  17 rows side by side (4 bytes of each line a row): 11 us,
-// lines that every row's block fetches again.
+// round trips' time.  17 rows side by side (4 bytes of each line a row): 10-11 us,
+// 20480 accesses a row that each take a line, one a cycle and CU.
 template <int TPG, int THREADS, int E, bool VEC> __global__ void __launch_bounds__(THREADS) block_norm_kernel(Args a) {
     __shared__ double part[THREADS / 64];
     const int tid = threadIdx.x % TPG;
