@@ -130,7 +130,7 @@ __device__ __forceinline__ uint64_t lane_key(uint64_t k, int lane) {
 // after the first batch few are looked at one by one.
 struct Best {
     uint64_t key, thr;
-    float low;  // value of thr: a later token (of a higher index) has to be above it
+    float low;  // value of thr before the batch under way: a token of it has to be above
     __device__ __forceinline__ void clear() { key = thr = 0; low = -INFINITY; }
     __device__ __forceinline__ void limit(int top) {
         thr = lane_key(key, top - 1);
@@ -244,8 +244,10 @@ __device__ __forceinline__ void finish(const Args &a, int row, const Stats &st, 
     }
 }
 
-// N tokens a lane more (-inf: none), at(e) the e-th one's number; those of a
-// wave come in rising batches.  fresh: the first batch.
+// N tokens a lane more (-inf: none), at(e) the e-th one's number.  Those of a
+// wave come in rising batches, so an equal of the last one kept is no better in
+// a later batch and `low` rejects it by value; inside a batch tokens rise with
+// neither e nor the lane, and their keys decide.  fresh: the first batch.
 template <int N, typename F>
 __device__ __forceinline__ void take(const float *z, F at, bool fresh, Stats &st, Best &best, float scale, int top, int lane, uint64_t *lds) {
     float most = z[0];
@@ -258,10 +260,8 @@ __device__ __forceinline__ void take(const float *z, F at, bool fresh, Stats &st
     } else if (__ballot(most > best.low)) {
 #pragma unroll
         for (int e = 0; e < N; ++e)
-            if (__ballot(z[e] > best.low)) {
-                best.offer(z[e] > best.low ? key_of(z[e], at(e)) : 0, top, lane);
-                best.low = best.thr ? key_value(best.thr) : -INFINITY;
-            }
+            if (__ballot(z[e] > best.low)) best.offer(z[e] > best.low ? key_of(z[e], at(e)) : 0, top, lane);
+        best.limit(top);
     }
 }
 
