@@ -723,10 +723,12 @@ typedef struct qk_probs {
  * logits (-0 and 0 are) go by the lower index.  A token outside 0..vocab-1 is
  * none: 0.  A row with no token left: lse -inf, entropy 0.  A NaN or +inf in
  * a row makes its lse, entropy and log probabilities NaN (NaN is no
- * alternative).  Sums are fp32 over terms 2^x of the distance to the row's
- * largest logit m: log probabilities within 2^-20 (1 + scale |z - m|), the
- * entropy within 2^-18 (1 + log vocab), lse within 2^-20 + 2^-23 scale |m|
- * of the exact values for logits below 2^125 / scale.
+ * alternative).  Terms are fp32 powers 2^x of the distance to a row's largest
+ * logit m, their sums compensated, so that nothing grows with the count of
+ * them: log probabilities within 2^-20 (1 + scale |z - m|) + 2^-21 log vocab,
+ * lse within 2^-20 + 2^-21 log vocab + 2^-23 scale |m|, the entropy within 2^-18
+ * (1 + log vocab) of the exact values for logits below 2^125 / scale.  No log
+ * probability is above 0.
  */
 int64_t qk_logprobs_workspace_bytes(const qk_heads *logits, int rows, int64_t vocab, int top);
 int qk_logprobs(const qk_heads *logits, int rows, int64_t vocab, float scale, const qk_probs *probs, void *workspace,

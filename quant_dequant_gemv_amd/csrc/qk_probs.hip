@@ -3,7 +3,7 @@
 //
 // One pass: with a running maximum m, s = sum 2^t and w = sum t 2^t of t =
 // (z - m) scale log2 e; lse = m scale + ln s, entropy = ln 2 (log2 s - w / s).
-// 1021 fp16 rows of 131071 (268 MB): 61-66 us, 4.1-4.4 TB/s, vector
+// 1021 fp16 rows of 131071 (268 MB): 63-66 us, 4.1-4.2 TB/s, vector
 // instructions (about 6 a logit, 70% of the issue slots) beside the loads; one
 // row of 160000: 6.0 + 5.6 us, two launches whose waves sort once each.
 #include <float.h>
@@ -25,7 +25,8 @@ constexpr int JOIN_WAVES = 8;      // where parts are joined (160 parts of 20: 5
 constexpr int LANE = 16;           // tokens a lane has at a time
 constexpr int STEP = 64 * LANE;    // and a wave
 constexpr int FEW = WAVES;         // rows that lie side by side (elem > 1) a block has at most, a wave a row or more
-constexpr float LN2 = 0.693147180559945f;
+constexpr float LN2 = 0.693147180559945f, LN2_HI = 0x1.62e4p-1f, LN2_LO = 0x1.7f7d1cp-20f;  // (HI: 15 bits)
+constexpr float SLACK = 4.f;  // in units of log 2
 constexpr float LOW = -1e4f;  // 2^LOW is 0: terms below say nothing, and never as inf * 0
 
 // One token as a number whose order is that of the logits, the lower index
@@ -49,7 +50,10 @@ __device__ __forceinline__ float of_order(int o) { return __builtin_bit_cast(flo
 
 // Statistics of a softmax under way, t = (z - m) * scale in units of log 2:
 // the maximum, sum 2^t, sum t 2^t.
-struct Stats { float m, s, w; };
+struct Stats {
+    float m;
+    double s, w;
+};
 
 // LDS between the lanes of one wave: its accesses stay in program order, the
 // compiler is told not to move them.
@@ -63,8 +67,9 @@ __device__ __forceinline__ void wave_sync() {
 __device__ __forceinline__ float step(float z, float m, float scale) { return (z - (m == -INFINITY ? 0.f : m)) * scale; }
 // The sums as they are with maximum m >= a.m.
 __device__ __forceinline__ void raise(Stats &a, float m, float scale) {
-    const float d = step(a.m, m, scale), f = __builtin_amdgcn_exp2f(d);
-    a.w = f * fmaf(fmaxf(d, LOW), a.s, a.w);
+    const float d = step(a.m, m, scale);
+    const double f = __builtin_amdgcn_exp2f(d);
+    a.w = f * fma((double)fmaxf(d, LOW), a.s, a.w);
     a.s *= f;
     a.m = m;
 }
@@ -75,17 +80,47 @@ __device__ __forceinline__ void join(Stats &a, Stats b, float scale) {
     a.s += b.s;
     a.w += b.w;
 }
-// N terms more, the largest of them `top`.
-template <int N> __device__ __forceinline__ void add(Stats &a, const float *z, float top, float scale) {
-    raise(a, fmaxf(a.m, top), scale);
-    const float m = a.m == -INFINITY ? 0.f : a.m;
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-        const float t = (z[e] - m) * scale, p = __builtin_amdgcn_exp2f(t);
-        a.s += p;
-        a.w = fmaf(p, fmaxf(t, LOW), a.w);
+
+// The same of one lane's terms.  Many equal terms round the same way each time,
+// and a lane has up to vocab / 64 of them, so its sums are s - ds and w - dw, what
+// an addition loses being taken from the next one (plain fp32 sums of 2^20 such
+// logits were off by 6e-5; in fp64 600 fp32 rows of 131072 took 78 us for 67).
+// m is up to SLACK below the largest logit: each change of it costs a rounded
+// power of 2, and maxima that rise all along a row would cost one a batch.
+struct Lane {
+    float m, most, s, ds, w, dw;
+    __device__ __forceinline__ void clear() {
+        m = -FLT_MAX;  // (finite: what a row of -inf is compared with)
+        most = -INFINITY;
+        s = ds = w = dw = 0.f;
     }
-}
+    // N terms more, the largest of them `top`, summed by themselves first.
+    template <int N> __device__ __forceinline__ void add(const float *z, float top, float scale) {
+        most = fmaxf(most, top);
+        const float rise = (most - m) * scale;  // (NaN: of two infinities)
+        const bool up = rise > SLACK;           // (no branch: 1021 fp16 rows of 131071 70 us with one, 66 without)
+        const float d = up ? fmaxf(-rise, LOW) : 0.f, f = __builtin_amdgcn_exp2f(d);
+        m = up ? most : m;
+        constexpr int C = N < 2 ? N : 2;
+        float p[C], q[C];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float t = (z[e] - m) * scale, x = __builtin_amdgcn_exp2f(t), y = fmaxf(t, LOW);
+            p[e % C] = e < C ? x : p[e % C] + x;
+            q[e % C] = e < C ? x * y : fmaf(x, y, q[e % C]);
+        }
+        w = fmaf(d, s, w);
+        plus(s, ds, f, C == 2 ? p[0] + p[1] : p[0]);
+        plus(w, dw, f, C == 2 ? q[0] + q[1] : q[0]);
+    }
+    // sum <- f sum + x
+    static __device__ __forceinline__ void plus(float &sum, float &over, float f, float x) {
+        const float y = fmaf(-f, over, x), t = fmaf(f, sum, y);
+        over = fmaf(-f, sum, t) - y;
+        sum = t;
+    }
+};
+
 // Over the 64 lanes, by DPP inside rows of 16 (no LDS): every lane gets it.
 template <int CTRL> __device__ __forceinline__ float dpp(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
@@ -112,11 +147,29 @@ __device__ __forceinline__ int over_lanes_max(int v) {
 __device__ __forceinline__ float wave_max(float v) {
     return over_lanes(v, [](float a, float b) { return fmaxf(a, b); });
 }
-__device__ __forceinline__ float wave_sum(float v) {
-    return over_lanes(v, [](float a, float b) { return a + b; });
+template <int CTRL> __device__ __forceinline__ double dpp(double v) {
+    const uint2 w = __builtin_bit_cast(uint2, v);
+    return __builtin_bit_cast(double, make_uint2(__builtin_amdgcn_update_dpp(0, (int)w.x, CTRL, 0xf, 0xf, true),
+                                                 __builtin_amdgcn_update_dpp(0, (int)w.y, CTRL, 0xf, 0xf, true)));
+}
+__device__ __forceinline__ double lane_of(double v, int lane) {
+    const uint2 w = __builtin_bit_cast(uint2, v);
+    return __builtin_bit_cast(double, make_uint2(__builtin_amdgcn_readlane((int)w.x, lane), __builtin_amdgcn_readlane((int)w.y, lane)));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    v += dpp<0xB1>(v);
+    v += dpp<0x4E>(v);
+    v += dpp<0x141>(v);
+    v += dpp<0x140>(v);
+    return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
 }
 __device__ __forceinline__ Stats over_wave(Stats a, float scale) {
     raise(a, wave_max(a.m), scale);
+    return Stats{a.m, wave_sum(a.s), wave_sum(a.w)};
+}
+__device__ __forceinline__ Stats over_wave(const Lane &l, float scale) {
+    Stats a{l.m, (double)l.s - l.ds, (double)l.w - l.dw};
+    raise(a, wave_max(l.most), scale);
     return Stats{a.m, wave_sum(a.s), wave_sum(a.w)};
 }
 
@@ -222,16 +275,28 @@ __device__ __forceinline__ Asked asked(const Probs &p, int row, int i) {
     return q;
 }
 
+// log s: the exponent's part exactly (a sum of one term is 0), the rest within 2^-23.
+__device__ __forceinline__ float log_of(double s) {
+    float f = (float)__builtin_amdgcn_frexp_mant(s);
+    int e = __builtin_amdgcn_frexp_exp(s);
+    if (f < 0.70710678f) {
+        f *= 2.f;
+        --e;
+    }
+    return fmaf((float)e, LN2_HI, fmaf((float)e, LN2_LO, __builtin_amdgcn_logf(f) * LN2));  // (base 2)
+}
+
 // A row's results, from its statistics (every lane), its sorted keys and the
 // first 64 asked tokens, one a lane.
 __device__ __forceinline__ void finish(const Args &a, int row, const Stats &st, uint64_t key, Asked q, int lane) {
     const Probs &p = a.p;
-    const bool none = st.m == -INFINITY && st.s == 0.f;  // every token masked
-    const float l2 = __builtin_amdgcn_logf(st.s), ln = l2 * LN2;  // (base 2)
+    const bool none = st.m == -INFINITY && st.s == 0;  // every token masked
+    const float ln = log_of(st.s < 1 ? 1 : st.s);  // (the largest logit's own term is 1: no log probability is above 0)
     auto lp = [&](float z) { return z == -INFINITY ? (st.s == st.s ? -INFINITY : NAN) : fmaf(z - st.m, p.scale, -ln); };
     if (lane == 0) {
         if (p.lse) p.lse[row] = none ? -INFINITY : fmaf(st.m, p.scale, ln);
-        if (p.entropy) p.entropy[row] = none ? 0.f : (l2 - st.w / st.s) * LN2;
+        const float h = fmaf(-(float)st.w / (float)st.s, LN2, ln);
+        if (p.entropy) p.entropy[row] = none || h < 0.f ? 0.f : h;
     }
     for (int i = lane; i < p.ntok; i += 64) {
         if (i != lane) q = asked(p, row, i);
@@ -249,11 +314,11 @@ __device__ __forceinline__ void finish(const Args &a, int row, const Stats &st, 
 // a later batch and `low` rejects it by value; inside a batch tokens rise with
 // neither e nor the lane, and their keys decide.  fresh: the first batch.
 template <int N, typename F>
-__device__ __forceinline__ void take(const float *z, F at, bool fresh, Stats &st, Best &best, float scale, int top, int lane, uint64_t *lds) {
+__device__ __forceinline__ void take(const float *z, F at, bool fresh, Lane &st, Best &best, float scale, int top, int lane, uint64_t *lds) {
     float most = z[0];
 #pragma unroll
     for (int e = 1; e < N; ++e) most = fmaxf(most, z[e]);
-    add<N>(st, z, most, scale);
+    st.add<N>(z, most, scale);
     if (!top) return;
     if (fresh) {
         best.first<N>([&](int e) { return z[e]; }, at, most, top, lane, lds);
@@ -295,7 +360,6 @@ template <int W> struct Shared {
 template <int W>
 __device__ __forceinline__ bool join_waves(Stats &st, Best &best, const Args &a, Shared<W> &sh, int lane, int wave) {
     const int top = a.p.top;
-    st = over_wave(st, a.scale);
     if (lane == 0) sh.part[wave] = st;
     if (lane < top) sh.keys[wave * top + lane] = best.key;
     __syncthreads();
@@ -309,7 +373,7 @@ __device__ __forceinline__ void leave(const Args &a, int row, int part, const St
     const int64_t cell = (int64_t)row * a.splits + part;
     if (lane == 0) {
         float *o = a.stats + cell * 3;
-        o[0] = st.m; o[1] = st.s; o[2] = st.w;
+        o[0] = st.m; o[1] = (float)st.s; o[2] = (float)st.w;
     }
     if (lane < a.p.top) a.keys[cell * a.p.top + lane] = key;
 }
@@ -332,7 +396,8 @@ template <bool F16> __global__ void __launch_bounds__(64 * ROW_WAVES) probs_row_
         const T *z = reinterpret_cast<const T *>(p.z.p) + (int64_t)row * p.z.row;
         Asked q{-1, 0.f};
         if (a.splits == 1 && wave == 0) q = asked(p, row, lane);
-        Stats st{-INFINITY, 0, 0};
+        Lane sums;
+        sums.clear();
         Best best;
         best.clear();
         // whole pieces of 16 bytes, and what is left before and behind them (wave 0 and the last one, at the end)
@@ -355,7 +420,7 @@ template <bool F16> __global__ void __launch_bounds__(64 * ROW_WAVES) probs_row_
 #pragma unroll
                 for (int e = 0; e < LANE; ++e) x[e] = i + 64 * (e / N) + lane < pieces ? x[e] : -INFINITY;
             }
-            take<LANE>(x, [&](int e) { return head + (i + 64 * (e / N) + lane) * N + e % N; }, fresh, st, best, a.scale, p.top, lane,
+            take<LANE>(x, [&](int e) { return head + (i + 64 * (e / N) + lane) * N + e % N; }, fresh, sums, best, a.scale, p.top, lane,
                        sh.sort[wave]);
             fresh = false;
 #pragma unroll
@@ -364,13 +429,14 @@ template <bool F16> __global__ void __launch_bounds__(64 * ROW_WAVES) probs_row_
         auto rest = [&](int from, int to) {
             if (from >= to) return;
             const float x = from + lane < to ? (float)z[from + lane] : -INFINITY;
-            add<1>(st, &x, x, a.scale);
+            sums.add<1>(&x, x, a.scale);
             if (p.top) best.offer(x > -INFINITY ? key_of(x, from + lane) : 0, p.top, lane);
         };
         if (wave == 0) rest(v0, head);
         if (wave == ROW_WAVES - 1) rest(tail, v1);
+        Stats st = over_wave(sums, a.scale);
         if (a.splits > 1) {
-            leave(a, row, part * ROW_WAVES + wave, over_wave(st, a.scale), best.key, lane);
+            leave(a, row, part * ROW_WAVES + wave, st, best.key, lane);
             continue;
         }
         if (join_waves(st, best, a, sh, lane, wave)) finish(a, row, st, best.key, q, lane);
@@ -394,7 +460,8 @@ __global__ void __launch_bounds__(64 * WAVES) probs_few_kernel(Args a) {
         const int v0 = part * a.span, v1 = min(v0 + a.span, p.vocab);
         const bool mine = wave < nr * a.subs;
         const int row = wave % nr, t0 = wave / nr * STEP;
-        Stats st{-INFINITY, 0, 0};
+        Lane sums;
+        sums.clear();
         Best best;
         best.clear();
         for (int v = v0; v < v1; v += tile) {
@@ -426,16 +493,17 @@ __global__ void __launch_bounds__(64 * WAVES) probs_few_kernel(Args a) {
             else each([&](int64_t o) { return reinterpret_cast<const float *>(p.z.p)[o]; });
             __syncthreads();
             if (mine) {
-                const float *tokens = z + row * pitch;
+                const float *tokens = z + row * pitch + t0;
+                const int left = n - t0;  // (scalars beside the lane: 12 registers less, two blocks a CU)
                 float x[LANE];
 #pragma unroll
-                for (int e = 0; e < LANE; ++e) x[e] = t0 + 64 * e + lane < n ? tokens[t0 + 64 * e + lane] : -INFINITY;
-                take<LANE>(x, [&](int e) { return v + t0 + 64 * e + lane; }, v == v0, st, best, a.scale, p.top, lane, sort[wave]);
+                for (int e = 0; e < LANE; ++e) x[e] = lane < left - 64 * e ? tokens[64 * e + lane] : -INFINITY;
+                take<LANE>(x, [&](int e) { return v + t0 + 64 * e + lane; }, v == v0, sums, best, a.scale, p.top, lane, sort[wave]);
             }
             __syncthreads();
         }
         if (!mine) continue;
-        st = over_wave(st, a.scale);
+        const Stats st = over_wave(sums, a.scale);
         if (a.splits == 1) finish(a, r0 + row, st, best.key, asked(p, r0 + row, lane), lane);
         else leave(a, r0 + row, part * a.subs + wave / nr, st, best.key, lane);
     }
@@ -457,6 +525,7 @@ __global__ void __launch_bounds__(64 * JOIN_WAVES) probs_join_kernel(Args a) {
         join(st, Stats{s[0], s[1], s[2]}, a.scale);
     }
     if (top) gather(a.keys + ((int64_t)row * a.splits + first) * top, count * top, best, top, lane, sh.sort[wave]);
+    st = over_wave(st, a.scale);
     if (join_waves(st, best, a, sh, lane, wave)) finish(a, row, st, best.key, q, lane);
 }
 

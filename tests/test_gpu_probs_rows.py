@@ -1,5 +1,5 @@
 """GPU: log probabilities of rows of many batches a wave -- equal logits at any
-place of a batch."""
+place of a batch, and sums of flat rows."""
 import numpy as np
 import pytest
 
@@ -51,3 +51,55 @@ def test_equal_logits_go_by_the_lower_index(kind, layout, dt, rows, vocab):
         torch.cuda.synchronize()
         assert np.array_equal(host(got.top_ids), ids[:, :top])
         assert np.array_equal(host(few.top_ids)[0], ids[rows // 2, :top])
+
+
+# ------------------------------------------------------------------ sums
+
+def flat(kind, V):
+    """A row of float32 whose terms repeat, so that roundings of a sum add up where it has few bits."""
+    rng = np.random.default_rng(V)
+    if kind == "two":
+        return np.where(rng.random(V) < 0.5, 0, -0.3).astype(F32)
+    if kind == "one above":
+        z = np.full(V, 2.0, F32)
+        z[V // 3] = 2.37
+        return z
+    if kind == "some above":
+        z = np.full(V, -1.7, F32)
+        z[rng.permutation(V)[:4096]] = 1.1
+        return z
+    if kind == "rising":  # ever a new maximum
+        return np.linspace(-9, 3, V).astype(F32)
+    return np.linspace(3, -9, V).astype(F32)
+
+
+@pytest.mark.parametrize("V", [131072, 262144, 1 << 20, 300001])
+@pytest.mark.parametrize("side_by_side", [False, True])
+@pytest.mark.parametrize("kind", ["two", "one above", "some above", "rising", "falling"])
+def test_sums_of_flat_rows(kind, side_by_side, V):
+    """In units u = 2^-24 of a sum, for rows of one kind of term: a term 2 (its power) and 3.5 of its distance (difference,
+    scale, product), 16 of them summed in two halves 8, what follows compensated or in fp64 but for a power of 2 u where a
+    maximum rises -- over lanes, waves and, a row in parts, again over lanes and waves, whose sums are stored in 1: 19 of 24
+    in all, and 24 more where maxima rise as a lane goes, by 4 log 2 or more each (3 each, and 3.5 of the 4 log 2 that a
+    lane's maximum is behind).  The logarithm 2 and one of its value; the result one."""
+    z = flat(kind, V)
+    for scale in (1.0, 0.7):
+        t = (z.astype(np.float64) - float(z.max())) * float(F32(scale))
+        p = np.exp(t)
+        s = p.sum()
+        lse = float(z.max()) * float(F32(scale)) + np.log(s)
+        dist = -(p * t).sum() / s
+        ent = np.log(s) + dist
+        err = 2.0 ** -24 * (26 + 24 * (kind == "rising") + 3.5 * dist + np.log(s) + abs(lse) + abs(float(z.max())) * scale)
+        zd = dev(np.repeat(z, 2))[::2] if side_by_side else dev(z)
+        at = np.array([0, V // 3, V - 1])
+        for rows in (1, 600, 4200):  # a row in parts, a block's, a wave's
+            tok = torch.from_numpy(np.tile(at.astype(np.int32), (rows, 1))).cuda()
+            got = binding.logprobs(zd.expand(rows, V), tok, scale=scale)
+            torch.cuda.synchronize()
+            assert np.abs(host(got.lse) - lse).max() <= err
+            # (a token's own distance: difference, scale, sum)
+            assert (np.abs(host(got.token_lp) - (t[at] - np.log(s))) <= err - 4.0 * 2.0 ** -24 * t[at]).all()
+            assert np.abs(host(got.entropy) - ent).max() <= 2.0 ** -18 * (1 + np.log(V))
+            assert (host(got.lse) == host(got.lse)[0]).all()
+            assert (host(got.token_lp) <= 0).all() and (host(got.entropy) >= 0).all()
