@@ -685,9 +685,11 @@ typedef struct qk_delta_rows {
  * + 2^-18 |S_tj|) and its rounding; where 64 rows are worked on together, both also
  * within 2^-25 of the largest |v_j| and 24 |S_j| among the last 64 rows, however
  * small the decays have made them.  Sums of squares of rows of q and k must be
- * below 2^126, values and states below 2^110.  A non-finite value of a row makes
- * the rows of its head and sequence, from up to 63 rows before it on, and their
- * state undefined, and touches no other sequence or head.
+ * below 2^126, values and states below 2^110; with norm 1 rows may be as short
+ * as fp32 has them, and a row of zeros is zeros, with eps 0 too.  A non-finite
+ * value of a row makes the rows of its head and sequence, from up to 63 rows
+ * before it on, and their state undefined, and touches no other sequence or
+ * head.
  */
 int64_t qk_delta_workspace_bytes(const qk_delta *delta, const qk_state_seqs *seqs);
 int qk_delta_rule(const qk_delta *delta, const qk_state_seqs *seqs, const qk_delta_rows *in, const qk_heads *out,

@@ -78,6 +78,22 @@ __device__ __forceinline__ void load_pieces(bool vec, const Heads &x, int64_t t,
     }
 }
 
+// Rows whose sum of squares is below SHORT: fp32 has lost bits of smaller
+// squares, and of products with a row of the other kind.  Their elements are
+// made larger by a power of two first.
+constexpr float SHORT = 0x1p-80f;
+template <int P> __device__ __forceinline__ float enlarge(float (*x)[4], float up) {
+    float xx = 0;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[p][e] *= up;
+            xx = fmaf(x[p][e], x[p][e], xx);
+        }
+    return xx;
+}
+
 // Log decay (never above 0) and step of a row's head.  Raw gates: g = A log(1 +
 // e^(alpha + dt)), without overflow on either side; beta through the logistic
 // function.

@@ -13,6 +13,17 @@ constexpr int WAVES = 4;
 constexpr int THREADS = 64 * WAVES;
 constexpr int R = 16;  // rows made ready at once: 16 lanes each
 
+// A short row over 16 lanes, enlarged, and the factor that brings it to length 1
+// (rows of zeros stay zeros without an eps too).
+template <int P> __device__ __forceinline__ float to_length_1(float (*x)[4], float xx, float eps) {
+    if (eps >= 0x1p-74f) {  // (with 2^100 below it would leave fp32)
+        enlarge<P>(x, 0x1p60f);
+        return rsqrtf(xx + eps) * 0x1p-60f;
+    }
+    const float s = sum16(enlarge<P>(x, 0x1p100f)) + eps * 0x1p100f * 0x1p100f;
+    return s > 0.f ? rsqrtf(s) : 0.f;
+}
+
 // The state of a head is held as S[Dv][Dk]: a column (one value dimension) is
 // 16 lanes with DK / 16 values each, a lane has CPL columns.  With the old
 // state S, a row is
@@ -69,7 +80,18 @@ template <int DK, int CPL> __global__ void __launch_bounds__(THREADS) delta_rows
                     kq = fmaf(k[p][x], q[p][x], kq);
                 }
             qq = sum16(qq); kk = sum16(kk); kq = sum16(kq);
-            const float rq = a.norm ? a.scale * rsqrtf(qq + a.eps) : a.scale, rk = a.norm ? rsqrtf(kk + a.eps) : 1.f;
+            float rq = a.norm ? a.scale * rsqrtf(qq + a.eps) : a.scale, rk = a.norm ? rsqrtf(kk + a.eps) : 1.f;
+            float both = kq * rq * rk;
+            if (a.norm && (qq < SHORT || kk < SHORT)) {  // (alike for the row's 16 lanes)
+                if (qq < SHORT) rq = a.scale * to_length_1<P>(q, qq, a.eps);
+                if (kk < SHORT) rk = to_length_1<P>(k, kk, a.eps);
+                kq = 0;
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) kq = fmaf(k[p][x], q[p][x], kq);
+                both = sum16(kq) * (rq * rk);
+            }
             const Gate g = gates(a, h, al, be);
 #pragma unroll
             for (int p = 0; p < P; ++p) {
@@ -78,7 +100,7 @@ template <int DK, int CPL> __global__ void __launch_bounds__(THREADS) delta_rows
             }
 #pragma unroll
             for (int c = 0; c < COLS / 16; ++c) v_s[r][l + 16 * c] = v[c];
-            if (l == 0) g_s[r] = make_float4(expf(g.g), g.b, kq * rq * rk, 0);
+            if (l == 0) g_s[r] = make_float4(expf(g.g), g.b, both, 0);
         }
         __syncthreads();
         // with one column a lane a row's numbers come from LDS while the row before is worked on

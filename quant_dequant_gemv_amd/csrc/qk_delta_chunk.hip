@@ -209,12 +209,19 @@ template <int DK> __global__ void __launch_bounds__(TILE_THREADS) delta_tile_ker
             }
         qq += dpp<0xB1>(qq); kk += dpp<0xB1>(kk);
         qq += dpp<0x4E>(qq); kk += dpp<0x4E>(kk);
+        // a row's length over the root that it is divided by, its square as it is or 2^200 of it
+        auto length = [&](float (*x)[4], float &xx) {
+            if (!(xx < SHORT)) return xx * rsqrtf(xx) * rsqrtf(xx + a.eps);  // (NaN too)
+            xx = enlarge<Q4>(x, 0x1p100f);
+            xx += dpp<0xB1>(xx);
+            xx += dpp<0x4E>(xx);
+            return xx > 0.f ? (float)sqrt(xx / (xx + a.eps * 0x1p200)) : 0.f;
+        };
+        const float len_k = length(k, kk), len_q = length(q, qq);
         const float rq = qq > 0.f ? rsqrtf(qq) : 0.f, rk = kk > 0.f ? rsqrtf(kk) : 0.f;
         if (l == 0) {
-            c_s[r] = kk * rk * rsqrtf(kk + a.eps);
-            e_s[r] = qq * rq * rsqrtf(qq + a.eps);
-            if (!(kk > 0.f)) c_s[r] = kk;  // (0, or NaN)
-            if (!(qq > 0.f)) e_s[r] = qq;
+            c_s[r] = len_k;
+            e_s[r] = len_q;
         }
 #pragma unroll
         for (int p = 0; p < Q4; ++p) {
