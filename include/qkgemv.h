@@ -675,8 +675,8 @@ typedef struct qk_delta_rows {
  *          writes; or NULL: the state alone
  *   nseq x v_heads x value_dim is at most 2^27
  *   workspace  qk_delta_workspace_bytes bytes (16-byte aligned; NULL when that is
- *          0), for this call until it has run: calls that may overlap, captured
- *          ones among them, need workspaces of their own
+ *          0, and with norm 0 or without A), for this call until it has run: calls
+ *          that may overlap, captured ones among them, need workspaces of their own
  * States, sums and decays are fp32.  Sequences of many rows with norm 1 and
  * raw gates go 64 rows at a time through the matrix instructions, every factor
  * a sum of two fp16 values.  Accuracy, for exact S, u, a in 0..1, b in 0..1 and

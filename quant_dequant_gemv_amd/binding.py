@@ -1108,8 +1108,9 @@ def delta_rule(state: DeltaState, q, k, v, alpha, beta, slots, slots_out=None, q
     outputs, None: key_dim ** -0.5.  Sequences as in conv_silu.  Returns out,
     float32 [rows, v heads, value_dim] unless given, None with state_only.
     workspace: uint8 device tensor of at least qk_delta_workspace_bytes bytes
-    (None: allocated for the call).  Rows of no sequence are left as they were:
-    undefined in an out that is allocated here."""
+    (None: allocated for the call where it takes one, which it does not
+    without norm or A).  Rows of no sequence are left as they were: undefined
+    in an out that is allocated here."""
     hk, hv, dk = state.k_heads, state.v_heads, state.key_dim
     try:
         rows = q.shape[0]
@@ -1134,7 +1135,8 @@ def delta_rule(state: DeltaState, q, k, v, alpha, beta, slots, slots_out=None, q
     if out is None and not state_only:
         out = q.new_empty(vshape, dtype=_torch.float32)
     lib = _packed_calls()
-    ws, need, keep = _workspace(workspace, lib.qk_delta_workspace_bytes(state._c, seqs) if workspace is None else 0, q)
+    tiles = workspace is None and norm and A is not None
+    ws, need, keep = _workspace(workspace, lib.qk_delta_workspace_bytes(state._c, seqs) if tiles else 0, q)
     rc = lib.qk_delta_rule(state._c, seqs, ins, None if out is None else _view_arg(out, "out", vshape), ws, need, _current(dev))
     if rc != QK_OK:
         raise QKError(rc, "qk_delta_rule")

@@ -610,7 +610,7 @@ int qk_conv_silu(const qk_conv *c, const qk_state_seqs *seqs, int act, const qk_
 
 int64_t qk_delta_workspace_bytes(const qk_delta *delta, const qk_state_seqs *seqs) {
     if (check_delta(delta, seqs)) return -1;
-    return seqs->rows ? qk::delta_workspace(to_state_seqs(seqs, delta->num_slots), to_delta(delta)) : 0;
+    return seqs->rows ? qk::delta_workspace(to_state_seqs(seqs, delta->num_slots), to_delta(delta), true, true) : 0;
 }
 
 int qk_delta_rule(const qk_delta *d, const qk_state_seqs *seqs, const qk_delta_rows *r, const qk_heads *out,
@@ -638,7 +638,7 @@ int qk_delta_rule(const qk_delta *d, const qk_state_seqs *seqs, const qk_delta_r
         return rc;
     if (out && (rc = check_heads(out, rows, hv, d->value_dim, true, &so))) return rc;
     const qk::StateSeqs sq = to_state_seqs(seqs, d->num_slots);
-    const int64_t need = qk::delta_workspace(sq, to_delta(d));
+    const int64_t need = qk::delta_workspace(sq, to_delta(d), r->norm, r->A);
     if (workspace_bytes < need) return QK_EINVAL_SHAPE;
     if (need && (!workspace || !aligned(workspace, 16))) return QK_EINVAL_PTR;
     const Span ws{need ? workspace : nullptr, need};

@@ -202,16 +202,19 @@ template <int DK, int CPL> hipError_t go(const Args &a, int nseq, hipStream_t st
 // 128 47 / 37, of 256 91 / 44; 8 of 64 95 / 74; 32 of 64 248 / 270, of 128 479 /
 // 383).  Where lengths differ they may be all in one sequence, which takes
 // 0.35 us a row one by one, while tiles lose less than half at 32 rows each.
-static bool in_tiles(const StateSeqs &q) { return q.rows / q.nseq >= (q.q_start ? 32 : 80); }
+// Rows brought to length 1 and steps in 0..1 keep what a tile's inverse holds in
+// fp16's range: others go row by row.
+static bool in_tiles(const StateSeqs &q, bool norm, bool raw) { return norm && raw && q.rows / q.nseq >= (q.q_start ? 32 : 80); }
 
-int64_t delta_workspace(const StateSeqs &q, const DeltaState &d) { return in_tiles(q) ? delta_chunk_workspace(q, d) : 0; }
+int64_t delta_workspace(const StateSeqs &q, const DeltaState &d, bool norm, bool raw) {
+    return in_tiles(q, norm, raw) ? delta_chunk_workspace(q, d) : 0;
+}
 
 hipError_t launch_delta(const StateSeqs &q, const DeltaState &d, const DeltaIn &in, const Heads &out, void *workspace,
                         hipStream_t st) {
     using namespace delta;
     const Args a = make_args(q, d, in, out);
-    // (of rows brought to length 1 with steps in 0..1, which keep what a tile's inverse holds in fp16's range)
-    if (in_tiles(q) && in.norm && in.A) return launch_delta_chunk(a, d.hk, d.dk, workspace, st);
+    if (in_tiles(q, in.norm, in.A)) return launch_delta_chunk(a, d.hk, d.dk, workspace, st);
     // A lane's columns: more as soon as that leaves 2 blocks a CU, since what is made ready a row then
     // serves more of them; 4 of many rows, whose chain more waves hide, from 4 blocks on.  1 / 2 / 4
     // columns, 48 heads of 128 x 128: 2 sequences of 1 token 6.1 / 6.0 / 6.2 us, 3 8.5 / 6.8 / 7.1,

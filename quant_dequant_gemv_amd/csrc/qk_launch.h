@@ -174,7 +174,8 @@ struct DeltaIn {
     int norm;
     float eps, scale;
 };
-int64_t delta_workspace(const StateSeqs &q, const DeltaState &d);
+// What a call that goes in tiles takes, 0 for row by row; `norm` and `raw` (gates): of rows as they may be.
+int64_t delta_workspace(const StateSeqs &q, const DeltaState &d, bool norm, bool raw);
 // out.p may be NULL (the state alone).
 hipError_t launch_delta(const StateSeqs &q, const DeltaState &d, const DeltaIn &in, const Heads &out, void *workspace,
                         hipStream_t stream);
