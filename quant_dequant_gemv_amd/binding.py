@@ -1047,6 +1047,9 @@ class ConvState:
         self._c = _CONV(_float_arg(pool, "pool", (num_slots, taps - 1, C)), num_slots, C, taps, weight.data_ptr(),
                         _float_arg(bias, "bias", (C,)))
 
+    def __reduce__(self):  # (copies have addresses of their own)
+        return type(self), (self.num_slots, self.weight, self.bias, self.pool)
+
 
 class DeltaState:
     """The state of a gated delta recurrence (qk_delta): pool, a float32 device
@@ -1068,6 +1071,9 @@ class DeltaState:
         self.__dict__["pool"] = pool
         self.num_slots, self.k_heads, self.v_heads, self.key_dim, self.value_dim = num_slots, k_heads, v_heads, key_dim, value_dim
         self._c = _DELTA(_float_arg(pool, "pool", shape), num_slots, k_heads, v_heads, key_dim, value_dim)
+
+    def __reduce__(self):  # (copies have an address of their own)
+        return type(self), (self.num_slots, self.k_heads, self.v_heads, self.key_dim, self.value_dim, self.pool.device, self.pool)
 
 
 def conv_silu(conv: ConvState, x, slots, slots_out=None, q_start=None, kv_len=None, commit=None, act: str = "silu",
