@@ -873,8 +873,7 @@ _PROBS = struct.Struct("PPPPPPii").pack         # qk_probs
 @functools.lru_cache(None)
 def _packed_calls():
     """The library's functions that the helpers below call, taking packed structures."""
-    load_library()
-    lib = ctypes.CDLL(LIB_PATH)
+    lib = ctypes.CDLL(load_library()._name)
     S, P, i64, c_int, f32 = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
     for f, restype, args in ((lib.qk_block_norm, c_int, [S, c_int, c_int, c_int, S, S, S, S, S, P]),
                              (lib.qk_conv_silu, c_int, [S, S, c_int, S, S, P]),
