@@ -117,7 +117,8 @@ __device__ __forceinline__ float gate_of(float z, int act) {
 
 // What brings a row of mean square m to length 1 an element: fp32 (the
 // hardware's root refined once) for the sums of squares that fp32 holds, 1e-25
-// to 1e37, fp64 for the others: no row overflows or vanishes.
+// to 1e37, fp64 for the others: no row overflows or vanishes (with an eps of up to
+// 1e37, above which the kernel of long groups, fp64 throughout, takes all).
 __device__ __forceinline__ bool ordinary(double ss) { return ss >= 1e-25 && ss <= 1e37; }
 __device__ __forceinline__ float root32(double ss, double inv, float eps) {
     const float m = (float)fma(ss, inv, (double)eps), r = rsqrtf(m);
@@ -259,14 +260,16 @@ hipError_t launch_block_norm(const BlockNorm &b, int rows, int groups, int dim, 
     // Threads a group: enough loads at once in each, few waves to meet at the sums (one row of 5120
     // with 8 / 16 values a thread: 4.5 / 4.2 us, 2048 rows 36.4 / 35.1; 2048 rows of 1024: 8.2 / 5.9;
     // 2048 rows of 4096: 32.4 / 21.4, but of 2048 11.5 / 13.6)
-    if (dim <= 64) return go<16, 256, 4>(a, vec, st);
-    if (dim <= 128) return go<16, 256, 8>(a, vec, st);
-    if (dim <= 256) return go<32, 256, 8>(a, vec, st);
-    if (dim <= 512) return go<64, 256, 8>(a, vec, st);
-    if (dim <= 1024) return go<64, 256, 16>(a, vec, st);
-    if (dim <= 2048) return go<256, 256, 8>(a, vec, st);
-    if (dim <= 4096) return go<256, 256, 16>(a, vec, st);
-    if (dim <= 8192) return go<512, 512, 16>(a, vec, st);
+    if (b.eps <= 1e37f) {
+        if (dim <= 64) return go<16, 256, 4>(a, vec, st);
+        if (dim <= 128) return go<16, 256, 8>(a, vec, st);
+        if (dim <= 256) return go<32, 256, 8>(a, vec, st);
+        if (dim <= 512) return go<64, 256, 8>(a, vec, st);
+        if (dim <= 1024) return go<64, 256, 16>(a, vec, st);
+        if (dim <= 2048) return go<256, 256, 8>(a, vec, st);
+        if (dim <= 4096) return go<256, 256, 16>(a, vec, st);
+        if (dim <= 8192) return go<512, 512, 16>(a, vec, st);
+    }
     const unsigned blocks = (unsigned)std::min<int64_t>(a.units, 1 << 20);
     auto wide = [&](auto kern, hipError_t e) {
         if (e != hipSuccess) return e;
