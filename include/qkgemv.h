@@ -656,7 +656,7 @@ typedef struct qk_delta_rows {
     qk_heads alpha, beta;     /* rows x v_heads (elem says nothing)                       */
     const float *A;           /* v_heads values <= 0, or NULL: alpha is the log decay, beta the step */
     const float *dt_bias;     /* v_heads values, or NULL: 0 (NULL without A)              */
-    float eps;                /* >= 0, of the rows' norm                                  */
+    float eps;                /* 0 .. 2^126, of the rows' norm                            */
     float scale;              /* of the outputs; finite                                   */
     int norm;                 /* 1: q / sqrt(sum(q^2) + eps), and k so; 0: as they are    */
 } qk_delta_rows;

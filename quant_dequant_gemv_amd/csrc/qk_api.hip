@@ -618,7 +618,7 @@ int qk_delta_rule(const qk_delta *d, const qk_state_seqs *seqs, const qk_delta_r
     int rc = check_delta(d, seqs);
     if (rc) return rc;
     if (!r) return QK_EINVAL_PTR;
-    if (!(r->eps >= 0.f) || !isfinite(r->eps) || !isfinite(r->scale)) return QK_EINVAL_SHAPE;
+    if (!(r->eps >= 0.f && r->eps <= 0x1p126f) || !isfinite(r->scale)) return QK_EINVAL_SHAPE;  // (a row's sum and eps: below 2^127)
     if (r->norm != 0 && r->norm != 1) return QK_EINVAL_FLAGS;
     const int rows = seqs->rows, hk = d->k_heads, hv = d->v_heads;
     if (rows == 0) return QK_OK;
@@ -703,7 +703,7 @@ const char *qk_strerror(int code) {
                "whose elements do not coincide, at most 2^25 rows x heads and 2^21 sequences x KV heads, |scale| <= 2^64, a window >= 0, a workspace of "
                "qk_kv_attn_workspace_bytes; qk_block_norm 1..4096 groups of 1..32768 and a finite scale; recurrent layers "
                "1..65536 channels, 2..8 taps, key_dim 64 or 128, value_dim a multiple of 32 in 32..512, value heads a "
-               "multiple of the key heads, at most 2^27 sequences x value heads x value_dim, a workspace of "
+               "multiple of the key heads, an eps up to 2^126, at most 2^27 sequences x value heads x value_dim, a workspace of "
                "qk_delta_workspace_bytes; qk_logprobs a vocabulary of 1..2^30, 0..1024 tokens, the top 0..64, "
                "0 < scale <= 2^64, a workspace of qk_logprobs_workspace_bytes";
     case QK_EINVAL_PTR:
