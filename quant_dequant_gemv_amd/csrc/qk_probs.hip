@@ -18,7 +18,7 @@
 namespace qk {
 namespace probs {
 
-// waves of a block where a row's tokens lie side by side (2048 rows of 131071 181 us, 8 waves 212; one row 10.4, 10.8)
+// waves of a block where a row's tokens lie side by side (2048 fp32 rows of 131071 190 us, 8 waves 212; one row 10.4, 10.8)
 constexpr int ROW_WAVES = 4;
 constexpr int WAVES = 8;           // where rows do: two blocks a CU (17 rows of 160000: 11.2 us, one of 16 waves 15.0)
 constexpr int JOIN_WAVES = 8;      // where parts are joined (160 parts of 20: 5.6 us; 4 waves 6.8, 16 waves 6.0)
@@ -404,10 +404,11 @@ template <bool F16> __global__ void __launch_bounds__(64 * ROW_WAVES) probs_row_
         const int head = min(v1, v0 + (int)((16 - ((uintptr_t)(z + v0) & 15)) % 16 / sizeof(T)));
         const int pieces = max(0, (v1 - head) / N), tail = head + pieces * N;
         bool fresh = true;
+        // (scalars beside the lane: 124 registers for 133, 4 waves a SIMD; 2048 fp32 rows of 131071 190 us for 196)
         auto load = [&](int i, Vec *q) {
 #pragma unroll
             for (int j = 0; j < J; ++j)
-                if (i + 64 * j + lane < pieces) q[j] = *reinterpret_cast<const Vec *>(z + head + (i + 64 * j + lane) * N);
+                if (lane < pieces - i - 64 * j) q[j] = *reinterpret_cast<const Vec *>(z + head + (i + 64 * j + lane) * N);
         };
         Vec cur[J], nx[J];
         load(wave * 64 * J, cur);
@@ -418,7 +419,7 @@ template <bool F16> __global__ void __launch_bounds__(64 * ROW_WAVES) probs_row_
             for (int e = 0; e < LANE; ++e) x[e] = (float)cur[e / N][e % N];
             if (i + 64 * J > pieces) {
 #pragma unroll
-                for (int e = 0; e < LANE; ++e) x[e] = i + 64 * (e / N) + lane < pieces ? x[e] : -INFINITY;
+                for (int e = 0; e < LANE; ++e) x[e] = lane < pieces - i - 64 * (e / N) ? x[e] : -INFINITY;
             }
             take<LANE>(x, [&](int e) { return head + (i + 64 * (e / N) + lane) * N + e % N; }, fresh, sums, best, a.scale, p.top, lane,
                        sh.sort[wave]);
