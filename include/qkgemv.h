@@ -568,6 +568,7 @@ typedef struct qk_block {
  * the x of the next GEMV, x_out is {x, 1, 0, ncols, 1}, dim x ncols fp16.
  *
  *   rows      0 .. 2^22     groups  1 .. 4096     dim  1 .. 32768
+ *             rows x groups is at most 2^25
  *   y         rows x groups x dim, as is each of the others
  *   gate, residual   may be NULL
  *   h_out, x_out     either may be NULL
@@ -673,7 +674,7 @@ typedef struct qk_delta_rows {
  *
  *   out    rows x v_heads x value_dim, overlapping nothing that the call reads or
  *          writes; or NULL: the state alone
- *   nseq x v_heads x value_dim is at most 2^27
+ *   rows x v_heads is at most 2^25, nseq x v_heads x value_dim 2^27
  *   workspace  qk_delta_workspace_bytes bytes (16-byte aligned; NULL when that is
  *          0, and with norm 0 or without A), for this call until it has run: calls
  *          that may overlap, captured ones among them, need workspaces of their own

@@ -190,7 +190,8 @@ template <int TPG, int THREADS, int E, bool VEC> __global__ void __launch_bounds
 }
 
 // Groups too long for registers: the row's values wait in LDS between the
-// sums, one group a block.
+// sums, one group a block.  2048 rows of 16384 with a residual (470 MB): 118 us,
+// 4.0 TB/s, its waves waiting 80% of their time; one row 9.7 us, four round trips.
 template <bool VEC> __global__ void __launch_bounds__(1024) block_norm_wide_kernel(Args a) {
     constexpr int T = 1024, E = VEC ? 4 : 1;
     extern __shared__ float row[];

@@ -31,8 +31,9 @@ template <int P> __device__ __forceinline__ float to_length_1(float (*x)[4], flo
 // so that only one sum over lanes lies between a state and the next one.  What
 // does not depend on the state -- normed queries and keys, k.q, gates -- is
 // made ready for R rows at once, a row to 16 lanes, and waits in LDS.
-// One token of 48 heads of 128 x 128 (6.4 MB of state read and written) is 5 us,
-// latency; 64 sequences (407 MB) 82-87 us, 4.7-4.9 TB/s: memory.  Of many rows
+// One token of 48 heads of 128 x 128 (6.4 MB of state read and written) is 5.6 us,
+// latency; 64 sequences (407 MB) 85-88 us, 4.6-4.8 TB/s: memory (70 in place: the
+// states stay in the Infinity Cache).  Of many rows
 // each takes 0.35 us, the chain from state to state.
 template <int DK, int CPL> __global__ void __launch_bounds__(THREADS) delta_rows_kernel(Args a) {
     constexpr int P = DK / 64;                 // pieces of 4 dimensions a lane has
@@ -201,7 +202,9 @@ template <int DK, int CPL> hipError_t go(const Args &a, int nseq, hipStream_t st
 // heads of 128 x 128, in a graph; rows / tiles: 1 sequence of 64 rows 25 / 34 us, of
 // 128 47 / 37, of 256 91 / 44; 8 of 64 95 / 74; 32 of 64 248 / 270, of 128 479 /
 // 383).  Where lengths differ they may be all in one sequence, which takes
-// 0.35 us a row one by one, while tiles lose less than half at 32 rows each.
+// 0.35 us a row one by one, while tiles lose less than half at 32 rows each.  (The
+// count of sequences and heads says more than rows do: 8 of 64 rows lose by this
+// rule, as does one long sequence among many of few rows.)
 // Rows brought to length 1 and steps in 0..1 keep what a tile's inverse holds in
 // fp16's range: others go row by row.
 static bool in_tiles(const StateSeqs &q, bool norm, bool raw) { return norm && raw && q.rows / q.nseq >= (q.q_start ? 32 : 80); }
@@ -217,9 +220,9 @@ hipError_t launch_delta(const StateSeqs &q, const DeltaState &d, const DeltaIn &
     if (in_tiles(q, in.norm, in.A)) return launch_delta_chunk(a, d.hk, d.dk, workspace, st);
     // A lane's columns: more as soon as that leaves 2 blocks a CU, since what is made ready a row then
     // serves more of them; 4 of many rows, whose chain more waves hide, from 4 blocks on.  1 / 2 / 4
-    // columns, 48 heads of 128 x 128: 2 sequences of 1 token 6.1 / 6.0 / 6.2 us, 3 8.5 / 6.8 / 7.1,
-    // 8 14.6 / 11.0 / 9.3, 64 84 / - / 70; 2 of 17 rows 12.6 / 13.6 / 15.9, 3 18.2 / 16.5 / 19.8,
-    // 12 46.7 / 39.1 / 41.9, 16 64.7 / 51.4 / 50.6.
+    // columns, 48 heads of 128 x 128, in place: 2 sequences of 1 token 6.1 / 6.0 / 6.2 us, 3 8.5 / 6.8 / 7.1,
+    // 8 14.6 / 11.0 / 9.3, 64 84 / 70 / 70 (from other slots 105 / 84 / 85); 2 of 17 rows 12.6 / 13.6 / 15.9,
+    // 3 18.2 / 16.5 / 19.8, 12 46.7 / 39.1 / 41.9, 16 64.7 / 51.4 / 50.6.
     const int64_t columns = (int64_t)q.nseq * d.hv * d.dv, many = q.rows > 8 * (int64_t)q.nseq ? 4 : 2;
     const int cpl = d.dv % 64 == 0 && columns >= 64 * many * device_cus() ? 4 : columns >= 32 * 2 * device_cus() ? 2 : 1;
     if (d.dk == 64) return cpl == 4 ? go<64, 4>(a, q.nseq, st) : cpl == 2 ? go<64, 2>(a, q.nseq, st) : go<64, 1>(a, q.nseq, st);

@@ -5,7 +5,7 @@
 // (z - m) scale log2 e; lse = m scale + ln s, entropy = ln 2 (log2 s - w / s).
 // 1021 fp16 rows of 131071 (268 MB): 63-66 us, 4.1-4.2 TB/s, vector
 // instructions (about 6 a logit, 70% of the issue slots) beside the loads; one
-// row of 160000: 6.0 + 5.6 us, two launches whose waves sort once each.
+// row of 160000: 6.0 + 5.8 us, two launches whose waves sort once each.
 #include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -20,8 +20,8 @@ namespace probs {
 
 // waves of a block where a row's tokens lie side by side (2048 fp32 rows of 131071 190 us, 8 waves 212; one row 10.4, 10.8)
 constexpr int ROW_WAVES = 4;
-constexpr int WAVES = 8;           // where rows do: two blocks a CU (17 rows of 160000: 11.2 us, one of 16 waves 15.0)
-constexpr int JOIN_WAVES = 8;      // where parts are joined (160 parts of 20: 5.6 us; 4 waves 6.8, 16 waves 6.0)
+constexpr int WAVES = 8;           // where rows do: two blocks a CU (17 rows of 160000: 11.6 us, one of 16 waves 15.0)
+constexpr int JOIN_WAVES = 8;      // where parts are joined (160 parts of 20: 5.8 us; 4 waves 6.8, 16 waves 6.0)
 constexpr int LANE = 16;           // tokens a lane has at a time
 constexpr int STEP = 64 * LANE;    // and a wave
 constexpr int FEW = WAVES;         // rows that lie side by side (elem > 1) a block has at most, a wave a row or more
